@@ -30,6 +30,8 @@ POOL_BLOCK = 8
 POOL_BLOCKS = 2048
 CAP_ALIGN = 128
 MAX_TOPK = 4096
+MIN_PAGE = 16
+MAX_ROPE_DIM = 128
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "misaligned",
           -4: "CUDA error", -5: "device wait timed out", -6: "workspace", -7: "device rejected input",
@@ -93,6 +95,16 @@ def _load():
                                                     vp, vp, sz, vp]),
         "csa2_sparse_attn_prefill_replay": (ctypes.c_int, [vp, i32, vp, vp, i64, vp, i32, vp, i32, i32, f32, vp,
                                                            vp, vp, vp, sz, vp]),
+        "csa2_rope": (ctypes.c_int, [vp, i64, i32, i32, vp, i64, i32, vp, i32, i32, vp, vp]),
+        "csa2_paged_kv_append": (ctypes.c_int, [vp, vp, i32, vp, i32, vp, i64, i32, vp, i32, vp, vp, vp, vp, i64, i32,
+                                                vp, i32, vp, vp, vp]),
+        "csa2_paged_index_score": (ctypes.c_int, [vp, vp, vp, i32, vp, vp, i64, i32, vp, i32, vp, i64, vp, vp, vp]),
+        "csa2_paged_sparse_attn_workspace_size": (sz, [i32, i32, i32, i32]),
+        "csa2_paged_sparse_attn_decode": (ctypes.c_int, [vp, i32, i32, vp, vp, i64, i32, vp, i32, vp, vp, i32, vp, i32,
+                                                         f32, vp, vp, vp, vp, sz, vp]),
+        "csa2_paged_attn_workspace_size": (sz, [i32, i32]),
+        "csa2_paged_attn": (ctypes.c_int, [vp, i32, vp, i32, vp, vp, i64, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp,
+                                           sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -443,6 +455,156 @@ def csa2_sparse_attn_prefill_replay(q, kv_data, kv_scale, idx, swa, n_swa, repla
           _s(stream))
 
 
+# ---- the cache in pages ---------------------------------------------------------
+# Planes are [n_pages, page_size, width]; entry e of sequence b is row
+# e % page_size of page page_table[b, e // page_size].
+
+def _shape(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(first, *others):
+    """Every tensor of a call lives on the first one's device, and that is the
+    current device (the kernels are launched there)."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+
+
+def _pool(planes, widths, page_table, n_visible):
+    """(n_pages, page_size, B, max_pages) of the pool's planes and the table."""
+    first = planes[0]
+    for t, (width, name) in zip(planes, widths):
+        _req(t, torch.uint8, name)
+        _shape(t.dim() == 3 and t.shape[2] == width and t.shape[:2] == first.shape[:2],
+               f"{name} must be [n_pages, page_size, {width}] like the other planes")
+    _req(page_table, torch.int32, "page_table")
+    _req(n_visible, torch.int32, "n_visible")
+    _shape(page_table.dim() == 2 and n_visible.shape == page_table.shape[:1],
+           "page_table must be [B, max_pages] and n_visible [B]")
+    return first.shape[0], first.shape[1], page_table.shape[0], page_table.shape[1]
+
+
+def _runs(cu, B, name):
+    if cu is not None:
+        _req(cu, torch.int32, name)
+        _shape(cu.shape == (B + 1,), f"{name} must be [B + 1]")
+
+
+def _rope_table(rope):
+    _req(rope, torch.float32, "rope")
+    _shape(rope.dim() == 3 and rope.shape[2] == 2, "rope must be [n_rope, rope_dim / 2, 2]")
+    return rope.shape[0], 2 * rope.shape[1]
+
+
+def csa2_rope(x, rope, positions, out, interleaved=False, inverse=False, stream=None):
+    """x [n_tokens, heads, dim] bf16 -> out (may be x): the last rope_dim
+    channels turned by rope [n_rope, rope_dim / 2, 2] fp32 (cos, sin) at
+    positions [n_tokens] int32 (None: row t is at position t)."""
+    _req(x, torch.bfloat16, "x"); _req(out, torch.bfloat16, "out")
+    _req(positions, torch.int32, "positions", allow_none=True)
+    _shape(x.dim() == 3 and out.shape == x.shape, "x must be [n_tokens, heads, dim], out like it")
+    n_rope, rope_dim = _rope_table(rope)
+    n, heads, dim = x.shape
+    _shape(positions is None or positions.shape == (n,), "positions must be [n_tokens]")
+    _same_device(x, rope, positions, out)
+    _call("csa2_rope", _p(x), n, heads, dim, _p(rope), n_rope, rope_dim, _p(positions), int(bool(interleaved)),
+          int(bool(inverse)), _p(out), _s(stream))
+
+
+def csa2_paged_kv_append(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_table, n_visible, n_visible_out=None,
+                         cu_tokens=None, rope=None, positions=None, interleaved=False, stream=None):
+    """kv [n_tokens, 512], ik [n_tokens, 128] bf16 (before their rotation when a
+    rope table is given) -> entries n_visible[b], n_visible[b] + 1, ... of each
+    sequence; cu_tokens [B + 1] int32 gives each sequence its rows (None: the
+    same number each); n_visible_out may be n_visible."""
+    _req(kv, torch.bfloat16, "kv"); _req(ik, torch.bfloat16, "ik")
+    _shape(kv.dim() == 2 and kv.shape[1] == HEAD_DIM and ik.shape == (kv.shape[0], IDX_DIM),
+           "kv must be [n_tokens, 512] and ik [n_tokens, 128]")
+    n_pages, page, B, max_pages = _pool((kv_data, kv_scale, ik_data, ik_scale),
+                                        ((256, "kv_data"), (32, "kv_scale"), (64, "ik_data"), (4, "ik_scale")),
+                                        page_table, n_visible)
+    _req(n_visible_out, torch.int32, "n_visible_out", allow_none=True)
+    _shape(n_visible_out is None or n_visible_out.shape == (B,), "n_visible_out must be [B]")
+    _runs(cu_tokens, B, "cu_tokens")
+    n_rope = rope_dim = 0
+    if rope is not None:
+        n_rope, rope_dim = _rope_table(rope)
+    _req(positions, torch.int32, "positions", allow_none=True)
+    _shape(positions is None or positions.shape == kv.shape[:1], "positions must be [n_tokens]")
+    _same_device(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_table, n_visible, n_visible_out, cu_tokens, rope,
+                 positions)
+    _call("csa2_paged_kv_append", _p(kv), _p(ik), kv.shape[0], _p(cu_tokens), B, _p(rope), n_rope, rope_dim,
+          _p(positions), int(bool(interleaved)), _p(kv_data), _p(kv_scale), _p(ik_data), _p(ik_scale), n_pages, page,
+          _p(page_table), max_pages, _p(n_visible), _p(n_visible_out), _s(stream))
+
+
+def csa2_paged_index_score(q_data, q_e8m0, w, ik_data, ik_scale, page_table, n_visible, scores, tile_counters=None,
+                           stream=None):
+    """q_data [B, 32, 64], q_e8m0 [B, 32, 4], w [B, 32]; scores [B, n_pos] fp32
+    (out); tile_counters [2 * B] int32 as in csa2_index_score_claimed (None: a
+    fixed range of tiles per CTA)."""
+    _req(q_data, torch.uint8, "q_data"); _req(q_e8m0, torch.uint8, "q_e8m0"); _req(w, torch.float32, "w")
+    _req(scores, torch.float32, "scores"); _req(tile_counters, torch.int32, "tile_counters", allow_none=True)
+    n_pages, page, B, max_pages = _pool((ik_data, ik_scale), ((64, "ik_data"), (4, "ik_scale")), page_table, n_visible)
+    _shape(q_data.numel() == B * IDX_HEADS * 64 and q_e8m0.numel() == B * IDX_HEADS * 4
+           and w.numel() == B * IDX_HEADS, "q_data, q_e8m0 and w must hold B x 32 heads")
+    _shape(scores.dim() == 2 and scores.shape[0] == B, "scores must be [B, n_pos]")
+    _shape(tile_counters is None or tile_counters.numel() >= 2 * B, "tile_counters needs 2 * B int32")
+    _same_device(q_data, q_e8m0, w, ik_data, ik_scale, page_table, n_visible, scores, tile_counters)
+    _call("csa2_paged_index_score", _p(q_data), _p(q_e8m0), _p(w), B, _p(ik_data), _p(ik_scale), n_pages, page,
+          _p(page_table), max_pages, _p(n_visible), scores.shape[1], _p(scores), _p(tile_counters), _s(stream))
+
+
+def csa2_paged_sparse_attn_decode(q, kv_data, kv_scale, page_table, n_visible, idx, swa, out, workspace, out_f32=None,
+                                  lse=None, sm_scale=1.0, stream=None):
+    """As csa2_sparse_attn_decode, idx [B, k] naming entries of the paged
+    sequences; q [B, L, 64, 512] bf16, swa [B, L, n_swa, 512] u8 or None."""
+    _req(q, torch.bfloat16, "q"); _req(idx, torch.int32, "idx"); _req(out, torch.bfloat16, "out")
+    _req(workspace, torch.uint8, "workspace"); _req(swa, torch.uint8, "swa", allow_none=True)
+    _req(out_f32, torch.float32, "out_f32", allow_none=True); _req(lse, torch.float32, "lse", allow_none=True)
+    n_pages, page, B, max_pages = _pool((kv_data, kv_scale), ((256, "kv_data"), (32, "kv_scale")), page_table,
+                                        n_visible)
+    _shape(q.dim() == 4 and q.shape[0] == B and q.shape[2:] == (HEADS, HEAD_DIM), "q must be [B, L, 64, 512]")
+    L = q.shape[1]
+    _shape(idx.dim() == 2 and idx.shape[0] == B, "idx must be [B, k]")
+    _shape(swa is None or (swa.dim() == 4 and swa.shape[:2] == (B, L) and swa.shape[3] == HEAD_DIM),
+           "swa must be [B, L, n_swa, 512]")
+    _outputs(q, out, out_f32, lse)
+    _same_device(q, kv_data, kv_scale, page_table, n_visible, idx, swa, out, workspace, out_f32, lse)
+    n_swa = swa.shape[2] if swa is not None else 0
+    _call("csa2_paged_sparse_attn_decode", _p(q), B, L, _p(kv_data), _p(kv_scale), n_pages, page, _p(page_table),
+          max_pages, _p(n_visible), _p(idx), idx.shape[1], _p(swa), n_swa, float(sm_scale), _p(out), _p(out_f32),
+          _p(lse), _p(workspace), workspace.numel(), _s(stream))
+
+
+def _outputs(q, out, out_f32, lse):
+    _shape(out.shape == q.shape and (out_f32 is None or out_f32.shape == q.shape)
+           and (lse is None or lse.shape == q.shape[:-1]), "out and out_f32 must be like q, lse without its last axis")
+
+
+def csa2_paged_attn(q, kv_data, kv_scale, page_table, n_visible, out, workspace, cu_q=None, causal=True, out_f32=None,
+                    lse=None, sm_scale=1.0, stream=None):
+    """Dense attention of q [n_tokens, 64, 512] bf16 over every entry a token
+    sees; cu_q [B + 1] int32 gives each sequence its rows (None: the same number
+    each); out_f32 [n_tokens, 64, 512] and lse [n_tokens, 64] are optional."""
+    _req(q, torch.bfloat16, "q"); _req(out, torch.bfloat16, "out"); _req(workspace, torch.uint8, "workspace")
+    _req(out_f32, torch.float32, "out_f32", allow_none=True); _req(lse, torch.float32, "lse", allow_none=True)
+    n_pages, page, B, max_pages = _pool((kv_data, kv_scale), ((256, "kv_data"), (32, "kv_scale")), page_table,
+                                        n_visible)
+    _shape(q.dim() == 3 and q.shape[1:] == (HEADS, HEAD_DIM), "q must be [n_tokens, 64, 512]")
+    _outputs(q, out, out_f32, lse)
+    _runs(cu_q, B, "cu_q")
+    _same_device(q, kv_data, kv_scale, page_table, n_visible, out, workspace, cu_q, out_f32, lse)
+    _call("csa2_paged_attn", _p(q), q.shape[0], _p(cu_q), B, _p(kv_data), _p(kv_scale), n_pages, page, _p(page_table),
+          max_pages, _p(n_visible), int(bool(causal)), float(sm_scale), _p(out), _p(out_f32), _p(lse), _p(workspace),
+          workspace.numel(), _s(stream))
+
+
 # ---- allocating helpers (torch memory plumbing + the entry points above) --------
 
 def _ws(nbytes, device):
@@ -488,3 +650,11 @@ def merge_workspace(R, B, k, k_out, device="cuda"):
 
 def attn_workspace(n_queries, k, n_swa, device="cuda"):
     return _ws(_lib.csa2_sparse_attn_workspace_size(n_queries, k, n_swa), device)
+
+
+def paged_attn_workspace(n_tokens, B, device="cuda"):
+    return _ws(_lib.csa2_paged_attn_workspace_size(n_tokens, B), device)
+
+
+def paged_sparse_attn_workspace(B, L, k, n_swa, device="cuda"):
+    return _ws(_lib.csa2_paged_sparse_attn_workspace_size(B, L, k, n_swa), device)

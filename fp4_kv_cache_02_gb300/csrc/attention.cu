@@ -16,7 +16,7 @@
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
-#include "common.cuh"
+#include "paged_common.cuh"
 
 namespace csa2 {
 
@@ -353,4 +353,57 @@ extern "C" int csa2_sparse_attn_prefill(const void* q_bf16, int32_t T, const uin
                                         csa2_stream_t stream) {
   return csa2_sparse_attn_prefill_replay(q_bf16, T, kv_data, kv_scale, n_entries, idx, k, swa, n_swa, 0, sm_scale,
                                          out_bf16, out_f32, lse, workspace, workspace_bytes, stream);
+}
+
+// ---- over pages: the selected entries become rows of the pool (one small
+// launch), and the pool is one shared plane to the kernel ----
+int csa2_launch_page_rows(const int32_t* idx, int32_t B, int32_t k, const int32_t* n_visible, const PageTable& pages,
+                          int32_t* rows, cudaStream_t s);
+
+extern "C" size_t csa2_paged_sparse_attn_workspace_size(int32_t B, int32_t L, int32_t k, int32_t n_swa) {
+  if (B <= 0 || L <= 0 || k < 0 || n_swa < 0 || (int64_t)B * L > 0x7FFFFFFFLL) return 0;
+  return csa2_sparse_attn_workspace_size(B * L, k, n_swa) + ((size_t)B * (size_t)k * 4 + 255) / 256 * 256;
+}
+
+extern "C" int csa2_paged_sparse_attn_decode(const void* q_bf16, int32_t B, int32_t L, const uint8_t* kv_data,
+                                             const uint8_t* kv_scale, int64_t n_pages, int32_t page_size,
+                                             const int32_t* page_table, int32_t max_pages, const int32_t* n_visible,
+                                             const int32_t* idx, int32_t k, const uint8_t* swa, int32_t n_swa,
+                                             float sm_scale, void* out_bf16, float* out_f32, float* lse,
+                                             void* workspace, size_t workspace_bytes, csa2_stream_t stream) {
+  if (B != 0 && (!q_bf16 || !kv_data || !kv_scale || !n_visible || (!idx && k > 0) || !out_bf16))
+    return CSA2_ERR_INVALID_ARG;
+  PageTable pages;
+  if (int rc = paged_check(page_table, n_pages, page_size, max_pages, B, pages)) return rc;
+  if (L < 1 || k < 0 || n_swa < 0) return CSA2_ERR_INVALID_ARG;
+  if (n_swa > 0 && !swa) return CSA2_ERR_INVALID_ARG;
+  if (k > CSA2_MAX_TOPK || n_swa > 512 || (int64_t)B * L > 0x7FFFFFFFLL) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (!csa2_aligned(q_bf16, 16) || !csa2_aligned(kv_data, 16) || !csa2_aligned(kv_scale, 16) ||
+      !csa2_aligned(out_bf16, 8) || (swa && !csa2_aligned(swa, 16)) || (out_f32 && !csa2_aligned(out_f32, 16)) ||
+      !csa2_aligned(idx, 4) || !csa2_aligned(n_visible, 4) || !csa2_aligned(lse, 4))
+    return CSA2_ERR_ALIGNMENT;
+  if (B == 0) return CSA2_OK;
+  const size_t attn_bytes = csa2_sparse_attn_workspace_size(B * L, k, n_swa);
+  if (!workspace || !csa2_aligned(workspace, 256) ||
+      workspace_bytes < csa2_paged_sparse_attn_workspace_size(B, L, k, n_swa))
+    return CSA2_ERR_WORKSPACE;
+  int32_t* rows = (int32_t*)((uint8_t*)workspace + attn_bytes);
+  if (int rc = csa2_launch_page_rows(idx, B, k, n_visible, pages, rows, (cudaStream_t)stream)) return rc;
+  AttnArgs a{};
+  a.kv_data = kv_data;
+  a.kv_scale = kv_scale;
+  a.kv_seq_stride = 0;
+  a.n_visible = nullptr;
+  a.nv_const = n_pages << pages.shift;
+  a.idx = rows;
+  a.k = k;
+  a.L = L;
+  a.lgrp = 1;
+  a.swa = swa;
+  a.swa_q_stride = (int64_t)n_swa * kHeadDim;
+  a.n_swa = n_swa;
+  a.swa_first_row = INT32_MIN;
+  a.sm_scale = sm_scale;
+  return launch_attn(a, q_bf16, B * L, (uint16_t*)out_bf16, out_f32, lse, workspace, attn_bytes,
+                     (cudaStream_t)stream);
 }

@@ -45,7 +45,8 @@ extern "C" int csa2_get_last_error(csa2_stream_t stream, int* device_status) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return CSA2_ERR_CUDA;
   int first = CSA2_OK;
   int (*readers[])(cudaStream_t) = {csa2_read_and_clear_codec_error, csa2_read_and_clear_index_error,
-                                    csa2_read_and_clear_topk_error, csa2_read_and_clear_attn_error};
+                                    csa2_read_and_clear_topk_error, csa2_read_and_clear_attn_error,
+                                    csa2_read_and_clear_paged_error, csa2_read_and_clear_paged_attn_error};
   for (auto rd : readers) {
     int v = rd(s);
     if (v == CSA2_ERR_CUDA) return CSA2_ERR_CUDA;

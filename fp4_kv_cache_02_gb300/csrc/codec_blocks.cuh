@@ -56,20 +56,14 @@ __device__ __forceinline__ void encode_mxfp4_block(const uint32_t (&w)[16], uint
   e8m0 = (uint8_t)(X + 127);
 }
 
-// One main-KV block: 16 bf16 values (8 words) -> 8 bytes of E2M1 pairs and
-// the E4M3 scale. The scale is amax / 6 rounded to nearest-even E4M3 (6 is
-// the largest E2M1 magnitude); each value is divided by the decoded scale and
-// rounded to nearest-even E2M1, saturating. A zero scale stores zero codes.
-__device__ __forceinline__ void encode_kv_fp4_block(const uint32_t (&w)[8], uint2& data, uint8_t& scale) {
-  float f[16];
+// One main-KV block: 16 values -> 8 bytes of E2M1 pairs and the E4M3 scale. The
+// scale is amax / 6 rounded to nearest-even E4M3 (6 is the largest E2M1
+// magnitude); each value is divided by the decoded scale and rounded to
+// nearest-even E2M1, saturating. A zero scale stores zero codes.
+__device__ __forceinline__ void encode_kv_fp4_values(const float (&f)[16], uint2& data, uint8_t& scale) {
   float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-    f[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
-    amax = fmaxf(amax, fabsf(f[2 * i]));
-    amax = fmaxf(amax, fabsf(f[2 * i + 1]));
-  }
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
   const float q = __fdiv_rn(amax, 6.0f);
   const uint32_t sc = cvt_e4m3x2(q, 0.0f) & 0xFFu;
   const float s = e4m3_to_f32(sc);
@@ -83,6 +77,17 @@ __device__ __forceinline__ void encode_kv_fp4_block(const uint32_t (&w)[8], uint
   }
   data = make_uint2(out0, out1);
   scale = (uint8_t)sc;
+}
+
+// The same from 16 bf16 values (8 words of pairs, element 2i in the low half).
+__device__ __forceinline__ void encode_kv_fp4_block(const uint32_t (&w)[8], uint2& data, uint8_t& scale) {
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
+    f[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
+  }
+  encode_kv_fp4_values(f, data, scale);
 }
 
 }  // namespace csa2

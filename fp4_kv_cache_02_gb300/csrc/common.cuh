@@ -202,3 +202,5 @@ int csa2_read_and_clear_codec_error(cudaStream_t s);
 int csa2_read_and_clear_index_error(cudaStream_t s);
 int csa2_read_and_clear_topk_error(cudaStream_t s);
 int csa2_read_and_clear_attn_error(cudaStream_t s);
+int csa2_read_and_clear_paged_error(cudaStream_t s);
+int csa2_read_and_clear_paged_attn_error(cudaStream_t s);

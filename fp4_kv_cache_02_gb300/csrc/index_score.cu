@@ -93,16 +93,66 @@ int csa2_launch_index_score_tc(const uint8_t* q_data, const uint8_t* q_e8m0, con
   const int64_t per = (tiles + chunks - 1) / chunks;
   chunks = (tiles + per - 1) / per;
   static Csa2PerDeviceOnce optin;
-  if (csa2_smem_optin((const void*)scan_tc::index_score_tc_kernel, scan_tc::kSmemBytes, optin) != CSA2_OK)
+  if (csa2_smem_optin((const void*)scan_tc::index_score_tc_kernel<false>, scan_tc::kSmemBytes, optin) != CSA2_OK)
     return CSA2_ERR_CUDA;
   // claimed tiles (dense mode with counters): a fixed first range of one
   // pipeline's depth, then claims of two tiles
   scan_tc::Params prm{ik_data, positions, q_data, q_e8m0, w, ik_scale, cap, n_visible, n_pos, scores, (int32_t)per,
                       hist, positions ? nullptr : bmax, early_reads, (const uint16_t*)q_bf16,
                       positions ? nullptr : tile_ctr, tile_ctr_stride, scan_tc::kStages, 2,
-                      positions ? nullptr : tile_done};
-  CSA2_LAUNCH_PDL(scan_tc::index_score_tc_kernel, dim3((unsigned)B, (unsigned)chunks), dim3(scan_tc::kThreads),
+                      positions ? nullptr : tile_done, PageTable{}};
+  CSA2_LAUNCH_PDL(scan_tc::index_score_tc_kernel<false>, dim3((unsigned)B, (unsigned)chunks), dim3(scan_tc::kThreads),
                   (size_t)scan_tc::kSmemBytes, stream, map, prm);
+  return CSA2_OK;
+}
+
+// The dense scan over pages. The pool is one plane to the tensor map; a box is
+// one run of a tile: the whole tile, or a page where pages are smaller.
+extern "C" int csa2_paged_index_score(const uint8_t* q_data, const uint8_t* q_e8m0, const float* w, int32_t B,
+                                      const uint8_t* ik_data, const uint8_t* ik_scale, int64_t n_pages,
+                                      int32_t page_size, const int32_t* page_table, int32_t max_pages,
+                                      const int32_t* n_visible, int64_t n_pos, float* scores, int32_t* tile_counters,
+                                      csa2_stream_t stream) {
+  if (n_pos < 0) return CSA2_ERR_INVALID_ARG;
+  if (n_pos > 0 && B != 0 && (!q_data || !q_e8m0 || !w || !ik_data || !ik_scale || !n_visible || !scores))
+    return CSA2_ERR_INVALID_ARG;
+  PageTable pages;
+  if (int rc = paged_check(page_table, n_pages, page_size, max_pages, B, pages)) return rc;
+  if (n_pos > pages.capacity()) return CSA2_ERR_INVALID_ARG;
+  if (!csa2_aligned(ik_data, 16) || !csa2_aligned(ik_scale, 16) || !csa2_aligned(q_data, 16) ||
+      !csa2_aligned(q_e8m0, 4) || !csa2_aligned(w, 4) || !csa2_aligned(n_visible, 4) || !csa2_aligned(scores, 4) ||
+      (tile_counters && !csa2_aligned(tile_counters, 8)))
+    return CSA2_ERR_ALIGNMENT;
+  if (n_pos == 0 || B == 0) return CSA2_OK;
+  auto encode = tensor_map_encoder();
+  if (!encode) return CSA2_ERR_CUDA;
+  const int64_t pool = n_pages << pages.shift;
+  const int run = page_size < scan_tc::kTileRows ? page_size : scan_tc::kTileRows;
+  CUtensorMap map;
+  // (an empty pool has no page to follow: the map then only has to be valid)
+  cuuint64_t dims[3] = {(cuuint64_t)kIkBytes, (cuuint64_t)(pool > 0 ? pool : 1), 1};
+  cuuint64_t strides[2] = {(cuuint64_t)kIkBytes, (cuuint64_t)(pool > 0 ? pool : 1) * kIkBytes};
+  cuuint32_t box[3] = {(cuuint32_t)kIkBytes, (cuuint32_t)run, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void*)ik_data, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return CSA2_ERR_CUDA;
+  const int64_t tiles = (n_pos + scan_tc::kTileRows - 1) / scan_tc::kTileRows;
+  int64_t chunks = 3LL * device_sm_count() / B;
+  if (chunks < 1) chunks = 1;
+  if (chunks > tiles) chunks = tiles;
+  const int64_t per = (tiles + chunks - 1) / chunks;
+  chunks = (tiles + per - 1) / per;
+  if (chunks > 65535) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  static Csa2PerDeviceOnce optin;
+  if (csa2_smem_optin((const void*)scan_tc::index_score_tc_kernel<true>, scan_tc::kSmemBytes, optin) != CSA2_OK)
+    return CSA2_ERR_CUDA;
+  scan_tc::Params prm{ik_data, nullptr, q_data, q_e8m0, w, ik_scale, pages.capacity(), n_visible, n_pos, scores,
+                      (int32_t)per, nullptr, nullptr, 0, nullptr, tile_counters, 2, scan_tc::kStages, 2,
+                      tile_counters ? tile_counters + 1 : nullptr, pages};
+  CSA2_LAUNCH_PDL(scan_tc::index_score_tc_kernel<true>, dim3((unsigned)B, (unsigned)chunks), dim3(scan_tc::kThreads),
+                  (size_t)scan_tc::kSmemBytes, (cudaStream_t)stream, map, prm);
   return CSA2_OK;
 }
 

@@ -26,6 +26,7 @@
 #include <cudaTypedefs.h>
 
 #include "codec_blocks.cuh"
+#include "paged_common.cuh"
 #include "tc_common.cuh"
 
 namespace csa2 {
@@ -55,7 +56,8 @@ constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kOffHist = kOffMisc + 16;               // Top-K histogram of this CTA's scores
 constexpr int kRing = 16;                             // tile index of each tile in flight (claimed mode)
 constexpr int kOffRing = kOffHist + kTopkHistBins * 4;
-constexpr int kSmemBytes = kOffRing + kRing * 4 + 1024;  // + alignment slack
+constexpr int kOffMask = kOffRing + kRing * 4;        // paged: which of the tile's pages were there
+constexpr int kSmemBytes = kOffMask + kRing * 4 + 1024;  // + alignment slack
 static_assert(kOffQ % 1024 == 0, "q operand must be 1024-byte aligned");
 
 struct Params {
@@ -91,8 +93,12 @@ struct Params {
   // optional, beside tile_ctr (same stride): CTAs of the sequence that have
   // finished; the last one puts both words back to zero for the next launch
   int32_t* tile_done;
+  // paged mode: ik_data / ik_scale are the pool's planes, entries found by the
+  // table; a tile is one piece of a page, or several whole small pages
+  PageTable pages;
 };
 
+template <bool kPaged>
 __global__ void __launch_bounds__(kThreads, 3)
     index_score_tc_kernel(const __grid_constant__ CUtensorMap tmap_ik, Params p) {
   if (p.early_reads)
@@ -115,8 +121,9 @@ __global__ void __launch_bounds__(kThreads, 3)
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + kOffMisc + 4);
   uint32_t* s_hist = reinterpret_cast<uint32_t*>(sm + kOffHist);
   volatile int32_t* s_ring = reinterpret_cast<volatile int32_t*>(sm + kOffRing);
+  volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(sm + kOffMask);
   const bool with_hist = p.hist != nullptr;
-  const bool pos_mode = p.positions != nullptr;
+  const bool pos_mode = !kPaged && p.positions != nullptr;
   // claimed mode: tiles come from the sequence's counter, their indices pass
   // from the producer to the MMA warp and the epilogue through s_ring; a tile
   // index of -1 ends the stream
@@ -244,6 +251,38 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (!tc::mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, &g_index_error)) return false;
         const int64_t row0 = tile * kTileRows;
         if (claimed) s_ring[i % kRing] = (int32_t)tile;
+        if constexpr (kPaged) {
+          // the tile's entries: one run of a page, or up to 8 whole pages. Pages
+          // past the visible entries are not looked up; what a missing page
+          // leaves in the stage is never scored (s_mask)
+          const int run_shift = p.pages.shift < 7 ? p.pages.shift : 7;
+          const int run = 1 << run_shift;
+          const int n_runs = kTileRows >> run_shift;
+          const int32_t* places = p.pages.table + (int64_t)b * p.pages.max_pages;
+          int32_t page[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            page[j] = j < n_runs && row0 + (int64_t)j * run < nv ? places[(row0 + (int64_t)j * run) >> p.pages.shift]
+                                                                 : INT32_MIN;
+          uint32_t mask = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (page[j] >= 0 && page[j] < p.pages.n_pages) mask |= 1u << j;
+            else if (page[j] != INT32_MIN || (j < n_runs && row0 + (int64_t)j * run < nv))
+              record_error(&g_index_error, CSA2_ERR_DEVICE);
+          }
+          s_mask[i % kRing] = mask;
+          tc::mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(mask) * (uint32_t)run * (kIkBytes + kIkScales));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (!((mask >> j) & 1u)) continue;
+            const int64_t prow = ((int64_t)page[j] << p.pages.shift) + (row0 & (p.pages.page_size() - 1));
+            tc::tma_load_3d(sA + s * kTileBytes + j * run * kIkBytes, &tmap_ik, 0, (int32_t)prow, 0, &full[s]);
+            tc::bulk_load(sSfRaw + s * kSfBytes + j * run * kIkScales, p.ik_scale + prow * kIkScales,
+                          (uint32_t)(run * kIkScales), &full[s]);
+          }
+          return true;
+        }
         tc::mbar_arrive_expect_tx(&full[s], kTileBytes + kSfBytes);
         tc::tma_load_3d(sA + s * kTileBytes, &tmap_ik, 0, (int32_t)row0, b, &full[s]);
         tc::bulk_load(sSfRaw + s * kSfBytes, p.ik_scale + ((int64_t)b * p.cap + row0) * kIkScales, kSfBytes,
@@ -371,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int h = 0; h < kIdxHeads; ++h) sc = fmaf(wr[h], fmaxf(__uint_as_float(r[h]), 0.0f), sc);
       const int64_t li = tile * kTileRows + row;  // list index
       bool valid = li < nv;
+      if (kPaged && !((s_mask[i % kRing] >> (row >> (p.pages.shift < 7 ? p.pages.shift : 7))) & 1u)) valid = false;
       if (pos_mode) {
         const int32_t pp = li < p.n_pos ? p.positions[(int64_t)b * p.n_pos + li] : -1;
         valid = pp >= 0 && pp < nv_pos;

@@ -570,6 +570,168 @@ int csa2_sparse_attn_prefill_replay(const void* q_bf16, int32_t T,
                                     void* workspace, size_t workspace_bytes,
                                     csa2_stream_t stream);
 
+/* ======================================================================== */
+/* The cache in pages                                                        */
+/* ======================================================================== */
+/* Entries of many sequences in one pool of pages. The planes are
+ *     kv_data [n_pages][page_size][256], kv_scale [n_pages][page_size][32],
+ *     ik_data [n_pages][page_size][64],  ik_scale [n_pages][page_size][4],
+ * an entry being laid out as in the planes of the conventions above. Entry e of
+ * sequence b is row e % page_size of page page_table[b][e / page_size].
+ *   - page_size is a power of two, at least CSA2_MIN_PAGE. A pool holds at most
+ *     2^31 - 1 entries. Plane base pointers are 16-byte aligned.
+ *   - page_table [B][max_pages] int32. Only the table's first
+ *     ceil(n / page_size) places of a sequence with n entries are read; the
+ *     others may hold anything. A page outside [0, n_pages) that is needed is
+ *     not followed: the entry point says what happens to its entries, and
+ *     csa2_get_last_error then reports DEVICE. Sequences may share pages that
+ *     are only read.
+ *   - cu [B+1] int32, rising, gives each sequence its run of token rows:
+ *     sequence b has rows cu[b] .. cu[b+1]-1. NULL: n_tokens / B rows each (B
+ *     must divide n_tokens). Rows before cu[0] and from cu[B] on belong to
+ *     no sequence: they are neither read nor written. A sequence whose run is
+ *     not within 0 .. n_tokens is passed over and reported as DEVICE.
+ *   - Position rotation: a row x of d channels at position p has its last
+ *     rope_dim channels turned, pair i by the angle whose cosine and sine are
+ *     rope[p][i][0] and rope[p][i][1] (fp32, [n_rope][rope_dim/2][2],
+ *     16-byte aligned):
+ *         (u, v) -> (u cos - v sin, u sin + v cos).
+ *     Pair i is channels (2i, 2i+1) of the turned part when `interleaved` is
+ *     not 0, else channels (i, i + rope_dim/2). rope_dim is a multiple of 32.
+ *     A turned value is held in fp32, rounded once. */
+
+#define CSA2_MIN_PAGE 16
+#define CSA2_MAX_ROPE_DIM 128
+
+/**
+ * Position rotation of [n_tokens][heads][dim] bf16 rows (queries, indexer
+ * queries, or with `inverse` attention outputs turned back: the latent is key
+ * and value at once, so an output carries its entries' rotation). The turned
+ * channels are rounded to bf16, the others copied. (Report section 2.4.4: the
+ * main-KV latent has RoPE and non-RoPE channels.)
+ *   positions [n_tokens] int32, NULL: row t is at position t. A token whose
+ *   position is not within 0 .. n_rope-1 keeps its output as it was and is
+ *   reported as DEVICE.
+ *   x_bf16, out_bf16 16-byte aligned; out may be x (not overlap it otherwise).
+ *   dim is a multiple of 8, at least rope_dim; rope_dim 32 .. CSA2_MAX_ROPE_DIM.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, CUDA.
+ */
+int csa2_rope(const void* x_bf16, int64_t n_tokens, int32_t heads, int32_t dim,
+              const float* rope, int64_t n_rope, int32_t rope_dim,
+              const int32_t* positions, int32_t interleaved, int32_t inverse,
+              void* out_bf16, csa2_stream_t stream);
+
+/**
+ * KV append into pages: csa2_kv_append for ragged batches, with the position
+ * rotation applied on the way (report section 2.4.4: the latent is quantised
+ * after RoPE, with one format for RoPE and non-RoPE channels). Token t of
+ * sequence b becomes its entry n_visible[b] + t.
+ *   kv_bf16 [n_tokens][512], ik_bf16 [n_tokens][128] (16-byte aligned): the
+ *   last rope_dim channels of each are turned at the token's position, then
+ *   encoded as csa2_pack_kv_fp4 and csa2_quant_mxfp4 encode (from the fp32
+ *   values: no rounding to bf16 in between). rope_dim 0 or rope NULL: rows are
+ *   taken as they are, and the bytes equal csa2_kv_append's.
+ *   positions [n_tokens] int32, NULL: a token's position is its entry's index.
+ *   n_visible [B] int32; n_visible_out [B] int32 (nullable) receives n_visible
+ *   plus the sequence's new tokens; it may be n_visible itself.
+ * A sequence whose tokens do not fit below max_pages * page_size (or whose
+ * count is negative) gets none of them and keeps its count. An entry whose page
+ * is outside the pool or whose position is outside the table is not written
+ * (the count still advances). Both are reported as DEVICE. Pages written by one
+ * call must not be shared between its sequences.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, CUDA.
+ */
+int csa2_paged_kv_append(const void* kv_bf16, const void* ik_bf16,
+                         int32_t n_tokens, const int32_t* cu_tokens, int32_t B,
+                         const float* rope, int64_t n_rope, int32_t rope_dim,
+                         const int32_t* positions, int32_t interleaved,
+                         uint8_t* kv_data, uint8_t* kv_scale, uint8_t* ik_data,
+                         uint8_t* ik_scale, int64_t n_pages, int32_t page_size,
+                         const int32_t* page_table, int32_t max_pages,
+                         const int32_t* n_visible, int32_t* n_visible_out,
+                         csa2_stream_t stream);
+
+/**
+ * csa2_index_score over pages: s[b][i] for entries i = 0 .. n_pos-1 of every
+ * sequence, -inf from n_visible[b] on and for entries of a page outside the
+ * pool (reported as DEVICE). n_pos <= max_pages * page_size.
+ *   tile_counters: NULL, or [2 * B] int32 as in csa2_index_score_claimed (the
+ *   CTAs of a sequence then claim its tiles; all zero before the first call,
+ *   left zero by every call, one buffer per call that may run at the same time).
+ * The scores feed csa2_topk and csa2_block_pool (with n_visible) as usual.
+ * Errors: as csa2_index_score.
+ */
+int csa2_paged_index_score(const uint8_t* q_data, const uint8_t* q_e8m0,
+                           const float* w, int32_t B, const uint8_t* ik_data,
+                           const uint8_t* ik_scale, int64_t n_pages,
+                           int32_t page_size, const int32_t* page_table,
+                           int32_t max_pages, const int32_t* n_visible,
+                           int64_t n_pos, float* scores,
+                           int32_t* tile_counters, csa2_stream_t stream);
+
+/** Bytes of workspace csa2_paged_sparse_attn_decode needs. */
+size_t csa2_paged_sparse_attn_workspace_size(int32_t B, int32_t L, int32_t k,
+                                             int32_t n_swa);
+
+/**
+ * csa2_sparse_attn_decode over pages: idx holds entries of the sequences
+ * (from csa2_topk over csa2_paged_index_score); the results are those of that
+ * call on flat planes of the same entries. An entry >= n_visible[b], or of a
+ * page outside the pool, is skipped and reported as DEVICE.
+ * Errors: as csa2_sparse_attn_decode.
+ */
+int csa2_paged_sparse_attn_decode(const void* q_bf16, int32_t B, int32_t L,
+                                  const uint8_t* kv_data,
+                                  const uint8_t* kv_scale, int64_t n_pages,
+                                  int32_t page_size, const int32_t* page_table,
+                                  int32_t max_pages, const int32_t* n_visible,
+                                  const int32_t* idx, int32_t k,
+                                  const uint8_t* swa, int32_t n_swa,
+                                  float sm_scale, void* out_bf16,
+                                  float* out_f32, float* lse, void* workspace,
+                                  size_t workspace_bytes, csa2_stream_t stream);
+
+/** Bytes of workspace csa2_paged_attn needs on the current device (it depends
+ *  on n_tokens only up to the device's number of SMs). */
+size_t csa2_paged_attn_workspace_size(int32_t n_tokens, int32_t B);
+
+/**
+ * Dense attention over the paged FP4 cache: every query token attends to all
+ * the entries that it sees (report section 2.3 with every entry selected; a
+ * context no longer than the Top-K, or a layer without an index).
+ *   q [n_tokens][64][512] bf16; sequence b's tokens are rows cu_q[b] ..
+ *   cu_q[b+1]-1 (T of them). causal != 0: its token t sees entries
+ *   0 .. n_visible[b] - T + t (the sequence's last T entries are the tokens'
+ *   own; a token before entry 0 sees nothing). causal == 0: every token sees
+ *   entries 0 .. n_visible[b]-1.
+ *   S = sm_scale * q . row over those entries' latents (one latent for all 64
+ *   heads), softmax, out = P . rows.
+ *   out_bf16, out_f32 (nullable), lse (nullable, [n_tokens][64]) as in
+ *   csa2_sparse_attn_decode: a token that sees nothing gets 0 and -inf. To
+ *   join the sliding window, merge with csa2_attn_merge.
+ *   Entries of a page outside the pool are left out of the softmax, a sequence
+ *   whose n_visible is negative or above max_pages * page_size is passed over
+ *   (its rows stay as they were); both are reported as DEVICE.
+ *   q, out_bf16 and out_f32 16-byte aligned. q is finite.
+ *   Precision: as csa2_sparse_attn_decode (rows and q exact in fp16, P in fp16).
+ *   Results do not depend on the schedule but for the last bits: the entries of
+ *   a token may be summed in parts whose bounds follow from the batch and the
+ *   device. The same call gives the same bits.
+ *   workspace: csa2_paged_attn_workspace_size bytes, 256-byte aligned, its
+ *   contents need not be kept; calls that may run at the same time (graphs
+ *   among them) need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA; a
+ * bounded device wait that runs out is reported by csa2_get_last_error as
+ * TIMEOUT.
+ */
+int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32_t* cu_q,
+                    int32_t B, const uint8_t* kv_data, const uint8_t* kv_scale,
+                    int64_t n_pages, int32_t page_size,
+                    const int32_t* page_table, int32_t max_pages,
+                    const int32_t* n_visible, int32_t causal, float sm_scale,
+                    void* out_bf16, float* out_f32, float* lse, void* workspace,
+                    size_t workspace_bytes, csa2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
