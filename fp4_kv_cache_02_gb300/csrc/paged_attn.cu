@@ -25,6 +25,8 @@
 // such a token go to the workspace and a second kernel joins them in order.
 // Few long sequences and many short ones load the SMs alike, and the workspace
 // (two parts per SM) does not grow with the batch.
+#include <cudaTypedefs.h>
+
 #include "attn_common.cuh"
 #include "paged_common.cuh"
 
@@ -43,27 +45,41 @@ using attn_tc::mul_f16x2;
 using attn_tc::named_barrier;
 using attn_tc::warp_transpose_reduce16;
 
-constexpr int kThreads = 512;             // 16 warps: 4 lane quadrants x 4 (a 17th would cap registers at 96)
+// Roles: warps 0 .. 7 take the softmax and the outputs, 8 .. 15 load and
+// dequantise, 16 and 17 issue the products for S^T and for O^T, 18 walks the
+// list and looks pages up, 19 copies the rows into shared memory. A warp's
+// tensor-memory lanes are the quadrant warp % 4; the two warps of a quadrant in a
+// role share its rows by heads (softmax) or channels (dequantisation).
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kSWarp = 16, kOWarp = 17, kWalkWarp = 18, kCopyWarp = 19;
+constexpr int kThreads = 640;
 constexpr int kWarps = kThreads / 32;
+// Registers: 640 threads start with 96 each (61,440 in all).
+constexpr int kRegsSoft = 112, kRegsLoad = 112, kRegsIssue = 32;
+static_assert(256 * kRegsSoft + 256 * kRegsLoad + 128 * kRegsIssue <= kThreads * 96, "register split");
 constexpr int kRows = 128;
-constexpr int kBlkR = kRows * 128;        // one 64-channel block of R: [128 rows][128 B]
-constexpr int kBlkQ = kHeads * 128;       // one 64-channel block of Q: [64 heads][128 B]
+constexpr int kPlaces = 3;                // rings of 128-channel groups of R, in tensor and in shared memory
+constexpr int kBlkR = kRows * 128;        // 64 channels of R: [128 rows][128 B]
+constexpr int kBlkQ = kHeads * 128;       // 64 channels of Q: [64 heads][128 B]
 constexpr int kBlkP = kHeads * 128;       // 64 rows of P: [64 heads][128 B]
-constexpr int kOffR = 0;                  // 8 blocks, 128 KiB
-constexpr int kOffQ = kOffR + 8 * kBlkR;  // 8 blocks, 64 KiB
-constexpr int kOffP = kOffQ + 8 * kBlkQ;  // 2 blocks, 16 KiB
-constexpr int kOffMisc = kOffP + 2 * kBlkP;
-constexpr int kSmemBytes = kOffMisc + 128 + 1024;
+constexpr int kOffR = 0;                                // 3 groups of 2 blocks, 96 KiB
+constexpr int kOffQ = kOffR + kPlaces * 2 * kBlkR;      // 8 blocks, 64 KiB
+constexpr int kOffP = kOffQ + 8 * kBlkQ;                // 2 blocks, 16 KiB
+constexpr int kRawGroup = kRows * 64;                   // a group's codes, [128 rows][64 B] with the 64-byte swizzle
+constexpr int kOffRaw = kOffP + 2 * kBlkP;              // a tile's codes, 32 KiB
+constexpr int kOffRawSc = kOffRaw + 4 * kRawGroup;      // and scales, [128 rows][32 B], 4 KiB
+constexpr int kOffMisc = kOffRawSc + kRows * kKvScales;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;             // S^T: 64 columns (heads), lanes = rows
 constexpr uint32_t kColO = 64;            // O^T: 4 blocks x 64 columns, lanes = channels
+// R as the A operand of S^T: lanes = rows, 64 columns per 128 channels, a ring of
+// three places
+constexpr uint32_t kColA = 320;
 
 // P = 2^(S' - ref): at most 2^kTop when ref is the maximum itself, at most
 // 2^(kTop + kSlack) = 2^15 before ref moves, below fp16's 65,504. The offset
 // kTop keeps weights down to 2^-25 of the maximum at fp16's full precision
 // (2^-14 is its smallest normal), and to 2^-35 above zero.
 constexpr float kTop = 11.0f, kSlack = 4.0f;
-constexpr float kNoRef = -1e30f;          // a head that has seen nothing yet
 
 constexpr int kPartFloats = kHeads * kHeadDim;
 
@@ -94,8 +110,8 @@ struct Args {
 };
 
 // ---- the list of tiles --------------------------------------------------------
-__device__ __forceinline__ int64_t tiles_of(int64_t visible) {  // a token without entries has one empty tile
-  return visible <= kRows ? 1 : (visible + kRows - 1) / kRows;
+__device__ __forceinline__ int32_t tiles_of(int32_t visible) {  // a token without entries has one empty tile
+  return visible <= kRows ? 1 : (int32_t)(((uint32_t)visible + kRows - 1) / kRows);
 }
 // sum of ceil(v / 128) for v = 1 .. x
 __device__ __forceinline__ int64_t tiles_upto(int64_t x) {
@@ -104,7 +120,7 @@ __device__ __forceinline__ int64_t tiles_upto(int64_t x) {
 }
 struct Seq {
   int32_t first, count;  // token rows
-  int64_t visible;       // entries of its last token (of every one if not causal)
+  int32_t visible;       // entries of its last token (of every one if not causal)
 };
 __device__ __forceinline__ Seq load_seq(const Args& a, int32_t b, bool report) {
   const TokenRun run = token_run(a.cu, b, a.n_tokens, a.per_seq);
@@ -116,17 +132,94 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int32_t b, bool report) {
   }
   return s;
 }
-__device__ __forceinline__ int64_t visible_of(const Args& a, const Seq& s, int32_t t) {
+__device__ __forceinline__ int32_t visible_of(const Args& a, const Seq& s, int32_t t) {
   return a.causal ? s.visible - s.count + 1 + t : s.visible;
 }
 // tiles of the sequence's first n tokens
-__device__ __forceinline__ int64_t tiles_before(const Args& a, const Seq& s, int64_t n) {
-  if (!a.causal) return n * tiles_of(s.visible);
-  const int64_t v0 = s.visible - s.count + 1;  // entries of token 0
-  const int64_t blind = v0 > 0 ? 0 : 1 - v0 < n ? 1 - v0 : n;  // tokens that see nothing
-  const int64_t hi = v0 + n - 1;               // entries of the last of the n
+__device__ __forceinline__ int64_t tiles_before(const Args& a, const Seq& s, int32_t n) {
+  if (!a.causal) return (int64_t)n * tiles_of(s.visible);
+  const int64_t v0 = (int64_t)s.visible - s.count + 1;              // entries of token 0
+  const int64_t blind = v0 > 0 ? 0 : 1 - v0 < n ? 1 - v0 : n;       // tokens that see nothing
+  const int64_t hi = v0 + n - 1;                                    // entries of the last of the n
   return blind + (hi > 0 ? tiles_upto(hi) - tiles_upto(v0 > 1 ? v0 - 1 : 0) : 0);
 }
+
+// A walk along the list.
+struct Walk {
+  int32_t b, tok;
+  Seq seq;
+  int32_t tile, visible, tiles;  // the place in the token, its entries and tiles
+  __device__ __forceinline__ void start(const Args& a, int32_t b_, int64_t at) {
+    b = b_;
+    seq = load_seq(a, b, false);
+    int32_t lo = 0, hi = seq.count;  // tiles_before(lo) <= at < tiles_before(hi)
+    while (hi - lo > 1) {
+      const int32_t mid = lo + (hi - lo) / 2;
+      if (tiles_before(a, seq, mid) <= at) lo = mid;
+      else hi = mid;
+    }
+    tok = lo;
+    tile = (int32_t)(at - tiles_before(a, seq, lo));
+    visible = visible_of(a, seq, tok);
+    tiles = tiles_of(visible);
+  }
+  // only called while the list has a tile behind this one
+  __device__ __forceinline__ void step(const Args& a) {
+    if (++tile < tiles) return;
+    tile = 0;
+    ++tok;
+    while (tok >= seq.count) {
+      ++b;
+      seq = load_seq(a, b, false);
+      tok = 0;
+    }
+    visible = visible_of(a, seq, tok);
+    tiles = tiles_of(visible);
+  }
+};
+// What the roles need to know of a tile, in a ring of kRing tiles.
+constexpr int kRing = 8;
+struct Info {
+  int32_t page[8];  // the table's entries for its rows, 16 at a time
+  int32_t rows;     // entries of the token from the tile's first row on
+  int32_t at;       // its first entry
+  int32_t token;    // row of q
+  int32_t left;     // tiles of the token behind this one
+};
+
+// Shared memory behind the operands.
+struct __align__(16) Shared {
+  Info info[kRing];
+  float mul[kHeads];      // sm_scale log2(e) 2^-k of the head's fp16 queries
+  float ref[kHeads];      // reference of P, log2 domain, less kTop
+  float red[4][kHeads];   // per-quadrant maxima, then sums
+  float up[kHeads];       // how far a reference moves; at a token's end what O^T is multiplied with
+  float shrink[kHeads];   // what O^T and l shrink by when a reference moves
+  int64_t scan[kWarps];
+  int64_t at;             // first tile of the run, within its sequence
+  int32_t seq;            // the sequence of the run's first tile
+  uint32_t tmem;
+  volatile int abort;
+  // barriers. Those of a tile complete once per tile, so that tile j waits for
+  // phase j; those of a place once per use.
+  uint64_t full[kPlaces];     // a group is in its place in tensor memory: 4 warps
+  uint64_t empty[kPlaces];    // S^T over it is done
+  uint64_t raw;               // a tile's codes and scales have arrived
+  uint64_t raw_read;          // and been read: 8 warps
+  uint64_t r_full[kPlaces];   // a group is in its place in shared memory: 4 warps
+  uint64_t r_empty[kPlaces];  // its channels of O^T are done
+  uint64_t q;                 // Q written: 8 warps (once per token)
+  uint64_t s;                 // S^T complete
+  uint64_t s_read;            // S^T read: 8 warps
+  uint64_t p;                 // P written, O^T rescaled (or read out): 8 warps
+  uint64_t o;                 // O^T complete
+  uint64_t info_full[kRing];
+  uint64_t info_used[kRing];  // 19 warps
+  uint64_t end[2];
+};
+// (no static shared memory: dynamic shared memory then starts 1,024-byte aligned)
+constexpr int kSmemBytes = kOffMisc + (int)sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory of one block");
 
 // bar.red.or over the 128 threads of a head group
 __device__ __forceinline__ bool group_any(int id, bool p) {
@@ -140,40 +233,48 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
   return r != 0;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args a) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_u32 = tc::smem_u32(smem_raw);
-  uint8_t* sm = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
+// 32 bytes of the cache (read once per token, by many CTAs: L2)
+__device__ __forceinline__ void ldg_32(const uint8_t* p, uint32_t* r) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap rows_map, Args a) {
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sR = sm + kOffR;
   uint8_t* sQ = sm + kOffQ;
   uint8_t* sP = sm + kOffP;
-  uint64_t* bar_r = reinterpret_cast<uint64_t*>(sm + kOffMisc);  // R (and Q) of a tile written: 16 warps
-  uint64_t* bar_s = bar_r + 1;                                   // S^T complete
-  uint64_t* bar_p = bar_r + 2;                                   // P written, O^T rescaled: 16 warps
-  uint64_t* bar_pv = bar_r + 3;                                  // [4] a channel block of O^T complete
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kOffMisc + 64);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + kOffMisc + 68);
-  __shared__ __align__(16) float s_mul[kHeads];     // sm_scale log2(e) 2^-k of the head's fp16 queries
-  __shared__ __align__(16) float s_ref[kHeads];     // reference of P, log2 domain, less kTop
-  __shared__ __align__(16) float s_red[4][kHeads];  // per-quadrant maxima, then sums
-  __shared__ float s_inv[kHeads];
-  __shared__ int64_t s_scan[kWarps];
-  __shared__ int64_t s_at;       // first tile of the run, within its sequence
-  __shared__ int32_t s_seq;      // the sequence of the run's first tile
+  Shared& sh = *reinterpret_cast<Shared*>(sm + kOffMisc);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = (int)gridDim.x, cta = (int)blockIdx.x;
 
   if (tid == 0) {
-    tc::mbar_init(bar_r, 16);
-    tc::mbar_init(bar_s, 1);
-    tc::mbar_init(bar_p, 16);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(bar_pv + i, 1);
-    *s_abort = 0;
-    s_seq = -1;
+    for (int i = 0; i < kPlaces; ++i) {
+      tc::mbar_init(sh.full + i, 4);
+      tc::mbar_init(sh.empty + i, 1);
+      tc::mbar_init(sh.r_full + i, 4);
+      tc::mbar_init(sh.r_empty + i, 1);
+    }
+    tc::mbar_init(&sh.raw, 1);
+    tc::mbar_init(&sh.raw_read, 8);
+    tc::mbar_init(&sh.q, kSoftWarps);
+    tc::mbar_init(&sh.s, 1);
+    tc::mbar_init(&sh.s_read, kSoftWarps);
+    tc::mbar_init(&sh.p, kSoftWarps);
+    tc::mbar_init(&sh.o, 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(sh.end + i, 1);
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(sh.info_full + i, 1);
+      tc::mbar_init(sh.info_used + i, 19);
+    }
+    sh.abort = 0;
+    sh.seq = -1;
     tc::fence_mbar_init();
   }
-  if (warp == 0) tc::tmem_alloc(s_tmem, kTmemCols);
+  if (warp == 0) tc::tmem_alloc(&sh.tmem, kTmemCols);
   pdl_begin();
 
   // ---- this CTA's run [f0, f1) of the list: a scan over the sequences' tiles ----
@@ -187,9 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args a) {
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) s_scan[warp] = n;
+    if (lane == 0) sh.scan[warp] = n;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) total += s_scan[w];
+    for (int w = 0; w < kWarps; ++w) total += sh.scan[w];
     __syncthreads();
   }
   const int64_t f0 = total * cta / G, f1 = total * (cta + 1) / G;
@@ -210,16 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args a) {
         const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (lane == 31) s_scan[warp] = incl;
+      if (lane == 31) sh.scan[warp] = incl;
       __syncthreads();
       int64_t lo = base + incl - n;
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) lo += s_scan[w];
-        base += s_scan[w];
+        if (w < warp) lo += sh.scan[w];
+        base += sh.scan[w];
       }
       if (f0 >= lo && f0 < lo + n) {
-        s_seq = b;
-        s_at = f0 - lo;
+        sh.seq = b;
+        sh.at = f0 - lo;
       }
       __syncthreads();
     }
@@ -227,379 +328,510 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(Args a) {
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *s_tmem;
-  const int64_t n_run = f1 - f0;  // tiles of this CTA
+  const uint32_t tmem = sh.tmem;
+  const int32_t n_run = (int32_t)(f1 - f0);  // tiles of this CTA (the host has checked the range)
 
-  if (n_run > 0) {
-    // ---- workers: warp w, lane quadrant q = w % 4 (rows 32q ..), group g = w / 4
-    // (channels 128g .. of R and O^T; heads 16g .. of S and P) ----
-    const int quad = warp & 3, grp = warp >> 2, h0 = grp * 16;
-    // ---- the products, issued by warp 0 once every warp's rows (or P) are there ----
-    const auto issue_s = [&](uint32_t par) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_bounded(bar_r, par, s_abort, &g_paged_attn_error))) return;
-      tc::tc_fence_after();
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_f16(128, 64, 0, 0);
-        const uint64_t ad = tc::smem_desc(tc::smem_u32(sR), 0, 1024, tc::kSwizzle128B);
-        const uint64_t bd = tc::smem_desc(tc::smem_u32(sQ), 0, 1024, tc::kSwizzle128B);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {  // block j / 4 of 64 channels, K step j % 4
-          const uint64_t ko = (uint64_t)((j & 3) * 2);
-          tc::mma_bf16(tmem + kColS, ad + (uint64_t)((j >> 2) * (kBlkR >> 4)) + ko,
-                       bd + (uint64_t)((j >> 2) * (kBlkQ >> 4)) + ko, idesc, j ? 1u : 0u);
-        }
-        tc::mma_commit(bar_s);
+  // A wait that runs out (2^22 tries, a tenth of a second at least) raises
+  // sh.abort, on which every later wait gives up at once and nothing more is
+  // issued. The loops then run to their ends all the same, so that no warp is
+  // missing at a barrier; the outputs are worthless and TIMEOUT is recorded.
+  // (Counted, not timed, and kept short: the code of all roles together has to
+  // stay in the instruction cache.)
+  const auto wait = [&](uint64_t* bar, uint32_t par) {
+    uint32_t n = 0;
+    while (!tc::mbar_try_wait(bar, par & 1u)) {
+      if (sh.abort || ++n >= (1u << 22)) {
+        sh.abort = 1;
+        break;
       }
-      __syncwarp();
-    };
-    const auto issue_pv = [&](uint32_t par, bool anew) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_bounded(bar_p, par, s_abort, &g_paged_attn_error))) return;
-      tc::tc_fence_after();
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_f16(128, 64, 1, 0);  // A = R^T is MN-major
-        const uint64_t ad = tc::smem_desc(tc::smem_u32(sR), kBlkR, 1024, tc::kSwizzle128B);
-        const uint64_t bd = tc::smem_desc(tc::smem_u32(sP), 0, 1024, tc::kSwizzle128B);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {  // channel block j / 8, K step j % 8 (16 rows)
-          const int mb = j >> 3, kk = j & 7;
-          tc::mma_bf16(tmem + kColO + 64u * (uint32_t)mb, ad + (uint64_t)((2 * mb * kBlkR + kk * 16 * 128) >> 4),
-                       bd + (uint64_t)(((kk >> 2) * kBlkP + (kk & 3) * 32) >> 4), idesc, kk || !anew ? 1u : 0u);
-          if (kk == 7) tc::mma_commit(bar_pv + mb);
-        }
-      }
-      __syncwarp();
-    };
-    // the place in the list: tile `tile` of token `tok` of sequence `b`
-    int32_t b = s_seq;
-    Seq seq = load_seq(a, b, false);
-    int32_t tok;
-    int64_t tile;
-    {
-      int64_t at = s_at;
-      int32_t lo = 0, hi = seq.count;  // tiles_before(lo) <= at < tiles_before(hi)
-      while (hi - lo > 1) {
-        const int32_t mid = lo + (hi - lo) / 2;
-        if (tiles_before(a, seq, mid) <= at) lo = mid;
-        else hi = mid;
-      }
-      tok = lo;
-      tile = at - tiles_before(a, seq, lo);
     }
-    int64_t visible = visible_of(a, seq, tok);
-    int64_t tiles = tiles_of(visible);
+    __syncwarp();
+  };
+  const auto arrive = [&](uint64_t* bar) {  // once per warp, after all its lanes' work
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+  };
+  // tile j's Info; info_done() when a warp is done with it
+  const auto info_of = [&](int32_t j) -> const Info& {
+    wait(sh.info_full + j % kRing, (uint32_t)(j / kRing));
+    return sh.info[j % kRing];
+  };
+  const auto info_done = [&](int32_t j) { arrive(sh.info_used + j % kRing); };
+  const int quad = warp & 3, half = (warp >> 2) & 1;
+  const int my_row = quad * 32 + lane;  // of a tile
+  const uint32_t lanes = (uint32_t)(quad * 32) << 16;
 
-    // loads of a tile: lane l of a group of 8 rows takes row l / 4, channels
-    // 128 grp + 32 (l % 4) .. +31 (16 bytes of codes, 2 of scales): 64 whole
-    // bytes of a row per 4 lanes
-    uint4 raw[4];
-    uint32_t scl[4];
-    uint32_t gone = 0;  // bit i: rows 8i .. 8i+7 of the warp's 32 lie in a page outside the pool
-    auto load_rows = [&](int32_t lb, int64_t ltile, int64_t lvisible) {
-int64_t row[4];
+  if (warp >= kSWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // The two issuing warps. An issue blocks while the tensor pipe's queue is
+    // full, and S^T of a tile and O^T of the one before depend on different
+    // things: one warp for both waited for each in turn (measured 8,700 cycles a
+    // tile, of which the products are 2,560). The votes say what is so: every
+    // branch around the products is the whole warp's. Only then does the compiler
+    // keep their operands in uniform registers; else each product costs moves
+    // there, 80 to 100 cycles against the 32 or 48 of the tensor pipe.
+    const auto all = [](bool c) { return __any_sync(0xffffffffu, c) != 0; };
+    const uint32_t elected = tc::elect_one();
+    if (warp == kSWarp) {
+      constexpr uint32_t idesc = idesc_f16(128, 64, 0, 0);
+      const uint32_t q_lo = tc::smem_u32(sQ);
+      uint32_t place = 0, use = 0;  // the ring's next place, and how often it went round
+      uint32_t tokens = 0;
+#pragma unroll 1
+      for (int32_t j = 0; all(j < n_run); ++j) {
+        if (all(info_of(j).at == 0 || j == 0)) wait(&sh.q, tokens++);
+        if (all(j > 0)) wait(&sh.s_read, (uint32_t)(j - 1));
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {  // channels 128 g ..
+          wait(sh.full + place, use);
+          tc::tc_fence_after();
+          if (all(sh.abort != 0)) break;
+          const uint32_t at = tmem + kColA + 64u * place;
+          const uint64_t bd = tc::smem_desc(q_lo + (uint32_t)(2 * g * kBlkQ), 0, 1024, tc::kSwizzle128B);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t e = ltile * kRows + quad * 32 + i * 8 + (lane >> 2);
-        row[i] = e < lvisible ? a.pages.row(lb, e) : -2;
-      }
-      gone = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (row[i] == -1) {
-          gone |= 1u << i;
-          record_error(&g_paged_attn_error, CSA2_ERR_DEVICE);
-        }
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        scl[i] = 0u;
-        if (row[i] >= 0) {
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(a.kv_data + row[i] * kKvBytes + grp * 64) + (lane & 3));
-          scl[i] = __ldg(reinterpret_cast<const uint16_t*>(a.kv_scale + row[i] * kKvScales + grp * 8) + (lane & 3));
-        }
-      }
-      gone = __reduce_or_sync(0xffffffffu, gone);
-    };
-    // the loaded rows as fp16 (exact) into R; rows not seen are zero. The eight
-    // lanes of a store phase (two rows) take their words in different orders, so
-    // that they cover the eight bank groups: lanes of odd 64-channel blocks swap
-    // words 0/1 and 2/3, those of odd rows the halves.
-    auto write_rows = [&]() {
-      const bool sw1 = (lane >> 1) & 1, sw2 = (lane >> 2) & 1;
-      const uint32_t kx = (sw1 ? 1u : 0u) ^ (sw2 ? 2u : 0u);
-      uint8_t* blk = sR + (2 * grp + ((lane >> 1) & 1)) * kBlkR;
-      const uint32_t c0 = (uint32_t)(lane & 1) * 4u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t r = (uint32_t)(quad * 32 + i * 8 + (lane >> 2));
-        uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = sw1 ? w[k ^ 1] : w[k];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = sw2 ? u[k ^ 2] : u[k];
-        const uint32_t s2 = e4m3x2_to_f16x2(scl[i]);
-        const uint32_t lo = __byte_perm(s2, 0u, 0x1010u), hi = __byte_perm(s2, 0u, 0x3232u);
-        const uint32_t sa = sw2 ? hi : lo, sb = sw2 ? lo : hi;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // w[k]: word k ^ kx of the 16 bytes
-          uint32_t o0, o1, o2, o3;
-          e2m1x8_to_f16(w[k], o0, o1, o2, o3);
-          const uint32_t m = k < 2 ? sa : sb;
-          *reinterpret_cast<uint4*>(blk + tc::sw128_offset(r, c0 + ((uint32_t)k ^ kx))) =
-              make_uint4(mul_f16x2(o0, m), mul_f16x2(o1, m), mul_f16x2(o2, m), mul_f16x2(o3, m));
-        }
-      }
-    };
-    // the token's queries as fp16 with a power-of-two scale per head (exact but
-    // for values below 2^-28 of the head's largest): thread (h, j) takes 16
-    // bytes of each 64-channel block
-    auto write_q = [&](int64_t token) {
-      const int h = tid >> 3, j = tid & 7;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (token * kHeads + h) * kHeadDim) + j;
-      uint4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = src[k * 8];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-      }
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-      int k2 = 0;
-      if (amax != 0u) k2 = min(max(14 - ((int)(amax >> 7) - 127), -100), 100);
-      const float up = __int_as_float((127 + k2) << 23);
-      const uint32_t col = (uint32_t)((j ^ (h & 7)) << 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = f32x2_to_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-        *reinterpret_cast<uint4*>(sQ + k * kBlkQ + h * 128 + col) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      if (j == 0) {
-        s_mul[h] = a.scale_log2 * __int_as_float((127 - k2) << 23);
-        s_ref[h] = kNoRef;
-      }
-    };
-
-    float l_acc[16];  // this row lane's share of l for the group's heads
-    int slot = 2 * cta;     // where a part of the present token goes
-    bool whole = tile == 0; // the CTA has the token from its first tile on
-    int64_t rows_seen = 0;  // the present tile's entries
-    uint32_t gone_now = 0;
-    load_rows(b, tile, visible);
-    write_q(seq.first + tok);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) l_acc[j] = 0.0f;
-    write_rows();
-    bool first = true;
-    rows_seen = visible - tile * kRows;
-    gone_now = gone;
-    tc::fence_proxy_async_smem();
-    __syncthreads();  // s_mul, s_ref
-    if (lane == 0) tc::mbar_arrive(bar_r);
-
-    // A wait that runs out (2 s) raises s_abort, on which every later wait gives
-    // up at once and nothing more is issued. The loop then runs to its end all
-    // the same, so that no warp is missing at a barrier; the outputs are
-    // worthless and TIMEOUT is recorded.
-    const auto wait = [&](uint64_t* bar, uint32_t par) {
-      const bool ok = tc::mbar_wait_bounded(bar, par, s_abort, &g_paged_attn_error);
-      return __all_sync(0xffffffffu, ok);
-    };
-    if (warp == 0) issue_s(0);
-    for (int64_t i = 0; i < n_run; ++i) {
-      const uint32_t par = (uint32_t)i & 1u;
-      const bool last_of_run = i + 1 == n_run;
-      const bool last_of_token = tile + 1 == tiles;
-      // the next tile of the list
-      int32_t nb = b, ntok = tok;
-      int64_t ntile = tile + 1, nvisible = visible, ntiles = tiles;
-      Seq nseq = seq;
-      if (!last_of_run) {
-        if (last_of_token) {
-          ntile = 0;
-          ++ntok;
-          while (ntok >= nseq.count) {  // ends: the list has a tile behind this one
-            ++nb;
-            nseq = load_seq(a, nb, false);
-            ntok = 0;
+          for (int k = 0; k < 8; ++k)  // block 2g + k / 4 of 64 channels, K step k % 4
+            tc::mma_f16_ta_one(elected, tmem + kColS, at + 8u * (uint32_t)k,
+                               bd + (uint64_t)((k >> 2) * (kBlkQ >> 4) + (k & 3) * 2), idesc,
+                               k ? 1u : (uint32_t)(g != 0));
+          tc::mma_commit_one(elected, sh.empty + place);
+          if (all(++place == kPlaces)) {
+            place = 0;
+            ++use;
           }
-          nvisible = visible_of(a, nseq, ntok);
-          ntiles = tiles_of(nvisible);
         }
-        load_rows(nb, ntile, nvisible);
+        tc::mma_commit_one(elected, &sh.s);
+        info_done(j);
       }
+    } else if (warp == kOWarp) {
+      constexpr uint32_t idesc = idesc_f16(128, 64, 1, 0);  // A = R^T is MN-major
+      const uint32_t r_lo = tc::smem_u32(sR), p_lo = tc::smem_u32(sP);
+      uint32_t place = 0, use = 0;
+#pragma unroll 1
+      for (int32_t j = 0; all(j < n_run); ++j) {
+        const uint32_t more = j > 0 && info_of(j).at != 0 ? 1u : 0u;  // 0: O^T starts anew
+        wait(&sh.p, (uint32_t)j);
+#pragma unroll 1
+        for (int mb = 0; mb < 4; ++mb) {  // 128 channels
+          wait(sh.r_full + place, use);
+          tc::tc_fence_after();
+          if (all(sh.abort != 0)) break;
+          const uint64_t ad = tc::smem_desc(r_lo + place * (uint32_t)(2 * kBlkR), kBlkR, 1024, tc::kSwizzle128B);
+          const uint64_t bd = tc::smem_desc(p_lo, 0, 1024, tc::kSwizzle128B);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 rows
+            tc::mma_f16_one(elected, tmem + kColO + 64u * (uint32_t)mb, ad + (uint64_t)((k * 16 * 128) >> 4),
+                            bd + (uint64_t)(((k >> 2) * kBlkP + (k & 3) * 32) >> 4), idesc, k ? 1u : more);
+          tc::mma_commit_one(elected, sh.r_empty + place);
+          if (all(++place == kPlaces)) {
+            place = 0;
+            ++use;
+          }
+        }
+        tc::mma_commit_one(elected, &sh.o);
+        info_done(j);
+      }
+    } else if (warp == kWalkWarp && n_run > 0) {
+      Walk w;
+      w.start(a, sh.seq, sh.at);
+#pragma unroll 1
+      for (int32_t j = 0; j < n_run; ++j) {
+        const int32_t e = w.tile * kRows + 16 * lane;
+        int32_t page = -1;
+        if (lane < 8 && e < w.visible) {
+          page = a.pages.table[(int64_t)w.b * a.pages.max_pages + (e >> a.pages.shift)];
+          if (page < 0 || page >= a.pages.n_pages) {
+            page = -1;
+            record_error(&g_paged_attn_error, CSA2_ERR_DEVICE);
+          }
+        }
+        if (j >= kRing) wait(sh.info_used + j % kRing, (uint32_t)(j / kRing) - 1u);
+        Info& to = sh.info[j % kRing];
+        if (lane < 8) to.page[lane] = page;
+        if (lane == 0) {
+          to.rows = w.visible - w.tile * kRows;
+          to.at = w.tile * kRows;
+          to.token = w.seq.first + w.tok;
+          to.left = w.tiles - 1 - w.tile;
+        }
+        arrive(sh.info_full + j % kRing);
+        if (j + 1 < n_run) w.step(a);
+      }
+    } else if (warp == kCopyWarp) {
+      // a run of rows is a whole small page, or the tile's piece of a page; a
+      // group's 64 bytes of its rows are one tensor copy, its scales a bulk copy.
+      // What a missing run leaves behind is never used (its scales count as 0).
+      const int run_shift = a.pages.shift < 7 ? a.pages.shift : 7;
+      const int run = 1 << run_shift;
+#pragma unroll 1
+      for (int32_t j = 0; j < n_run; ++j) {
+        const Info& info = info_of(j);
+        if (j > 0) wait(&sh.raw_read, (uint32_t)(j - 1));
+        // lane i: run i
+        const int r0 = lane << run_shift;
+        const int32_t page = r0 < kRows && r0 < info.rows ? info.page[r0 >> 4] : -1;
+        const uint32_t there = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        if (lane == 0) tc::mbar_arrive_expect_tx(&sh.raw, there * (uint32_t)run * (kKvBytes + kKvScales));
+        __syncwarp();
+        if (page >= 0 && !sh.abort) {
+          const int64_t row = ((int64_t)page << a.pages.shift) + ((info.at + r0) & (a.pages.page_size() - 1));
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            tc::tma_load_2d(sm + kOffRaw + g * kRawGroup + r0 * 64, &rows_map, g * 64, (int32_t)row, &sh.raw);
+          tc::bulk_load(sm + kOffRawSc + r0 * kKvScales, a.kv_scale + row * kKvScales, (uint32_t)(run * kKvScales),
+                        &sh.raw);
+        }
+        info_done(j);
+      }
+      // (the last copies are waited for by the warps that read them; those may not
+      // have when a wait ran out)
+      for (uint32_t n = 0; n_run > 0 && sh.abort && n < (1u << 22); ++n)
+        if (tc::mbar_try_wait(&sh.raw, (uint32_t)(n_run - 1) & 1u)) break;
+    }
+    if ((warp == kSWarp || warp == kOWarp) && n_run > 0 && sh.abort) {
+      // a wait ran out: products in flight end before tensor memory is freed
+      tc::mma_commit_one(elected, sh.end + (warp - kSWarp));
+      for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.end + (warp - kSWarp), 0); ++n) {
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    if (n_run > 0) {
+      // ---- dequantise: a thread takes the channels of groups half and half + 2
+      // (128 each: 64 bytes of codes, 8 of scales) of its row from where the copies
+      // put them (plain loads into registers made the warp wait for them at the
+      // next use of their scoreboard, 3,400 cycles a tile), and keeps them as they
+      // are for two tiles: tile t goes to tensor memory (for S^T) before tile t - 1
+      // goes to shared memory (for O^T) ----
+      struct Raw {
+        uint32_t w[16];
+        uint2 sc;
+      };
+      auto take = [&](Raw& r, int g, bool seen) {
+        const uint8_t* src = sm + kOffRaw + g * kRawGroup;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + tc::sw64_offset((uint32_t)my_row, (uint32_t)k));
+          r.w[4 * k] = v.x;
+          r.w[4 * k + 1] = v.y;
+          r.w[4 * k + 2] = v.z;
+          r.w[4 * k + 3] = v.w;
+        }
+        // (codes are finite whatever they are: times 0 they are zeros)
+        r.sc = *reinterpret_cast<const uint2*>(sm + kOffRawSc + my_row * kKvScales + g * 8);
+        if (!seen) r.sc = make_uint2(0u, 0u);
+      };
+      // channels 32 q .. +31 of a group as fp16 (exact; zeros for zero codes and scales)
+      auto convert = [&](const Raw& r, int q, uint32_t (&o)[16]) {
+        const uint32_t s2 = e4m3x2_to_f16x2(((q < 2 ? r.sc.x : r.sc.y) >> ((q & 1) * 16)) & 0xFFFFu);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t s = __byte_perm(s2, 0u, k < 2 ? 0x1010u : 0x3232u);
+          uint32_t o0, o1, o2, o3;
+          e2m1x8_to_f16(r.w[4 * q + k], o0, o1, o2, o3);
+          o[4 * k] = mul_f16x2(o0, s);
+          o[4 * k + 1] = mul_f16x2(o1, s);
+          o[4 * k + 2] = mul_f16x2(o2, s);
+          o[4 * k + 3] = mul_f16x2(o3, s);
+        }
+      };
+      // group g of tile t into its place in tensor memory
+      auto feed_s = [&](const Raw& r, int32_t t, int g) {
+        const uint32_t n = 4u * (uint32_t)t + (uint32_t)g, use = n / kPlaces, place = n - use * kPlaces;
+        if (use > 0) wait(sh.empty + place, use - 1u);
+        tc::tc_fence_after();
+        const uint32_t at = tmem + lanes + kColA + 64u * place;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[16];
+          convert(r, q, o);
+          tc::tmem_st_32x32b_x16(at + 16u * (uint32_t)q, o);
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        arrive(sh.full + place);
+      };
+      // group g of tile t into its place in R (the eight lanes of a store phase are
+      // eight rows: eight bank groups)
+      auto feed_o = [&](const Raw& r, int32_t t, int g) {
+        const uint32_t n = 4u * (uint32_t)t + (uint32_t)g, use = n / kPlaces, place = n - use * kPlaces;
+        if (use > 0) wait(sh.r_empty + place, use - 1u);
+        uint8_t* blk = sR + place * (2 * kBlkR);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[16];
+          convert(r, q, o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(blk + (q >> 1) * kBlkR +
+                                      tc::sw128_offset((uint32_t)my_row, (uint32_t)((q & 1) * 4 + k))) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        tc::fence_proxy_async_smem();
+        arrive(sh.r_full + place);
+      };
+      Raw c0, c1, p0, p1;  // tile t, tile t - 1
+#pragma unroll 1
+      for (int32_t t = 0; t <= n_run; ++t) {
+        if (t < n_run) {
+          const Info& info = info_of(t);
+          const bool seen = my_row < info.rows && info.page[my_row >> 4] >= 0;
+          wait(&sh.raw, (uint32_t)t);
+          take(c0, half, seen);
+          take(c1, half + 2, seen);
+          arrive(&sh.raw_read);
+          feed_s(c0, t, half);
+          feed_s(c1, t, half + 2);
+          info_done(t);
+        }
+        if (t > 0) {
+          feed_o(p0, t - 1, half);
+          feed_o(p1, t - 1, half + 2);
+        }
+        p0 = c0;
+        p1 = c1;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    if (n_run > 0) {
+      // ---- softmax: a thread takes heads 32 half .. +31 of its row ----
+      const int h0 = half * 32;
+      // the token's queries as fp16 with a power-of-two scale per head (exact but
+      // for values below 2^-28 of the head's largest): thread (h, c) takes the
+      // 16-byte columns c and c + 4 of each 64-channel block, in two passes (the
+      // second from L1: all its 64 words would not fit the registers)
+      auto write_q = [&](int64_t token) {
+        const int h = tid >> 2, c = tid & 3;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (token * kHeads + h) * kHeadDim) + c;
+        uint32_t amax = 0;
+#pragma unroll 1
+        for (int k = 0; k < 8; k += 2) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = src[(k + (i >> 1)) * 8 + (i & 1) * 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+          }
+        }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int k2 = 0;
+        if (amax != 0u) k2 = min(max(14 - ((int)(amax >> 7) - 127), -100), 100);
+        const float up = __int_as_float((127 + k2) << 23);
+#pragma unroll 1
+        for (int k = 0; k < 8; k += 2) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = src[(k + (i >> 1)) * 8 + (i & 1) * 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = f32x2_to_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+            *reinterpret_cast<uint4*>(sQ + (k + (i >> 1)) * kBlkQ +
+                                      tc::sw128_offset((uint32_t)h, (uint32_t)(c + (i & 1) * 4))) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        if (c == 0) sh.mul[h] = a.scale_log2 * __int_as_float((127 - k2) << 23);
+        tc::fence_proxy_async_smem();
+        arrive(&sh.q);
+      };
 
-      wait(bar_s, par);
-      tc::tc_fence_after();
-      // ---- P of the tile: this thread's row, the group's 16 heads ----
-      {
-        const int row = quad * 32 + lane;
-        const bool rv = row < rows_seen && !((gone_now >> (lane >> 3)) & 1u);
-        uint32_t sr[16];
-        tc::tmem_ld_32x32b_x16(tmem + ((uint32_t)(quad * 32) << 16) + kColS + (uint32_t)h0, sr);
+      float l_acc[32];  // this row lane's share of l
+#pragma unroll
+      for (int i = 0; i < 32; ++i) l_acc[i] = 0.0f;
+      if (tid < kHeads) sh.ref[tid] = 0.0f;
+      write_q(info_of(0).token);
+      named_barrier(8, kSoftWarps * 32);  // mul, ref
+      int slot = 2 * cta;               // where a part of the present token goes
+      bool whole = info_of(0).at == 0;  // the CTA has the token from its first tile on
+      bool first = true;                // the CTA's first tile of the token
+      bool open = true;                 // the references are not set yet
+#pragma unroll 1
+      for (int32_t j = 0; j < n_run; ++j) {
+        const uint32_t par = (uint32_t)j & 1u;
+        const Info& info = info_of(j);
+        const bool rv = my_row < info.rows && info.page[my_row >> 4] >= 0;
+
+        wait(&sh.s, par);
+        tc::tc_fence_after();
+        uint32_t pr[32];
+        tc::tmem_ld_32x32b_x32(tmem + lanes + kColS + (uint32_t)h0, pr);
         tc::tmem_ld_wait();
-        float p[16];
+        tc::tc_fence_before();
+        arrive(&sh.s_read);
+        // S' - ref
         float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          p[j] = rv ? __uint_as_float(sr[j]) * s_mul[h0 + j] : -INFINITY;
-          top = fmaxf(top, p[j] - s_ref[h0 + j]);
+        for (int i = 0; i < 32; i += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(sh.mul + h0 + i);
+          const float4 r4 = *reinterpret_cast<const float4*>(sh.ref + h0 + i);
+          const float t0 = fmaf(__uint_as_float(pr[i]), m4.x, -r4.x);
+          const float t1 = fmaf(__uint_as_float(pr[i + 1]), m4.y, -r4.y);
+          const float t2 = fmaf(__uint_as_float(pr[i + 2]), m4.z, -r4.z);
+          const float t3 = fmaf(__uint_as_float(pr[i + 3]), m4.w, -r4.w);
+          top = fmaxf(fmaxf(fmaxf(top, t0), fmaxf(t1, t2)), t3);
+          pr[i] = __float_as_uint(t0);
+          pr[i + 1] = __float_as_uint(t1);
+          pr[i + 2] = __float_as_uint(t2);
+          pr[i + 3] = __float_as_uint(t3);
         }
-        if (group_any(1 + grp, top > kTop + kSlack)) {
-          // a head's scores passed its reference: new references, O^T and l to match
-          float v[16];
+        if (!rv) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = p[j];
-          const float m = warp_transpose_reduce16<true>(v, lane);
-          if (lane < 16) s_red[quad][h0 + lane] = m;
-          named_barrier(1 + grp, 128);
-          float alpha[16];
+          for (int i = 0; i < 32; ++i) pr[i] = 0xFF800000u;  // -inf
+        }
+        if (group_any(1 + half, open || (rv && top > kTop + kSlack))) {
+          // a head's scores passed its reference (or it has none yet): new
+          // references, O^T and l to match
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float mt = fmaxf(fmaxf(s_red[0][h0 + j], s_red[1][h0 + j]), fmaxf(s_red[2][h0 + j], s_red[3][h0 + j]));
-            const float old = s_ref[h0 + j];
-            alpha[j] = mt > old + (kTop + kSlack) ? fast_exp2(old - (mt - kTop)) : 1.0f;
+          for (int u = 0; u < 32; u += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(pr[u + i]);
+            const float m = warp_transpose_reduce16<true>(v, lane);
+            if (lane < 16) sh.red[quad][h0 + u + lane] = m;
           }
-          named_barrier(1 + grp, 128);  // everyone has read the old references
-          if (quad == 0 && lane < 16) {
-            const float mt = fmaxf(fmaxf(s_red[0][h0 + lane], s_red[1][h0 + lane]),
-                                   fmaxf(s_red[2][h0 + lane], s_red[3][h0 + lane]));
-            if (mt > s_ref[h0 + lane] + (kTop + kSlack)) s_ref[h0 + lane] = mt - kTop;
+          named_barrier(1 + half, 128);
+          if (quad == 0) {
+            const int h = h0 + lane;
+            const float mt = fmaxf(fmaxf(sh.red[0][h], sh.red[1][h]), fmaxf(sh.red[2][h], sh.red[3][h]));
+            const bool move = open ? mt > -INFINITY : mt > kTop + kSlack;
+            const float up = move ? mt - kTop : 0.0f;
+            sh.ref[h] += up;
+            sh.up[h] = up;
+            sh.shrink[h] = open ? 1.0f : fast_exp2(-up);  // (before the first reference O^T and l are 0)
+          }
+          // (a tile with a row sets every head's reference)
+          open = open && !(fmaxf(fmaxf(sh.red[0][h0], sh.red[1][h0]), fmaxf(sh.red[2][h0], sh.red[3][h0])) > -INFINITY);
+          named_barrier(1 + half, 128);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            pr[i] = __float_as_uint(__uint_as_float(pr[i]) - sh.up[h0 + i]);
+            l_acc[i] *= sh.shrink[h0 + i];
           }
           if (!first) {
+            wait(&sh.o, (uint32_t)(j - 1));
+            tc::tc_fence_after();
 #pragma unroll 1
-            for (int mb = 0; mb < 4; ++mb) {
-              const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + kColO + 64u * (uint32_t)mb + (uint32_t)h0;
+            for (int x = 0; x < 8; ++x) {  // channel block x / 2, heads h0 + 16 (x % 2) ..
+              const int u = (x & 1) * 16;
+              const uint32_t at = tmem + lanes + kColO + 64u * (uint32_t)(x >> 1) + (uint32_t)(h0 + u);
               uint32_t ov[16];
               tc::tmem_ld_32x32b_x16(at, ov);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha[j]);
+              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * sh.shrink[h0 + u + i]);
               tc::tmem_st_32x32b_x16(at, ov);
             }
             tc::tmem_st_wait();
+            tc::tc_fence_before();
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) l_acc[j] *= alpha[j];
-          named_barrier(1 + grp, 128);  // the new references
         }
-        uint8_t* blkp = sP + (row >> 6) * kBlkP;
-        const uint32_t chunk = (uint32_t)(row & 63) >> 3, within = ((uint32_t)row & 7u) * 2u;
+        // P = 2^(S' - ref), summed in fp32 and rounded to fp16
+        uint32_t ph[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float e = fast_exp2(p[j] - s_ref[h0 + j]);
-          l_acc[j] += e;  // summed in fp32 before P is rounded to fp16
-          *reinterpret_cast<__half*>(blkp + tc::sw128_offset((uint32_t)(h0 + j), chunk) + within) = __float2half_rn(e);
+        for (int i = 0; i < 16; ++i) {
+          const float e0 = fast_exp2(__uint_as_float(pr[2 * i])), e1 = fast_exp2(__uint_as_float(pr[2 * i + 1]));
+          l_acc[2 * i] += e0;
+          l_acc[2 * i + 1] += e1;
+          ph[i] = f32x2_to_f16x2(e0, e1);
         }
-      }
-      tc::fence_proxy_async_smem();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar_p);
-      if (warp == 0) issue_pv(par, first);
-      first = false;
-
-      if (!last_of_run && !last_of_token) {
-        // ---- the next tile's rows, as the products over this tile's channels end ----
-        wait(bar_pv + grp, par);
-        write_rows();
+        if (j > 0) wait(&sh.o, (uint32_t)(j - 1));  // the last product has read P
+        {
+          uint8_t* blkp = sP + (my_row >> 6) * kBlkP;
+          const uint32_t chunk = (uint32_t)(my_row & 63) >> 3, within = ((uint32_t)my_row & 7u) * 2u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            *reinterpret_cast<uint16_t*>(blkp + tc::sw128_offset((uint32_t)(h0 + 2 * i), chunk) + within) =
+                (uint16_t)(ph[i] & 0xFFFFu);
+            *reinterpret_cast<uint16_t*>(blkp + tc::sw128_offset((uint32_t)(h0 + 2 * i + 1), chunk) + within) =
+                (uint16_t)(ph[i] >> 16);
+          }
+        }
         tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar_r);
-        if (warp == 0) issue_s(par ^ 1u);
-      } else {
-        // ---- the token's (or the run's) end: l over the rows, O^T out ----
-        const float lsum = warp_transpose_reduce16<false>(l_acc, lane);
-        if (lane < 16) s_red[quad][h0 + lane] = lsum;
-        for (int mb = 0; mb < 4; ++mb) wait(bar_pv + mb, par);
-        tc::tc_fence_after();
-        __syncthreads();
-        const bool complete = whole && last_of_token;
-        const int64_t token = seq.first + tok;
-        if (tid < kHeads) {
-          const float l = s_red[0][tid] + s_red[1][tid] + s_red[2][tid] + s_red[3][tid];
-          s_inv[tid] = !complete ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
-          if (!complete) a.part_ml[(int64_t)slot * kHeads + tid] = make_float2(s_ref[tid], l);
-          else if (a.lse)
-            a.lse[token * kHeads + tid] = l > 0.0f ? (s_ref[tid] + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        }
-        __syncthreads();
-        const int c = 128 * grp + 32 * quad + lane;
-        const uint32_t o_base = tmem + ((uint32_t)(quad * 32) << 16) + kColO + 64u * (uint32_t)grp;
-        float* po = a.part_o + (int64_t)slot * kPartFloats + c;
-        float* of = a.out_f32 ? a.out_f32 + token * kPartFloats + c : nullptr;
-        uint16_t* ob = a.out + token * kPartFloats + c;
-#pragma unroll 1
-        for (int hh = 0; hh < kHeads; hh += 16) {
-          uint32_t ov[16];
-          tc::tmem_ld_32x32b_x16(o_base + (uint32_t)hh, ov);
-          tc::tmem_ld_wait();
+        arrive(&sh.p);
+        first = false;
+
+        const bool last_of_token = info.left == 0;
+        if (last_of_token || j + 1 == n_run) {
+          // ---- the token's (or the run's) end: l over the rows, O^T out ----
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float v = __uint_as_float(ov[j]) * s_inv[hh + j];
+          for (int u = 0; u < 32; u += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v[i] = l_acc[u + i];
+              l_acc[u + i] = 0.0f;
+            }
+            const float lsum = warp_transpose_reduce16<false>(v, lane);
+            if (lane < 16) sh.red[quad][h0 + u + lane] = lsum;
+          }
+          named_barrier(8, kSoftWarps * 32);
+          const bool complete = whole && last_of_token;
+          const int64_t token = info.token;
+          if (tid < kHeads) {
+            const float l = sh.red[0][tid] + sh.red[1][tid] + sh.red[2][tid] + sh.red[3][tid];
+            sh.up[tid] = !complete ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+            if (!complete) a.part_ml[(int64_t)slot * kHeads + tid] = make_float2(sh.ref[tid], l);
+            else if (a.lse)
+              a.lse[token * kHeads + tid] = l > 0.0f ? (sh.ref[tid] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            sh.ref[tid] = 0.0f;
+          }
+          named_barrier(8, kSoftWarps * 32);
+          // S^T of the token is complete: the next token's queries, before its O^T
+          // is waited for
+          if (j + 1 < n_run) write_q(info_of(j + 1).token);
+          wait(&sh.o, (uint32_t)j);  // O^T of this tile is complete
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x) {  // channel block 2 half + x / 4, heads 16 (x % 4) ..
+            const int mb = 2 * half + (x >> 2), hh = (x & 3) * 16;
+            const int c = 128 * mb + my_row;
+            uint32_t ov[16];
+            tc::tmem_ld_32x32b_x16(tmem + lanes + kColO + 64u * (uint32_t)mb + (uint32_t)hh, ov);
+            tc::tmem_ld_wait();
             if (!complete) {
-              po[(hh + j) * kHeadDim] = v;
+              float* po = a.part_o + (int64_t)slot * kPartFloats + hh * kHeadDim + c;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) po[i * kHeadDim] = __uint_as_float(ov[i]);
             } else {
-              if (of) of[(hh + j) * kHeadDim] = v;
-              ob[(hh + j) * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+              const int64_t o = token * kPartFloats + hh * kHeadDim + c;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float v = __uint_as_float(ov[i]) * sh.up[hh + i];
+                if (a.out_f32) a.out_f32[o + i * kHeadDim] = v;
+                a.out[o + i * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+              }
             }
           }
-        }
-        if (tid == 0 && whole && !last_of_token) {
-          // the token's first part: its other parts lie with the next CTAs
-          const int64_t last = f1 - 1 + (tiles - 1 - tile);  // the token's last tile in the list
-          PartList pl;
-          pl.token = (int32_t)token;
-          pl.first_slot = slot;
-          pl.cta0 = cta;
-          pl.cta1 = (int32_t)(((last + 1) * G + total - 1) / total - 1);
-          pl.tiles = total;
-          a.lists[cta] = pl;
-        }
-        if (!last_of_run) {
+          // every block of O^T is read before the next token's products replace it
           tc::tc_fence_before();
-          write_rows();
-          // S^T of this token is complete: Q may be replaced
-          write_q(nseq.first + ntok);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) l_acc[j] = 0.0f;
+          if (tid == 0 && whole && !last_of_token) {
+            // the token's first part: its other parts lie with the next CTAs
+            const int64_t last = f1 - 1 + info.left;  // the token's last tile in the list
+            PartList pl;
+            pl.token = (int32_t)token;
+            pl.first_slot = slot;
+            pl.cta0 = cta;
+            pl.cta1 = (int32_t)(((last + 1) * G + total - 1) / total - 1);
+            pl.tiles = total;
+            a.lists[cta] = pl;
+          }
           first = true;
+          open = true;
           whole = true;
           slot = 2 * cta + 1;
-          tc::fence_proxy_async_smem();
-          __syncthreads();  // s_mul, s_ref, s_red
-          if (lane == 0) tc::mbar_arrive(bar_r);
-          if (warp == 0) issue_s(par ^ 1u);
+          named_barrier(8, kSoftWarps * 32);  // mul, ref, up, red
         }
+        info_done(j);
       }
-      b = nb;
-      tok = ntok;
-      tile = ntile;
-      visible = nvisible;
-      tiles = ntiles;
-      seq = nseq;
-      rows_seen = visible - tile * kRows;
-      gone_now = gone;
-    }
-    if (*s_abort && warp == 0) {
-      // a wait ran out: products in flight end before tensor memory is freed (one
-      // more commit behind them, on a barrier of its own)
-      uint64_t* bar_end = reinterpret_cast<uint64_t*>(sm + kOffMisc + 80);
-      if (lane == 0) {
-        tc::mbar_init(bar_end, 1);
-        tc::fence_mbar_init();
-        tc::mma_commit(bar_end);
-        int never = 0;
-        tc::mbar_wait_bounded(bar_end, 0, &never, &g_paged_attn_error, 100000000ull);
-      }
-      __syncwarp();
     }
   }
   tc::tc_fence_before();
@@ -607,6 +839,7 @@ int64_t row[4];
   if (warp == 0) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kTmemCols);
+    if (lane == 0 && sh.abort) record_error(&g_paged_attn_error, CSA2_ERR_TIMEOUT);
   }
 }
 
@@ -646,7 +879,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(Args a, i
     if (tid < 32) {
       // the parts: the first one, then the CTAs up to cta1 that have tiles
       int n = 0;
-      float M = kNoRef;
+      float M = -INFINITY;
       for (int c0 = pl.cta0; c0 <= pl.cta1; c0 += 32) {
         const int c = c0 + lane;
         const bool has = c <= pl.cta1 && (c == pl.cta0 || pl.tiles * c / G < pl.tiles * (c + 1) / G);
@@ -734,6 +967,19 @@ int csa2_read_and_clear_paged_attn_error(cudaStream_t s) {
   return v;
 }
 
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
 static constexpr int kMaxCtas = 1024;  // the joining kernel's tables
 
 static int paged_attn_ctas() {
@@ -777,6 +1023,9 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
     return CSA2_ERR_ALIGNMENT;
   if (n_tokens == 0 || B == 0) return CSA2_OK;
   const int G = paged_attn_ctas();
+  // a CTA counts its tiles in 32 bits
+  if ((int64_t)n_tokens * ((a.pages.capacity() + pattn::kRows) / pattn::kRows) / G >= 0x7FFFFFFFLL)
+    return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (!workspace || !csa2_aligned(workspace, 256) ||
       workspace_bytes < csa2_paged_attn_workspace_size(n_tokens, B))
     return CSA2_ERR_WORKSPACE;
@@ -796,10 +1045,25 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   a.part_o = (float*)ws;
   a.part_ml = (float2*)(ws + part_o_bytes(G));
   a.lists = (pattn::PartList*)(ws + part_o_bytes(G) + part_ml_bytes(G));
+  auto encode = tensor_map_encoder();
+  if (!encode) return CSA2_ERR_CUDA;
+  // the pool's codes, in boxes of one group's 64 bytes of a run of rows (an empty
+  // pool has nothing to copy: the map then only has to be valid)
+  const int64_t pool = n_pages << a.pages.shift;
+  CUtensorMap rows_map;
+  cuuint64_t dims[2] = {(cuuint64_t)kKvBytes, (cuuint64_t)(pool > 0 ? pool : 1)};
+  cuuint64_t strides[1] = {(cuuint64_t)kKvBytes};
+  cuuint32_t box[2] = {64, (cuuint32_t)(page_size < pattn::kRows ? page_size : pattn::kRows)};
+  cuuint32_t estr[2] = {1, 1};
+  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)kv_data, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return CSA2_ERR_CUDA;
   static Csa2PerDeviceOnce optin;
   if (csa2_smem_optin((const void*)pattn::paged_attn_kernel, pattn::kSmemBytes, optin) != CSA2_OK) return CSA2_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  CSA2_LAUNCH_PDL(pattn::paged_attn_kernel, dim3((unsigned)G), dim3(pattn::kThreads), (size_t)pattn::kSmemBytes, s, a);
+  CSA2_LAUNCH_PDL(pattn::paged_attn_kernel, dim3((unsigned)G), dim3(pattn::kThreads), (size_t)pattn::kSmemBytes, s,
+                  rows_map, a);
   CSA2_LAUNCH_PDL(pattn::paged_attn_join_kernel, dim3((unsigned)(2 * G)), dim3(pattn::kJoinThreads), (size_t)0, s, a,
                   (int32_t)G);
   return CSA2_OK;
