@@ -54,7 +54,7 @@ constexpr int kSoftWarps = 8, kLoadWarp = 8, kSWarp = 16, kOWarp = 17, kWalkWarp
 constexpr int kThreads = 640;
 constexpr int kWarps = kThreads / 32;
 // Registers: 640 threads start with 96 each (61,440 in all).
-constexpr int kRegsSoft = 112, kRegsLoad = 112, kRegsIssue = 32;
+constexpr int kRegsSoft = 112, kRegsLoad = 104, kRegsIssue = 48;
 static_assert(256 * kRegsSoft + 256 * kRegsLoad + 128 * kRegsIssue <= kThreads * 96, "register split");
 constexpr int kRows = 128;
 constexpr int kPlaces = 3;                // rings of 128-channel groups of R, in tensor and in shared memory
@@ -381,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t j = 0; all(j < n_run); ++j) {
         if (all(info_of(j).at == 0 || j == 0)) wait(&sh.q, tokens++);
         if (all(j > 0)) wait(&sh.s_read, (uint32_t)(j - 1));
+        if (all(sh.abort != 0)) break;
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {  // channels 128 g ..
           wait(sh.full + place, use);
           tc::tc_fence_after();
-          if (all(sh.abort != 0)) break;
           const uint32_t at = tmem + kColA + 64u * place;
           const uint64_t bd = tc::smem_desc(q_lo + (uint32_t)(2 * g * kBlkQ), 0, 1024, tc::kSwizzle128B);
 #pragma unroll
@@ -394,10 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                bd + (uint64_t)((k >> 2) * (kBlkQ >> 4) + (k & 3) * 2), idesc,
                                k ? 1u : (uint32_t)(g != 0));
           tc::mma_commit_one(elected, sh.empty + place);
-          if (all(++place == kPlaces)) {
-            place = 0;
-            ++use;
-          }
+          place = place + 1 == kPlaces ? 0 : place + 1;
+          use += place == 0 ? 1u : 0u;
         }
         tc::mma_commit_one(elected, &sh.s);
         info_done(j);
@@ -410,11 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t j = 0; all(j < n_run); ++j) {
         const uint32_t more = j > 0 && info_of(j).at != 0 ? 1u : 0u;  // 0: O^T starts anew
         wait(&sh.p, (uint32_t)j);
+        if (all(sh.abort != 0)) break;
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {  // 128 channels
           wait(sh.r_full + place, use);
           tc::tc_fence_after();
-          if (all(sh.abort != 0)) break;
           const uint64_t ad = tc::smem_desc(r_lo + place * (uint32_t)(2 * kBlkR), kBlkR, 1024, tc::kSwizzle128B);
           const uint64_t bd = tc::smem_desc(p_lo, 0, 1024, tc::kSwizzle128B);
 #pragma unroll
@@ -422,10 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mma_f16_one(elected, tmem + kColO + 64u * (uint32_t)mb, ad + (uint64_t)((k * 16 * 128) >> 4),
                             bd + (uint64_t)(((k >> 2) * kBlkP + (k & 3) * 32) >> 4), idesc, k ? 1u : more);
           tc::mma_commit_one(elected, sh.r_empty + place);
-          if (all(++place == kPlaces)) {
-            place = 0;
-            ++use;
-          }
+          place = place + 1 == kPlaces ? 0 : place + 1;
+          use += place == 0 ? 1u : 0u;
         }
         tc::mma_commit_one(elected, &sh.o);
         info_done(j);
