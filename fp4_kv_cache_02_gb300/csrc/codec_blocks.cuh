@@ -56,6 +56,20 @@ __device__ __forceinline__ void encode_mxfp4_block(const uint32_t (&w)[16], uint
   e8m0 = (uint8_t)(X + 127);
 }
 
+// x / d rounded to nearest, from r = 1 / d rounded to nearest: the product x r
+// is corrected once by its exact remainder (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990). The
+// remainder is taken as q d - x, which keeps the sign of a zero. It is exact
+// while x is finite, the quotient does not overflow and neither is near the
+// subnormals; further down the quotient is off by some last bits, far below
+// the lowest border of the codes made of it. Run over every finite fp32 x with
+// d = 6 and every E4M3 d that a block with x in it can have, the codes equal
+// those of __fdiv_rn.
+__device__ __forceinline__ float div_by(float x, float d, float r) {
+  const float q = x * r;
+  return __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);
+}
+
 // One main-KV block: 16 values -> 8 bytes of E2M1 pairs and the E4M3 scale. The
 // scale is amax / 6 rounded to nearest-even E4M3 (6 is the largest E2M1
 // magnitude); each value is divided by the decoded scale and rounded to
@@ -63,19 +77,28 @@ __device__ __forceinline__ void encode_mxfp4_block(const uint32_t (&w)[16], uint
 __device__ __forceinline__ void encode_kv_fp4_values(const float (&f)[16], uint2& data, uint8_t& scale) {
   float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-  const float q = __fdiv_rn(amax, 6.0f);
+  for (int i = 0; i < 8; ++i) amax = max_abs3(amax, f[2 * i], f[2 * i + 1]);
+  const bool finite = amax <= 3.402823466e38f;  // (an infinity has no remainder)
+  const float q = finite ? div_by(amax, 6.0f, 1.0f / 6.0f) : amax;
   const uint32_t sc = cvt_e4m3x2(q, 0.0f) & 0xFFu;
   const float s = e4m3_to_f32(sc);
-  uint32_t out0 = 0, out1 = 0;
+  uint32_t out[2] = {0, 0};
   if (s != 0.0f) {
+    const float r = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      out0 |= cvt_e2m1x2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s)) << (8 * i);
-      out1 |= cvt_e2m1x2(__fdiv_rn(f[8 + 2 * i], s), __fdiv_rn(f[8 + 2 * i + 1], s)) << (8 * i);
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+      if (finite) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = div_by(f[8 * h + i], s, r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(f[8 * h + i], s);
+      }
+      out[h] = cvt_e2m1x8(v);
     }
   }
-  data = make_uint2(out0, out1);
+  data = make_uint2(out[0], out[1]);
   scale = (uint8_t)sc;
 }
 
