@@ -19,6 +19,8 @@ __device__ int g_index_error = 0;
 
 }  // namespace csa2
 
+#include <numeric>
+
 #include "index_score_tc.cuh"
 #include "prefill_score_tc.cuh"
 
@@ -100,7 +102,7 @@ int csa2_launch_index_score_tc(const uint8_t* q_data, const uint8_t* q_e8m0, con
   scan_tc::Params prm{ik_data, positions, q_data, q_e8m0, w, ik_scale, cap, n_visible, n_pos, scores, (int32_t)per,
                       hist, positions ? nullptr : bmax, early_reads, (const uint16_t*)q_bf16,
                       positions ? nullptr : tile_ctr, tile_ctr_stride, scan_tc::kStages, 2,
-                      positions ? nullptr : tile_done, PageTable{}};
+                      positions ? nullptr : tile_done, PageTable{}, B, 1};
   CSA2_LAUNCH_PDL(scan_tc::index_score_tc_kernel<false>, dim3((unsigned)B, (unsigned)chunks), dim3(scan_tc::kThreads),
                   (size_t)scan_tc::kSmemBytes, stream, map, prm);
   return CSA2_OK;
@@ -139,19 +141,24 @@ extern "C" int csa2_paged_index_score(const uint8_t* q_data, const uint8_t* q_e8
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return CSA2_ERR_CUDA;
   const int64_t tiles = (n_pos + scan_tc::kTileRows - 1) / scan_tc::kTileRows;
-  int64_t chunks = 3LL * device_sm_count() / B;
-  if (chunks < 1) chunks = 1;
-  if (chunks > tiles) chunks = tiles;
-  const int64_t per = (tiles + chunks - 1) / chunks;
-  chunks = (tiles + per - 1) / per;
-  if (chunks > 65535) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  // one wave of 3 CTAs per SM; or a CTA for each tile there can be, or for each
+  // sequence, where that is less or more
+  const int64_t wave = 3LL * device_sm_count();
+  int64_t ctas = wave, spread = 0;
+  if (tiles * B <= wave) {
+    ctas = tiles * B;
+  } else if (B >= wave) {
+    ctas = B;
+  } else {
+    for (spread = wave * 5 / 8 + 1; std::gcd(spread, wave) != 1;) ++spread;
+  }
   static Csa2PerDeviceOnce optin;
   if (csa2_smem_optin((const void*)scan_tc::index_score_tc_kernel<true>, scan_tc::kSmemBytes, optin) != CSA2_OK)
     return CSA2_ERR_CUDA;
   scan_tc::Params prm{ik_data, nullptr, q_data, q_e8m0, w, ik_scale, pages.capacity(), n_visible, n_pos, scores,
-                      (int32_t)per, nullptr, nullptr, 0, nullptr, tile_counters, 2, scan_tc::kStages, 2,
-                      tile_counters ? tile_counters + 1 : nullptr, pages};
-  CSA2_LAUNCH_PDL(scan_tc::index_score_tc_kernel<true>, dim3((unsigned)B, (unsigned)chunks), dim3(scan_tc::kThreads),
+                      0, nullptr, nullptr, 0, nullptr, tile_counters, 2, 0, 0,
+                      tile_counters ? tile_counters + 1 : nullptr, pages, B, (int32_t)spread};
+  CSA2_LAUNCH_PDL(scan_tc::index_score_tc_kernel<true>, dim3((unsigned)ctas), dim3(scan_tc::kThreads),
                   (size_t)scan_tc::kSmemBytes, (cudaStream_t)stream, map, prm);
   return CSA2_OK;
 }

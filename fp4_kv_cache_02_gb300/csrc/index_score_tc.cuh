@@ -96,7 +96,63 @@ struct Params {
   // paged mode: ik_data / ik_scale are the pool's planes, entries found by the
   // table; a tile is one piece of a page, or several whole small pages
   PageTable pages;
+  int32_t B;
+  int32_t spread;  // 0, or prime to the grid's size (paged_share)
 };
+
+// Over pages: this CTA's sequence, its place among the sequence's CTAs and their
+// number. Where CTAs have several tiles each (p.spread > 0), each sequence has
+// one CTA and the grid's others go to the sequences in proportion to their
+// tiles, a tile that only has -inf written to it counting an eighth (512 bytes
+// against 9,200): 23.5 us over 32 sequences of 21,845 to 65,536 entries, 27.0
+// with equal shares. Every warp works it out for itself; false for the few CTAs
+// that the rounding leaves over. The CTAs of a sequence lie p.spread apart, so
+// that each has its part of the SMs with two CTAs and of those with three (30.0
+// us over 32 equal sequences; 31.8 side by side). Where the sequences' longest
+// has a CTA a tile, or there are no CTAs to spare, the shares are equal (5
+// sequences of at most 9,001 entries: 6.5 us, and 8.6 with the work above).
+__device__ __forceinline__ bool paged_share(const Params& p, int lane, int& b, int& chunk, int& n_chunks) {
+  const int B = p.B;
+  if (p.spread == 0) {
+    b = (int)(blockIdx.x % (uint32_t)B), chunk = (int)(blockIdx.x / (uint32_t)B), n_chunks = (int)(gridDim.x / (uint32_t)B);
+    return true;
+  }
+  const int spare = (int)gridDim.x - B;
+  // (a grid with CTAs to spare is one wave: products of its indices are small)
+  const int x = (int)(blockIdx.x * (uint32_t)p.spread % gridDim.x);
+  const float all = (float)((p.n_pos + kTileRows - 1) / kTileRows);
+  const auto weight = [&](int i) -> float {
+    const int nv = i < B ? p.n_visible[i] : 0;
+    return 7.0f * fminf((float)((nv < 0 ? 0 : nv) / kTileRows + 1), all) + all;
+  };
+  float total = 0.0f;
+  for (int i = lane; i < B; i += 32) total += weight(i);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  // rounded down by more than the sums' roundings: the shares stay within spare
+  const float scale = (float)spare / total * (1.0f - 1e-4f);
+  int first = 0;  // CTAs of the sequences before this group of 32
+  for (int base = 0; base < B; base += 32) {
+    const int i = base + lane;
+    const int own = i < B ? 1 + (int)(weight(i) * scale) : 0;
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t mine = __ballot_sync(0xffffffffu, x < first + upto);
+    if (mine) {
+      const int l = __ffs(mine) - 1;
+      b = base + l;
+      n_chunks = __shfl_sync(0xffffffffu, own, l);
+      chunk = x - (first + __shfl_sync(0xffffffffu, upto, l) - n_chunks);
+      return true;
+    }
+    first += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
 
 template <bool kPaged>
 __global__ void __launch_bounds__(kThreads, 3)
@@ -131,24 +187,28 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // grid (sequences, chunks): consecutive CTAs belong to different sequences,
-  // so each sequence's CTAs spread over the SMs of both dies
-  const int b = blockIdx.x;
-  const int chunk = blockIdx.y, n_chunks = gridDim.y;
+  // so each sequence's CTAs spread over the SMs of both dies. Over pages the
+  // grid is flat, and sequences have CTAs in proportion to their tiles.
+  int b = blockIdx.x, chunk = blockIdx.y, n_chunks = gridDim.y;
+  if constexpr (kPaged) {
+    if (!paged_share(p, lane, b, chunk, n_chunks)) return;
+  }
   const int64_t n_tiles_all = (p.n_pos + kTileRows - 1) / kTileRows;
   int64_t nv = (int64_t)p.n_visible[b];
   // positions mode: a listed position is scored when it is below n_visible
   // (and the capacity); dense mode: entries 0..nv-1 of the list
   const int64_t nv_pos = nv < 0 ? 0 : (nv > p.cap ? p.cap : nv);
   nv = nv < 0 ? 0 : (nv > p.n_pos ? p.n_pos : nv);
-  const int64_t t_begin = (int64_t)chunk * p.tiles_per_cta;
-  int64_t t_end_all = t_begin + p.tiles_per_cta;
+  // claimed mode: tiles 0 .. t_vis-1 of the sequence hold visible entries
+  const int64_t t_vis_ = (nv + kTileRows - 1) / kTileRows;
+  const int32_t t_vis = (int32_t)(t_vis_ < n_tiles_all ? t_vis_ : n_tiles_all);
+  const int64_t per = kPaged ? (t_vis + n_chunks - 1) / n_chunks : p.tiles_per_cta;
+  const int64_t t_begin = (int64_t)chunk * per;
+  int64_t t_end_all = t_begin + per;
   if (t_end_all > n_tiles_all) t_end_all = n_tiles_all;
   int64_t t_end = pos_mode ? t_end_all : (nv + kTileRows - 1) / kTileRows;
   if (t_end > t_end_all) t_end = t_end_all;
   const int n_tiles = t_end > t_begin ? (int)(t_end - t_begin) : 0;
-  // claimed mode: tiles 0 .. t_vis-1 of the sequence hold visible entries
-  const int64_t t_vis_ = (nv + kTileRows - 1) / kTileRows;
-  const int32_t t_vis = (int32_t)(t_vis_ < n_tiles_all ? t_vis_ : n_tiles_all);
 
   // ---- set-up: barriers, the q operand (B) and its scales, tensor memory ----
   if (threadIdx.x == 0) {
@@ -241,6 +301,105 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     tc::cp_async_wait_all();  // nothing of this lane is in flight when the CTA ends
     __syncwarp();
+  } else if (kPaged && warp == kProducerWarp) {
+    // ---- producer over pages: the whole warp, two tiles at a time ----
+    // A tile's entries are one run of a page, or up to 8 whole pages; lane
+    // 8g + j has run j of tile g of the pair. While a pair's copies are issued,
+    // the next pair's pages are being looked up and the pair after that is being
+    // claimed: in turn the three would take two round trips to L2 and the wait
+    // for a stage for each pair (50.5 us over 32 sequences of 65,536 entries,
+    // against 31.5 as here with the same ranges). Pages past the visible entries are not looked up; what a
+    // missing page leaves in the stage is never scored (s_mask).
+    const int run_shift = p.pages.shift < 7 ? p.pages.shift : 7;
+    const int run = 1 << run_shift;
+    const int g = lane >> 3, j = lane & 7;
+    const int32_t* places = p.pages.table + (int64_t)b * p.pages.max_pages;
+    // Seven eighths of the tiles are fixed ranges, the last eighth is claimed:
+    // that evens out the CTAs' different shares of the bandwidth (28.8 us over 32 sequences of
+    // 65,536 entries; 29.4
+    // with three quarters fixed, 31.4 with six tiles each, 30.5 with all fixed).
+    const int64_t part = (int64_t)t_vis * 7 / 8 / n_chunks;
+    const int64_t own = !claimed || n_chunks == 1 ? per : part > 0 ? part : 1;
+    const int64_t fixed0 = (int64_t)chunk * own;
+    int64_t fixed = fixed0;
+    const int64_t fixed_end = fixed0 + own < t_vis ? fixed0 + own : t_vis;
+    const int64_t claims = (int64_t)n_chunks * own;  // the first tile that is claimed
+    // first tile of the next pair, in lane 0; past the end once there is none
+    const auto next = [&]() -> int32_t {
+      int32_t t = 0x7FFFFFFF;
+      if (fixed < fixed_end) {
+        t = (int32_t)fixed;
+        fixed += 2;
+      } else if (claimed && claims < t_vis && lane == 0) {
+        // (the caller cleared the counter; a negative one would index before the table)
+        const int32_t c = atomicAdd(p.tile_ctr + (int64_t)b * p.tile_ctr_stride, 2);
+        if (c < 0)
+          record_error(&g_index_error, CSA2_ERR_DEVICE);
+        else
+          t = (int32_t)min((int64_t)0x7FFFFFFF, claims + c);
+      }
+      return t;
+    };
+    // (a pair of the fixed range ends with the range: the tile behind it is another CTA's)
+    const auto end_of = [&](int32_t t) { return t < fixed_end && t >= fixed0 ? fixed_end : claimed ? (int64_t)t_vis : 0; };
+    const auto row_of = [&](int32_t t) { return ((int64_t)t + g) * kTileRows + (int64_t)j * run; };
+    const auto wanted = [&](int32_t t) {
+      return g < 2 && j < (kTileRows >> run_shift) && (int64_t)t + g < end_of(t) && row_of(t) < nv;
+    };
+    const auto look_up = [&](int32_t t) { return wanted(t) ? places[row_of(t) >> p.pages.shift] : -1; };
+    int issued = 0;
+    bool ok = true;
+    int32_t t0 = __shfl_sync(0xffffffffu, next(), 0);
+    int32_t page0 = look_up(t0);
+    int32_t ahead = next();
+    while (t0 < end_of(t0)) {
+      const int32_t t1 = __shfl_sync(0xffffffffu, ahead, 0);
+      const int32_t page1 = look_up(t1);
+      if (t1 < end_of(t1)) ahead = next();
+      const bool there = page0 >= 0 && page0 < p.pages.n_pages;
+      if (wanted(t0) && !there) record_error(&g_index_error, CSA2_ERR_DEVICE);
+      const uint32_t masks = __ballot_sync(0xffffffffu, there && wanted(t0));
+      for (int k = 0; k < 2 && (int64_t)t0 + k < end_of(t0); ++k) {
+        const int s = issued % kStages;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&empty[s], ((uint32_t)(issued / kStages) & 1u) ^ 1u,
+                                                           s_abort, &g_index_error));
+        if (!ok) break;
+        const uint32_t mask = (masks >> (8 * k)) & 0xFFu;
+        if (lane == 0) {
+          if (claimed) s_ring[issued % kRing] = t0 + k;
+          s_mask[issued % kRing] = mask;
+          tc::mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(mask) * (uint32_t)run * (kIkBytes + kIkScales));
+        }
+        __syncwarp();
+        if (g == k && ((mask >> j) & 1u)) {
+          const int64_t prow = ((int64_t)page0 << p.pages.shift) + (row_of(t0) & (p.pages.page_size() - 1));
+          tc::tma_load_3d(sA + s * kTileBytes + j * run * kIkBytes, &tmap_ik, 0, (int32_t)prow, 0, &full[s]);
+          tc::bulk_load(sSfRaw + s * kSfBytes + j * run * kIkScales, p.ik_scale + prow * kIkScales,
+                        (uint32_t)(run * kIkScales), &full[s]);
+        }
+        __syncwarp();
+        ++issued;
+      }
+      if (!ok) break;
+      t0 = t1;
+      page0 = page1;
+    }
+    if (ok && claimed) {
+      // the end of the stream: one more stage, no bytes, tile index -1
+      const int s = issued % kStages;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&empty[s], ((uint32_t)(issued / kStages) & 1u) ^ 1u, s_abort,
+                                                         &g_index_error));
+      if (ok && lane == 0) {
+        s_ring[issued % kRing] = -1;
+        tc::mbar_arrive(&full[s]);
+      }
+    }
+    if (*s_abort) {
+      // let copies already in flight land before the CTA's memory goes away
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        tc::mbar_wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1u, s_abort, &g_index_error, 100000000ull);
+    }
+    __syncwarp();
   } else if (warp == kProducerWarp) {
     // ---- TMA producer ----
     if (lane == 0) {
@@ -251,38 +410,6 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (!tc::mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, &g_index_error)) return false;
         const int64_t row0 = tile * kTileRows;
         if (claimed) s_ring[i % kRing] = (int32_t)tile;
-        if constexpr (kPaged) {
-          // the tile's entries: one run of a page, or up to 8 whole pages. Pages
-          // past the visible entries are not looked up; what a missing page
-          // leaves in the stage is never scored (s_mask)
-          const int run_shift = p.pages.shift < 7 ? p.pages.shift : 7;
-          const int run = 1 << run_shift;
-          const int n_runs = kTileRows >> run_shift;
-          const int32_t* places = p.pages.table + (int64_t)b * p.pages.max_pages;
-          int32_t page[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            page[j] = j < n_runs && row0 + (int64_t)j * run < nv ? places[(row0 + (int64_t)j * run) >> p.pages.shift]
-                                                                 : INT32_MIN;
-          uint32_t mask = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (page[j] >= 0 && page[j] < p.pages.n_pages) mask |= 1u << j;
-            else if (page[j] != INT32_MIN || (j < n_runs && row0 + (int64_t)j * run < nv))
-              record_error(&g_index_error, CSA2_ERR_DEVICE);
-          }
-          s_mask[i % kRing] = mask;
-          tc::mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(mask) * (uint32_t)run * (kIkBytes + kIkScales));
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (!((mask >> j) & 1u)) continue;
-            const int64_t prow = ((int64_t)page[j] << p.pages.shift) + (row0 & (p.pages.page_size() - 1));
-            tc::tma_load_3d(sA + s * kTileBytes + j * run * kIkBytes, &tmap_ik, 0, (int32_t)prow, 0, &full[s]);
-            tc::bulk_load(sSfRaw + s * kSfBytes + j * run * kIkScales, p.ik_scale + prow * kIkScales,
-                          (uint32_t)(run * kIkScales), &full[s]);
-          }
-          return true;
-        }
         tc::mbar_arrive_expect_tx(&full[s], kTileBytes + kSfBytes);
         tc::tma_load_3d(sA + s * kTileBytes, &tmap_ik, 0, (int32_t)row0, b, &full[s]);
         tc::bulk_load(sSfRaw + s * kSfBytes, p.ik_scale + ((int64_t)b * p.cap + row0) * kIkScales, kSfBytes,
@@ -428,12 +555,28 @@ __global__ void __launch_bounds__(kThreads, 3)
       if (with_hist && valid && score_is_candidate(sc))
         atomicAdd(&s_hist[score_key(sc) >> (32 - kTopkHistBits)], 1u);
     }
+    if constexpr (kPaged) {
+      // what lies behind the visible tiles: one run of it to each CTA of the
+      // sequence, in 16-byte stores from the first boundary on
+      const int64_t rest0 = (int64_t)t_vis * kTileRows, rest = p.n_pos - rest0;
+      if (rest > 0) {
+        const int64_t each = (rest + n_chunks - 1) / n_chunks;
+        float* at = out + rest0 + each * chunk;
+        const int64_t left = rest - each * chunk, n = left < each ? left : each;
+        const int64_t lead = min(n, (int64_t)(((16 - (reinterpret_cast<uintptr_t>(at) & 15)) & 15) / 4));
+        const int64_t quads = n > lead ? (n - lead) / 4 : 0;
+        const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        for (int64_t i = threadIdx.x; i < lead; i += 128) at[i] = -INFINITY;
+        for (int64_t i = threadIdx.x; i < quads; i += 128) reinterpret_cast<float4*>(at + lead)[i] = none;
+        for (int64_t i = lead + 4 * quads + threadIdx.x; i < n; i += 128) at[i] = -INFINITY;
+      }
+    }
     // tiles past the visible entries: this CTA's range, or in claimed mode
     // every n_chunks-th tile from t_vis + chunk
     const int64_t fill_lo = claimed ? t_vis + (int64_t)chunk : (t_begin > t_end ? t_begin : t_end);
     const int64_t fill_hi = claimed ? n_tiles_all : t_end_all;
     const int64_t fill_step = claimed ? (int64_t)n_chunks : 1;
-    for (int64_t t = fill_lo; t < fill_hi; t += fill_step) {
+    for (int64_t t = fill_lo; !kPaged && t < fill_hi; t += fill_step) {
       const int64_t lo = t * kTileRows;
       const int64_t hi = lo + kTileRows < p.n_pos ? lo + kTileRows : p.n_pos;
       for (int64_t pos = lo + threadIdx.x; pos < hi; pos += 128) out[pos] = -INFINITY;

@@ -342,6 +342,46 @@ def test_scores_equal_the_flat_scan(csa2, page, claimed):
     assert csa2.csa2_get_last_error() == 0
 
 
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("claimed", [False, True])
+@pytest.mark.parametrize("lens,n_pos", [
+    ([0, 1, 12000, 11999, 128, 4097, 9000, 12000, 640], 12000),  # CTAs in proportion to lengths
+    ([0, 5, 30001], 40003),  # one long sequence, and room behind it
+    ([200 + 3 * (i % 61) for i in range(500)], 391),  # more sequences than CTAs in a wave
+    ([3000, 0, 9000], 2777),  # more entries than scores are asked for
+])
+def test_scores_of_many_tiles_equal_the_flat_scan(csa2, page, claimed, lens, n_pos):
+    c = Cache(csa2, lens, page, 26 + page)
+    q, s, w = queries(csa2, gen(27), len(lens))
+    flat = c.flat_planes()
+    cap = flat[2].shape[1]
+    want = torch.full((len(lens), n_pos), -float("inf"), device="cuda")
+    least = torch.empty(len(lens), min(n_pos, cap), device="cuda")
+    csa2.csa2_index_score(q, s, w, flat[2], flat[3], c.n_visible, least)
+    want[:, :least.shape[1]] = least
+    places = -(-n_pos // page)
+    table = torch.full((len(lens), max(places, c.table.shape[1])), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    counters = torch.zeros(2 * len(lens), dtype=torch.int32, device="cuda") if claimed else None
+    for _ in range(2):
+        got = torch.full_like(want, 5.0)
+        csa2.csa2_paged_index_score(q, s, w, c.ik_data, c.ik_scale, table, c.n_visible, got, tile_counters=counters)
+        assert torch.equal(got, want)
+        assert counters is None or not counters.any()
+    assert csa2.csa2_get_last_error() == 0
+
+
+def test_scores_with_a_negative_counter(csa2):
+    """A counter that was not cleared is reported, and no page is looked up before the table."""
+    c = Cache(csa2, [9000] * 8, 64, 28)
+    q, s, w = queries(csa2, gen(29), 8)
+    counters = torch.zeros(16, dtype=torch.int32, device="cuda")
+    counters[0::2] = -(1 << 30)
+    got = torch.empty(8, 9000, device="cuda")
+    csa2.csa2_paged_index_score(q, s, w, c.ik_data, c.ik_scale, c.table, c.n_visible, got, tile_counters=counters)
+    assert csa2.csa2_get_last_error() == DEVICE_ERROR
+
+
 def test_scores_against_64_bits(csa2):
     lens = [300, 41]
     c = Cache(csa2, lens, 32, 22)
