@@ -125,13 +125,12 @@ def lib():
 # ---- marshalling helpers -----------------------------------------------------
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    # (the handle without the Stream object: 0.4 us instead of 3)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _req(t, dtype, name, allow_none=False):
@@ -459,61 +458,83 @@ def csa2_sparse_attn_prefill_replay(q, kv_data, kv_scale, idx, swa, n_swa, repla
 # Planes are [n_pages, page_size, width]; entry e of sequence b is row
 # e % page_size of page page_table[b, e // page_size].
 
-def _shape(ok, what):
-    if not ok:
-        raise ValueError(what)
+# (A decode step makes several of these calls; their checks are written to cost
+# little, and say what is wrong only when something is.)
+
+def _refuse(t, dtype, name, dev):
+    _req(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, the call's device is cuda:{dev}")
 
 
-def _same_device(first, *others):
-    """Every tensor of a call lives on the first one's device, and that is the
-    current device (the kernels are launched there)."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
+def _take(t, dtype, name, dev):
+    """The address of a contiguous tensor of this type on the call's device."""
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, name, dev)
 
 
-def _pool(planes, widths, page_table, n_visible):
-    """(n_pages, page_size, B, max_pages) of the pool's planes and the table."""
-    first = planes[0]
-    for t, (width, name) in zip(planes, widths):
-        _req(t, torch.uint8, name)
-        _shape(t.dim() == 3 and t.shape[2] == width and t.shape[:2] == first.shape[:2],
-               f"{name} must be [n_pages, page_size, {width}] like the other planes")
-    _req(page_table, torch.int32, "page_table")
-    _req(n_visible, torch.int32, "n_visible")
-    _shape(page_table.dim() == 2 and n_visible.shape == page_table.shape[:1],
-           "page_table must be [B, max_pages] and n_visible [B]")
-    return first.shape[0], first.shape[1], page_table.shape[0], page_table.shape[1]
+def _device(t, name):
+    """The device of a call: its first tensor's, which has to be the current one
+    (the kernels are launched there)."""
+    _req(t, t.dtype if t is not None else None, name)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _runs(cu, B, name):
-    if cu is not None:
-        _req(cu, torch.int32, name)
-        _shape(cu.shape == (B + 1,), f"{name} must be [B + 1]")
+def _pool(dev, planes, page_table, n_visible):
+    """(addresses of the planes, n_pages, page_size, table, B, max_pages, counts)."""
+    at = []
+    pages = None
+    for t, width, name in planes:
+        at.append(_take(t, torch.uint8, name, dev))
+        shape = t.shape
+        if pages is None and len(shape) == 3:
+            pages = shape[0], shape[1]
+        if pages is None or shape != (*pages, width):
+            raise ValueError(f"{name} must be [n_pages, page_size, {width}] like the other planes")
+    table = _take(page_table, torch.int32, "page_table", dev)
+    counts = _take(n_visible, torch.int32, "n_visible", dev)
+    shape = page_table.shape
+    if len(shape) != 2 or n_visible.shape != (shape[0],):
+        raise ValueError("page_table must be [B, max_pages] and n_visible [B]")
+    return at, pages[0], pages[1], table, shape[0], shape[1], counts
 
 
-def _rope_table(rope):
-    _req(rope, torch.float32, "rope")
-    _shape(rope.dim() == 3 and rope.shape[2] == 2, "rope must be [n_rope, rope_dim / 2, 2]")
-    return rope.shape[0], 2 * rope.shape[1]
+def _shaped(t, dtype, shape, name, dev):
+    at = _take(t, dtype, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return at
+
+
+def _optional(t, dtype, shape, name, dev):
+    return None if t is None else _shaped(t, dtype, shape, name, dev)
+
+
+def _rope_table(rope, dev):
+    at = _take(rope, torch.float32, "rope", dev)
+    shape = rope.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise ValueError("rope must be [n_rope, rope_dim / 2, 2]")
+    return at, shape[0], 2 * shape[1]
 
 
 def csa2_rope(x, rope, positions, out, interleaved=False, inverse=False, stream=None):
     """x [n_tokens, heads, dim] bf16 -> out (may be x): the last rope_dim
     channels turned by rope [n_rope, rope_dim / 2, 2] fp32 (cos, sin) at
     positions [n_tokens] int32 (None: row t is at position t)."""
-    _req(x, torch.bfloat16, "x"); _req(out, torch.bfloat16, "out")
-    _req(positions, torch.int32, "positions", allow_none=True)
-    _shape(x.dim() == 3 and out.shape == x.shape, "x must be [n_tokens, heads, dim], out like it")
-    n_rope, rope_dim = _rope_table(rope)
-    n, heads, dim = x.shape
-    _shape(positions is None or positions.shape == (n,), "positions must be [n_tokens]")
-    _same_device(x, rope, positions, out)
-    _call("csa2_rope", _p(x), n, heads, dim, _p(rope), n_rope, rope_dim, _p(positions), int(bool(interleaved)),
-          int(bool(inverse)), _p(out), _s(stream))
+    dev = _device(x, "x")
+    x_at, out_at = _take(x, torch.bfloat16, "x", dev), _take(out, torch.bfloat16, "out", dev)
+    shape = x.shape
+    if len(shape) != 3 or out.shape != shape:
+        raise ValueError("x must be [n_tokens, heads, dim], out like it")
+    rope_at, n_rope, rope_dim = _rope_table(rope, dev)
+    n, heads, dim = shape
+    _call("csa2_rope", x_at, n, heads, dim, rope_at, n_rope, rope_dim,
+          _optional(positions, torch.int32, (n,), "positions", dev), 1 if interleaved else 0, 1 if inverse else 0, out_at,
+          _s(stream))
 
 
 def csa2_paged_kv_append(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_table, n_visible, n_visible_out=None,
@@ -522,25 +543,19 @@ def csa2_paged_kv_append(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_tabl
     rope table is given) -> entries n_visible[b], n_visible[b] + 1, ... of each
     sequence; cu_tokens [B + 1] int32 gives each sequence its rows (None: the
     same number each); n_visible_out may be n_visible."""
-    _req(kv, torch.bfloat16, "kv"); _req(ik, torch.bfloat16, "ik")
-    _shape(kv.dim() == 2 and kv.shape[1] == HEAD_DIM and ik.shape == (kv.shape[0], IDX_DIM),
-           "kv must be [n_tokens, 512] and ik [n_tokens, 128]")
-    n_pages, page, B, max_pages = _pool((kv_data, kv_scale, ik_data, ik_scale),
-                                        ((256, "kv_data"), (32, "kv_scale"), (64, "ik_data"), (4, "ik_scale")),
-                                        page_table, n_visible)
-    _req(n_visible_out, torch.int32, "n_visible_out", allow_none=True)
-    _shape(n_visible_out is None or n_visible_out.shape == (B,), "n_visible_out must be [B]")
-    _runs(cu_tokens, B, "cu_tokens")
-    n_rope = rope_dim = 0
-    if rope is not None:
-        n_rope, rope_dim = _rope_table(rope)
-    _req(positions, torch.int32, "positions", allow_none=True)
-    _shape(positions is None or positions.shape == kv.shape[:1], "positions must be [n_tokens]")
-    _same_device(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_table, n_visible, n_visible_out, cu_tokens, rope,
-                 positions)
-    _call("csa2_paged_kv_append", _p(kv), _p(ik), kv.shape[0], _p(cu_tokens), B, _p(rope), n_rope, rope_dim,
-          _p(positions), int(bool(interleaved)), _p(kv_data), _p(kv_scale), _p(ik_data), _p(ik_scale), n_pages, page,
-          _p(page_table), max_pages, _p(n_visible), _p(n_visible_out), _s(stream))
+    dev = _device(kv, "kv")
+    kv_at, ik_at = _take(kv, torch.bfloat16, "kv", dev), _take(ik, torch.bfloat16, "ik", dev)
+    n = kv.shape[0] if kv.dim() else 0
+    if kv.shape != (n, HEAD_DIM) or ik.shape != (n, IDX_DIM):
+        raise ValueError("kv must be [n_tokens, 512] and ik [n_tokens, 128]")
+    at, n_pages, page, table, B, max_pages, counts = _pool(
+        dev, ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"), (ik_scale, 4, "ik_scale")),
+        page_table, n_visible)
+    rope_at, n_rope, rope_dim = (None, 0, 0) if rope is None else _rope_table(rope, dev)
+    _call("csa2_paged_kv_append", kv_at, ik_at, n, _optional(cu_tokens, torch.int32, (B + 1,), "cu_tokens", dev), B,
+          rope_at, n_rope, rope_dim, _optional(positions, torch.int32, (n,), "positions", dev), 1 if interleaved else 0,
+          *at, n_pages, page, table, max_pages, counts,
+          _optional(n_visible_out, torch.int32, (B,), "n_visible_out", dev), _s(stream))
 
 
 def csa2_paged_index_score(q_data, q_e8m0, w, ik_data, ik_scale, page_table, n_visible, scores, tile_counters=None,
@@ -548,43 +563,49 @@ def csa2_paged_index_score(q_data, q_e8m0, w, ik_data, ik_scale, page_table, n_v
     """q_data [B, 32, 64], q_e8m0 [B, 32, 4], w [B, 32]; scores [B, n_pos] fp32
     (out); tile_counters [2 * B] int32 as in csa2_index_score_claimed (None: a
     fixed range of tiles per CTA)."""
-    _req(q_data, torch.uint8, "q_data"); _req(q_e8m0, torch.uint8, "q_e8m0"); _req(w, torch.float32, "w")
-    _req(scores, torch.float32, "scores"); _req(tile_counters, torch.int32, "tile_counters", allow_none=True)
-    n_pages, page, B, max_pages = _pool((ik_data, ik_scale), ((64, "ik_data"), (4, "ik_scale")), page_table, n_visible)
-    _shape(q_data.numel() == B * IDX_HEADS * 64 and q_e8m0.numel() == B * IDX_HEADS * 4
-           and w.numel() == B * IDX_HEADS, "q_data, q_e8m0 and w must hold B x 32 heads")
-    _shape(scores.dim() == 2 and scores.shape[0] == B, "scores must be [B, n_pos]")
-    _shape(tile_counters is None or tile_counters.numel() >= 2 * B, "tile_counters needs 2 * B int32")
-    _same_device(q_data, q_e8m0, w, ik_data, ik_scale, page_table, n_visible, scores, tile_counters)
-    _call("csa2_paged_index_score", _p(q_data), _p(q_e8m0), _p(w), B, _p(ik_data), _p(ik_scale), n_pages, page,
-          _p(page_table), max_pages, _p(n_visible), scores.shape[1], _p(scores), _p(tile_counters), _s(stream))
+    dev = _device(q_data, "q_data")
+    q_at, s_at = _take(q_data, torch.uint8, "q_data", dev), _take(q_e8m0, torch.uint8, "q_e8m0", dev)
+    w_at, out_at = _take(w, torch.float32, "w", dev), _take(scores, torch.float32, "scores", dev)
+    at, n_pages, page, table, B, max_pages, counts = _pool(
+        dev, ((ik_data, 64, "ik_data"), (ik_scale, 4, "ik_scale")), page_table, n_visible)
+    if q_data.numel() != B * IDX_HEADS * 64 or q_e8m0.numel() != B * IDX_HEADS * 4 or w.numel() != B * IDX_HEADS:
+        raise ValueError("q_data, q_e8m0 and w must hold B x 32 heads")
+    if scores.dim() != 2 or scores.shape[0] != B:
+        raise ValueError("scores must be [B, n_pos]")
+    counters = None
+    if tile_counters is not None:
+        counters = _take(tile_counters, torch.int32, "tile_counters", dev)
+        if tile_counters.numel() < 2 * B:
+            raise ValueError("tile_counters needs 2 * B int32")
+    _call("csa2_paged_index_score", q_at, s_at, w_at, B, *at, n_pages, page, table, max_pages, counts, scores.shape[1],
+          out_at, counters, _s(stream))
 
 
 def csa2_paged_sparse_attn_decode(q, kv_data, kv_scale, page_table, n_visible, idx, swa, out, workspace, out_f32=None,
                                   lse=None, sm_scale=1.0, stream=None):
     """As csa2_sparse_attn_decode, idx [B, k] naming entries of the paged
     sequences; q [B, L, 64, 512] bf16, swa [B, L, n_swa, 512] u8 or None."""
-    _req(q, torch.bfloat16, "q"); _req(idx, torch.int32, "idx"); _req(out, torch.bfloat16, "out")
-    _req(workspace, torch.uint8, "workspace"); _req(swa, torch.uint8, "swa", allow_none=True)
-    _req(out_f32, torch.float32, "out_f32", allow_none=True); _req(lse, torch.float32, "lse", allow_none=True)
-    n_pages, page, B, max_pages = _pool((kv_data, kv_scale), ((256, "kv_data"), (32, "kv_scale")), page_table,
-                                        n_visible)
-    _shape(q.dim() == 4 and q.shape[0] == B and q.shape[2:] == (HEADS, HEAD_DIM), "q must be [B, L, 64, 512]")
-    L = q.shape[1]
-    _shape(idx.dim() == 2 and idx.shape[0] == B, "idx must be [B, k]")
-    _shape(swa is None or (swa.dim() == 4 and swa.shape[:2] == (B, L) and swa.shape[3] == HEAD_DIM),
-           "swa must be [B, L, n_swa, 512]")
-    _outputs(q, out, out_f32, lse)
-    _same_device(q, kv_data, kv_scale, page_table, n_visible, idx, swa, out, workspace, out_f32, lse)
-    n_swa = swa.shape[2] if swa is not None else 0
-    _call("csa2_paged_sparse_attn_decode", _p(q), B, L, _p(kv_data), _p(kv_scale), n_pages, page, _p(page_table),
-          max_pages, _p(n_visible), _p(idx), idx.shape[1], _p(swa), n_swa, float(sm_scale), _p(out), _p(out_f32),
-          _p(lse), _p(workspace), workspace.numel(), _s(stream))
-
-
-def _outputs(q, out, out_f32, lse):
-    _shape(out.shape == q.shape and (out_f32 is None or out_f32.shape == q.shape)
-           and (lse is None or lse.shape == q.shape[:-1]), "out and out_f32 must be like q, lse without its last axis")
+    dev = _device(q, "q")
+    q_at, idx_at = _take(q, torch.bfloat16, "q", dev), _take(idx, torch.int32, "idx", dev)
+    ws_at = _take(workspace, torch.uint8, "workspace", dev)
+    at, n_pages, page, table, B, max_pages, counts = _pool(
+        dev, ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale")), page_table, n_visible)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[2] != HEADS or shape[3] != HEAD_DIM:
+        raise ValueError("q must be [B, L, 64, 512]")
+    L = shape[1]
+    if idx.dim() != 2 or idx.shape[0] != B:
+        raise ValueError("idx must be [B, k]")
+    swa_at, n_swa = None, 0
+    if swa is not None:
+        swa_at = _take(swa, torch.uint8, "swa", dev)
+        n_swa = swa.shape[2] if swa.dim() == 4 else 0
+        if swa.shape != (B, L, n_swa, HEAD_DIM):
+            raise ValueError("swa must be [B, L, n_swa, 512]")
+    _call("csa2_paged_sparse_attn_decode", q_at, B, L, *at, n_pages, page, table, max_pages, counts, idx_at,
+          idx.shape[1], swa_at, n_swa, float(sm_scale), _shaped(out, torch.bfloat16, shape, "out", dev),
+          _optional(out_f32, torch.float32, shape, "out_f32", dev), _optional(lse, torch.float32, shape[:3], "lse", dev),
+          ws_at, workspace.numel(), _s(stream))
 
 
 def csa2_paged_attn(q, kv_data, kv_scale, page_table, n_visible, out, workspace, cu_q=None, causal=True, out_f32=None,
@@ -592,17 +613,17 @@ def csa2_paged_attn(q, kv_data, kv_scale, page_table, n_visible, out, workspace,
     """Dense attention of q [n_tokens, 64, 512] bf16 over every entry a token
     sees; cu_q [B + 1] int32 gives each sequence its rows (None: the same number
     each); out_f32 [n_tokens, 64, 512] and lse [n_tokens, 64] are optional."""
-    _req(q, torch.bfloat16, "q"); _req(out, torch.bfloat16, "out"); _req(workspace, torch.uint8, "workspace")
-    _req(out_f32, torch.float32, "out_f32", allow_none=True); _req(lse, torch.float32, "lse", allow_none=True)
-    n_pages, page, B, max_pages = _pool((kv_data, kv_scale), ((256, "kv_data"), (32, "kv_scale")), page_table,
-                                        n_visible)
-    _shape(q.dim() == 3 and q.shape[1:] == (HEADS, HEAD_DIM), "q must be [n_tokens, 64, 512]")
-    _outputs(q, out, out_f32, lse)
-    _runs(cu_q, B, "cu_q")
-    _same_device(q, kv_data, kv_scale, page_table, n_visible, out, workspace, cu_q, out_f32, lse)
-    _call("csa2_paged_attn", _p(q), q.shape[0], _p(cu_q), B, _p(kv_data), _p(kv_scale), n_pages, page, _p(page_table),
-          max_pages, _p(n_visible), int(bool(causal)), float(sm_scale), _p(out), _p(out_f32), _p(lse), _p(workspace),
-          workspace.numel(), _s(stream))
+    dev = _device(q, "q")
+    q_at, ws_at = _take(q, torch.bfloat16, "q", dev), _take(workspace, torch.uint8, "workspace", dev)
+    at, n_pages, page, table, B, max_pages, counts = _pool(
+        dev, ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale")), page_table, n_visible)
+    shape = q.shape
+    if len(shape) != 3 or shape[1] != HEADS or shape[2] != HEAD_DIM:
+        raise ValueError("q must be [n_tokens, 64, 512]")
+    _call("csa2_paged_attn", q_at, shape[0], _optional(cu_q, torch.int32, (B + 1,), "cu_q", dev), B, *at, n_pages, page,
+          table, max_pages, counts, 1 if causal else 0, float(sm_scale), _shaped(out, torch.bfloat16, shape, "out", dev),
+          _optional(out_f32, torch.float32, shape, "out_f32", dev), _optional(lse, torch.float32, shape[:2], "lse", dev),
+          ws_at, workspace.numel(), _s(stream))
 
 
 # ---- allocating helpers (torch memory plumbing + the entry points above) --------
