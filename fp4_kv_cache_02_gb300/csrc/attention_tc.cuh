@@ -278,6 +278,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int pf_tile = -1;
   int64_t nv_seq = -1;
   bool pf_rows = false;   // pf_idx's row is still to be prefetched into L2
+  // place t of the sequence's list, over pages as the pool's row (below 2^31 - 1,
+  // which stands for an entry that has none: refused like one past the end)
+  auto listed = [&](const int t) -> int32_t {
+    const int32_t e = a.idx[(int64_t)seq * a.k + t];
+    if (!a.paged || e < 0) return e;
+    const int64_t row = e < a.paged_visible[seq] && e < a.pages.capacity() ? a.pages.row(seq, e) : -1;
+    return row < 0 ? 0x7FFFFFFF : (int32_t)row;
+  };
   auto gather_dequant = [&](const bool swa, const int tile, const int qi_swa, const int next_sel_tile) {
     const uint32_t par = items_done & 1u;
     // SWA tiles: one contiguous bulk copy of the tile's rows into the staging
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // n_visible may come from the kernel before this one (a KV append):
           // read after pdl_wait(), like the indices
           if (nv_seq < 0) nv_seq = a.n_visible ? (int64_t)a.n_visible[seq] : a.nv_const;
-          const int32_t p = pf_tile == tile ? pf_idx : a.idx[(int64_t)seq * a.k + t];
+          const int32_t p = pf_tile == tile ? pf_idx : listed(t);
           if (p >= 0) {
             if (p < nv_seq) {
               valid = 1;
@@ -320,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next selected tile's index for this row, in flight through this tile
         if (next_sel_tile >= 0) {
           const int tn = next_sel_tile * kRows + tid;
-          pf_idx = tn < a.k ? a.idx[(int64_t)seq * a.k + tn] : -1;
+          pf_idx = tn < a.k ? listed(tn) : -1;
           pf_tile = next_sel_tile;
         }
       }
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid < kRows) {
         if (nv_seq < 0) nv_seq = a.n_visible ? (int64_t)a.n_visible[seq] : a.nv_const;
         const int tn = next_sel * kRows + tid;
-        pf_idx = tn < a.k ? a.idx[(int64_t)seq * a.k + tn] : -1;
+        pf_idx = tn < a.k ? listed(tn) : -1;
         pf_tile = next_sel;
         pf_rows = true;
       }

@@ -328,22 +328,6 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   }
 }
 
-// ---- selected entries to rows of the pool ----------------------------------------
-__global__ void page_rows_kernel(const int32_t* __restrict__ idx, int32_t B, int32_t k,
-                                 const int32_t* __restrict__ n_visible, PageTable pages, int32_t* __restrict__ rows) {
-  pdl_begin();
-  const int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (j >= (int64_t)B * k) return;
-  const int32_t b = (int32_t)(j / k);
-  const int32_t e = idx[j];
-  int64_t row = -1;
-  if (e >= 0) {
-    if (e < n_visible[b] && e < pages.capacity()) row = pages.row(b, e);
-    if (row < 0) record_error(&g_paged_error, CSA2_ERR_DEVICE);
-  }
-  rows[j] = (int32_t)row;
-}
-
 }  // namespace csa2
 
 using namespace csa2;
@@ -445,15 +429,5 @@ extern "C" int csa2_paged_kv_append(const void* kv_bf16, const void* ik_bf16, in
   if (in_place)
     CSA2_LAUNCH_PDL(advance_paged_kernel, dim3((unsigned)((B + 255) / 256)), dim3(256), 0, s, n_visible_out,
                     cu_tokens, B, n_tokens, a.per_seq, a.pages);
-  return CSA2_OK;
-}
-
-// Rows of the pool of the selected entries (csa2_paged_sparse_attn_decode).
-int csa2_launch_page_rows(const int32_t* idx, int32_t B, int32_t k, const int32_t* n_visible, const PageTable& pages,
-                          int32_t* rows, cudaStream_t s) {
-  const int64_t n = (int64_t)B * k;
-  if (n == 0) return CSA2_OK;
-  CSA2_LAUNCH_PDL(page_rows_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, idx, B, k, n_visible, pages,
-                  rows);
   return CSA2_OK;
 }
