@@ -60,12 +60,12 @@ constexpr int kRows = 128;
 constexpr int kPlaces = 3;                // rings of 128-channel groups of R, in tensor and in shared memory
 constexpr int kBlkR = kRows * 128;        // 64 channels of R: [128 rows][128 B]
 constexpr int kBlkQ = kHeads * 128;       // 64 channels of Q: [64 heads][128 B]
-constexpr int kBlkP = kHeads * 128;       // 64 rows of P: [64 heads][128 B]
+constexpr int kBlkP = kRows * kHeads * 2; // P: [128 rows][64 heads]
 constexpr int kOffR = 0;                                // 3 groups of 2 blocks, 96 KiB
 constexpr int kOffQ = kOffR + kPlaces * 2 * kBlkR;      // 8 blocks, 64 KiB
-constexpr int kOffP = kOffQ + 8 * kBlkQ;                // 2 blocks, 16 KiB
+constexpr int kOffP = kOffQ + 8 * kBlkQ;                // 16 KiB
 constexpr int kRawGroup = kRows * 64;                   // a group's codes, [128 rows][64 B] with the 64-byte swizzle
-constexpr int kOffRaw = kOffP + 2 * kBlkP;              // a tile's codes, 32 KiB
+constexpr int kOffRaw = kOffP + kBlkP;              // a tile's codes, 32 KiB
 constexpr int kOffRawSc = kOffRaw + 4 * kRawGroup;      // and scales, [128 rows][32 B], 4 KiB
 constexpr int kOffMisc = kOffRawSc + kRows * kKvScales;
 constexpr uint32_t kTmemCols = 512;
@@ -87,7 +87,7 @@ constexpr int kPartFloats = kHeads * kHeadDim;
 struct PartList {
   int32_t token;       // -1: this CTA begins no such token
   int32_t first_slot;  // slot of the first part
-  int32_t cta0, cta1;  // the CTAs with parts: cta0 .. cta1 (those with tiles)
+  int32_t cta0, cta1;  // its first and last tile's CTAs
   int64_t tiles;       // tiles of the whole call
 };
 
@@ -233,13 +233,6 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
   return r != 0;
 }
 
-// 32 bytes of the cache (read once per token, by many CTAs: L2)
-__device__ __forceinline__ void ldg_32(const uint8_t* p, uint32_t* r) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "l"(p));
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap rows_map, Args a) {
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -277,52 +270,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tc::tmem_alloc(&sh.tmem, kTmemCols);
   pdl_begin();
 
-  // ---- this CTA's run [f0, f1) of the list: a scan over the sequences' tiles ----
-  int64_t total = 0;
-  for (int32_t b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int32_t b = b0 + tid;
-    int64_t n = 0;
+  // ---- this CTA's run [f0, f1) of the list: a scan over the sequences' tiles,
+  // kThreads at a time. The total is known behind the last ones only, so where
+  // there are more sequences than threads they are gone through once more ----
+  int64_t total = 0, n = 0, lo = 0;  // lo: tiles before this thread's sequence, n: its own
+  const auto scan = [&](int32_t b, bool report) {
+    n = 0;
     if (b < a.B) {
-      const Seq s = load_seq(a, b, cta == 0);
+      const Seq s = load_seq(a, b, report);
       n = tiles_before(a, s, s.count);
     }
+    int64_t incl = n;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) sh.scan[warp] = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) total += sh.scan[w];
+    const int64_t of_warp = lane < kWarps ? sh.scan[lane] : 0;
+    int64_t before = of_warp;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    lo = total + incl - n + __shfl_sync(0xffffffffu, before - of_warp, warp);
+    total += __shfl_sync(0xffffffffu, before, kWarps - 1);
     __syncthreads();
-  }
-  const int64_t f0 = total * cta / G, f1 = total * (cta + 1) / G;
+  };
+  for (int32_t b0 = 0; b0 < a.B; b0 += kThreads) scan(b0 + tid, cta == 0);
+  const int64_t all = total, f0 = all * cta / G, f1 = all * (cta + 1) / G;
   if (tid == 0) a.lists[cta].token = -1;
   if (f0 < f1) {
-    // the sequence that holds tile f0 (a second scan: the first did not know f0)
-    int64_t base = 0;
-    for (int32_t b0 = 0; b0 < a.B && base <= f0; b0 += kThreads) {
-      const int32_t b = b0 + tid;
-      int64_t n = 0;
-      if (b < a.B) {
-        const Seq s = load_seq(a, b, false);
-        n = tiles_before(a, s, s.count);
-      }
-      int64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      int64_t lo = base + incl - n;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) lo += sh.scan[w];
-        base += sh.scan[w];
-      }
-      if (f0 >= lo && f0 < lo + n) {
-        sh.seq = b;
-        sh.at = f0 - lo;
-      }
-      __syncthreads();
+    int32_t b0 = 0;
+    if (a.B > kThreads) {
+      total = 0;
+      for (; total <= f0; b0 += kThreads) scan(b0 + tid, false);
+      b0 -= kThreads;
+    }
+    if (f0 >= lo && f0 < lo + n) {
+      sh.seq = b0 + tid;
+      sh.at = f0 - lo;
     }
   }
   tc::tc_fence_before();
@@ -401,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         info_done(j);
       }
     } else if (warp == kOWarp) {
-      constexpr uint32_t idesc = idesc_f16(128, 64, 1, 0);  // A = R^T is MN-major
+      constexpr uint32_t idesc = idesc_f16(128, 64, 1, 1);  // A = R^T and B = P^T are MN-major
       const uint32_t r_lo = tc::smem_u32(sR), p_lo = tc::smem_u32(sP);
       uint32_t place = 0, use = 0;
 #pragma unroll 1
@@ -418,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 16 rows
             tc::mma_f16_one(elected, tmem + kColO + 64u * (uint32_t)mb, ad + (uint64_t)((k * 16 * 128) >> 4),
-                            bd + (uint64_t)(((k >> 2) * kBlkP + (k & 3) * 32) >> 4), idesc, k ? 1u : more);
+                            bd + (uint64_t)((k * 16 * 128) >> 4), idesc, k ? 1u : more);
           tc::mma_commit_one(elected, sh.r_empty + place);
           place = place + 1 == kPlaces ? 0 : place + 1;
           use += place == 0 ? 1u : 0u;
@@ -602,12 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (token * kHeads + h) * kHeadDim) + c;
         uint32_t amax = 0;
 #pragma unroll 1
-        for (int k = 0; k < 8; k += 2) {
-          uint4 v[4];
+        for (int k = 0; k < 8; k += 4) {
+          uint4 v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = src[(k + (i >> 1)) * 8 + (i & 1) * 4];
+          for (int i = 0; i < 8; ++i) v[i] = src[(k + (i >> 1)) * 8 + (i & 1) * 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
@@ -741,15 +730,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j > 0) wait(&sh.o, (uint32_t)(j - 1));  // the last product has read P
         {
-          uint8_t* blkp = sP + (my_row >> 6) * kBlkP;
-          const uint32_t chunk = (uint32_t)(my_row & 63) >> 3, within = ((uint32_t)my_row & 7u) * 2u;
+          // row my_row of P: 64 heads, this thread's 32 of them
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            *reinterpret_cast<uint16_t*>(blkp + tc::sw128_offset((uint32_t)(h0 + 2 * i), chunk) + within) =
-                (uint16_t)(ph[i] & 0xFFFFu);
-            *reinterpret_cast<uint16_t*>(blkp + tc::sw128_offset((uint32_t)(h0 + 2 * i + 1), chunk) + within) =
-                (uint16_t)(ph[i] >> 16);
-          }
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(sP + tc::sw128_offset((uint32_t)my_row, (uint32_t)(4 * half + i))) =
+                make_uint4(ph[4 * i], ph[4 * i + 1], ph[4 * i + 2], ph[4 * i + 3]);
         }
         tc::fence_proxy_async_smem();
         arrive(&sh.p);
@@ -816,8 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             pl.token = (int32_t)token;
             pl.first_slot = slot;
             pl.cta0 = cta;
-            pl.cta1 = (int32_t)(((last + 1) * G + total - 1) / total - 1);
-            pl.tiles = total;
+            pl.cta1 = (int32_t)(((last + 1) * G + all - 1) / all - 1);
+            pl.tiles = all;
             a.lists[cta] = pl;
           }
           first = true;
@@ -841,23 +826,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- the tokens whose tiles lie with several CTAs ---------------------------------
 // One block per (token, head) at a time: out = sum_j 2^(ref_j - M) O_j / sum_j
-// 2^(ref_j - M) l_j over the parts in list order, in a fixed tree (four groups
-// of threads take every fourth part).
-constexpr int kJoinThreads = 512;
+// 2^(ref_j - M) l_j over the parts in list order, even and odd parts summed
+// apart. Warp w takes channels 128 (w % 4) .. and the parts of parity w / 4, and
+// works out the weights for itself, so that a block only meets for its two sums:
+// a split token has two parts more often than many, and there may be one per SM
+// (64 heads of each), so the chain of dependent reads of an item is what counts.
+// (One block of 512 threads per item with the weights in shared memory: 70 us
+// after 2,048 tokens of one prompt, against XX.)
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 8;  // per SM
 
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(Args a, int32_t G) {
   __shared__ int32_t s_list[1024];
   __shared__ int32_t s_n;
-  __shared__ float s_w[1024];
-  __shared__ int32_t s_slot[1024];
-  __shared__ int32_t s_parts;
-  __shared__ float s_inv;
-  __shared__ __align__(16) float4 s_sum[3][128];
+  __shared__ __align__(16) float4 s_sum[128];
   pdl_begin();
-  const int tid = threadIdx.x, lane = tid & 31;
-  // the tokens to join, in order (G <= 1024: one place per thread, twice)
-  if (tid < 32) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the tokens to join, in order (G <= 1024)
+  if (warp == 0) {
     int n = 0;
+#pragma unroll 5
     for (int c0 = 0; c0 < G; c0 += 32) {
       const bool has = c0 + lane < G && a.lists[c0 + lane].token >= 0;
       const uint32_t m = __ballot_sync(0xffffffffu, has);
@@ -868,83 +856,71 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(Args a, i
   }
   __syncthreads();
   const int items = s_n * kHeads;
+  const int parity = warp >> 2, c4 = (warp & 3) * 32 + lane;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const PartList pl = a.lists[s_list[it / kHeads]];
     const int h = it % kHeads;
-    __syncthreads();  // the last item's shared values are done with
-    if (tid < 32) {
-      // the parts: the first one, then the CTAs up to cta1 that have tiles
-      int n = 0;
-      float M = -INFINITY;
-      for (int c0 = pl.cta0; c0 <= pl.cta1; c0 += 32) {
-        const int c = c0 + lane;
-        const bool has = c <= pl.cta1 && (c == pl.cta0 || pl.tiles * c / G < pl.tiles * (c + 1) / G);
-        const uint32_t m = __ballot_sync(0xffffffffu, has);
-        if (has) {
-          const int at = n + __popc(m & ((1u << lane) - 1u));
-          const int slot = c == pl.cta0 ? pl.first_slot : 2 * c;
-          s_slot[at] = slot;
-          const float2 ml = a.part_ml[(int64_t)slot * kHeads + h];
-          if (ml.y > 0.0f) M = fmaxf(M, ml.x);
-        }
-        n += __popc(m);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      __syncwarp();
-      float L = 0.0f;
-      for (int j = lane; j < n; j += 32) {
-        const float2 ml = a.part_ml[(int64_t)s_slot[j] * kHeads + h];
-        const float w = ml.y > 0.0f ? fast_exp2(ml.x - M) : 0.0f;
-        s_w[j] = w;
-        L += w * ml.y;
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane == 0) {
-        s_parts = n;
-        s_inv = L > 0.0f ? 1.0f / L : 0.0f;
-        if (a.lse)
-          a.lse[(int64_t)pl.token * kHeads + h] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-      }
-    }
-    __syncthreads();
-    const int g = tid >> 7, c4 = tid & 127, n = s_parts;
+    // Part j lies with the j-th CTA that has tiles: with fewer tiles than CTAs
+    // the one that holds tile first + j, else simply the next.
+    const bool sparse = pl.tiles < G;
+    const int64_t first = sparse ? pl.tiles * pl.cta0 / G : 0;
+    const int n = sparse ? (int)(pl.tiles * pl.cta1 / G - first) + 1 : pl.cta1 - pl.cta0 + 1;
+    float M = -INFINITY, L = 0.0f;  // L: this lane's share
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int j = g; j < n; j += 4) {
-      const float4 v =
-          reinterpret_cast<const float4*>(a.part_o + (int64_t)s_slot[j] * kPartFloats + (int64_t)h * kHeadDim)[c4];
-      const float w = s_w[j];
-      // a part that saw nothing has weight 0 and zeros
-      acc.x = fmaf(v.x, w, acc.x);
-      acc.y = fmaf(v.y, w, acc.y);
-      acc.z = fmaf(v.z, w, acc.z);
-      acc.w = fmaf(v.w, w, acc.w);
-    }
-    if (g) s_sum[g - 1][c4] = acc;
-    __syncthreads();
-    if (g == 0) {
-      const float inv = s_inv;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float4 v = s_sum[k][c4];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const int j = j0 + lane;
+      int slot = 0;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (j < n) {
+        const int c = sparse ? (int)(((first + j + 1) * G + pl.tiles - 1) / pl.tiles) - 1 : pl.cta0 + j;
+        slot = j == 0 ? pl.first_slot : 2 * c;
+        ml = a.part_ml[(int64_t)slot * kHeads + h];
       }
-      acc.x *= inv;
-      acc.y *= inv;
-      acc.z *= inv;
-      acc.w *= inv;
+      // (a part that saw nothing has l = 0, weight 0 and zeros)
+      float top = ml.y > 0.0f ? fmaxf(M, ml.x) : M;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float shrink = M > -INFINITY ? fast_exp2(M - top) : 0.0f;
+      const float w = ml.y > 0.0f ? fast_exp2(ml.x - top) : 0.0f;
+      M = top;
+      L = L * shrink + w * ml.y;
+      acc.x *= shrink;
+      acc.y *= shrink;
+      acc.z *= shrink;
+      acc.w *= shrink;
+      const int here = min(32, n - j0);
+#pragma unroll 8
+      for (int i = parity; i < here; i += 2) {
+        const int64_t at = __shfl_sync(0xffffffffu, slot, i);
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + at * kPartFloats + (int64_t)h * kHeadDim)[c4];
+        acc.x = fmaf(v.x, wi, acc.x);
+        acc.y = fmaf(v.y, wi, acc.y);
+        acc.z = fmaf(v.z, wi, acc.z);
+        acc.w = fmaf(v.w, wi, acc.w);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (parity) s_sum[c4] = acc;
+    __syncthreads();
+    if (!parity) {
+      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      const float4 v = s_sum[c4];
+      acc.x = (acc.x + v.x) * inv;
+      acc.y = (acc.y + v.y) * inv;
+      acc.z = (acc.z + v.z) * inv;
+      acc.w = (acc.w + v.w) * inv;
       const int64_t o = ((int64_t)pl.token * kHeads + h) * kHeadDim + c4 * 4;
       if (a.out_f32) *reinterpret_cast<float4*>(a.out_f32 + o) = acc;
       const __nv_bfloat162 b0 = __floats2bfloat162_rn(acc.x, acc.y);
       const __nv_bfloat162 b1 = __floats2bfloat162_rn(acc.z, acc.w);
       *reinterpret_cast<uint2*>(a.out + o) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+      if (a.lse && c4 == 0)
+        a.lse[(int64_t)pl.token * kHeads + h] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
     }
+    __syncthreads();  // the sums are done with
   }
 }
 
@@ -1060,7 +1036,7 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   cudaStream_t s = (cudaStream_t)stream;
   CSA2_LAUNCH_PDL(pattn::paged_attn_kernel, dim3((unsigned)G), dim3(pattn::kThreads), (size_t)pattn::kSmemBytes, s,
                   rows_map, a);
-  CSA2_LAUNCH_PDL(pattn::paged_attn_join_kernel, dim3((unsigned)(2 * G)), dim3(pattn::kJoinThreads), (size_t)0, s, a,
+  CSA2_LAUNCH_PDL(pattn::paged_attn_join_kernel, dim3((unsigned)(pattn::kJoinBlocks * G)), dim3(pattn::kJoinThreads), (size_t)0, s, a,
                   (int32_t)G);
   return CSA2_OK;
 }
