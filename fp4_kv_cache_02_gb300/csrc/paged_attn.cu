@@ -50,24 +50,24 @@ using attn_tc::warp_transpose_reduce16;
 // list and looks pages up, 19 copies the rows into shared memory. A warp's
 // tensor-memory lanes are the quadrant warp % 4; the two warps of a quadrant in a
 // role share its rows by heads (softmax) or channels (dequantisation).
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kSWarp = 16, kOWarp = 17, kWalkWarp = 18, kCopyWarp = 19;
-constexpr int kThreads = 640;
+constexpr int kSoftWarps = 8, kFeedS = 8, kFeedO = 16, kSWarp = 24, kOWarp = 25, kWalkWarp = 26, kCopyWarp = 27;
+constexpr int kThreads = 896;
 constexpr int kWarps = kThreads / 32;
-// Registers: 640 threads start with 96 each (61,440 in all).
-constexpr int kRegsSoft = 112, kRegsLoad = 104, kRegsIssue = 48;
-static_assert(256 * kRegsSoft + 256 * kRegsLoad + 128 * kRegsIssue <= kThreads * 96, "register split");
+// Registers: 896 threads start with 72 each (64,512 in all).
+constexpr int kRegsSoft = 112, kRegsFeed = 56, kRegsIssue = 40;
+static_assert(256 * kRegsSoft + 512 * kRegsFeed + 128 * kRegsIssue <= kThreads * 72, "register split");
 constexpr int kRows = 128;
-constexpr int kPlaces = 3;                // rings of 128-channel groups of R, in tensor and in shared memory
+constexpr int kPlacesA = 3, kPlaces = 2;  // rings of 128-channel groups of R, in tensor and in shared memory
 constexpr int kBlkR = kRows * 128;        // 64 channels of R: [128 rows][128 B]
 constexpr int kBlkQ = kHeads * 128;       // 64 channels of Q: [64 heads][128 B]
 constexpr int kBlkP = kRows * kHeads * 2; // P: [128 rows][64 heads]
-constexpr int kOffR = 0;                                // 3 groups of 2 blocks, 96 KiB
+constexpr int kOffR = 0;                                // 2 groups of 2 blocks, 64 KiB
 constexpr int kOffQ = kOffR + kPlaces * 2 * kBlkR;      // 8 blocks, 64 KiB
 constexpr int kOffP = kOffQ + 8 * kBlkQ;                // 16 KiB
 constexpr int kRawGroup = kRows * 64;                   // a group's codes, [128 rows][64 B] with the 64-byte swizzle
-constexpr int kOffRaw = kOffP + kBlkP;              // a tile's codes, 32 KiB
-constexpr int kOffRawSc = kOffRaw + 4 * kRawGroup;      // and scales, [128 rows][32 B], 4 KiB
-constexpr int kOffMisc = kOffRawSc + kRows * kKvScales;
+constexpr int kOffRaw = kOffP + kBlkP;              // two tiles' codes, 64 KiB
+constexpr int kOffRawSc = kOffRaw + 8 * kRawGroup;      // and scales, [128 rows][32 B], 8 KiB
+constexpr int kOffMisc = kOffRawSc + 2 * kRows * kKvScales;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;             // S^T: 64 columns (heads), lanes = rows
 constexpr uint32_t kColO = 64;            // O^T: 4 blocks x 64 columns, lanes = channels
@@ -202,10 +202,10 @@ struct __align__(16) Shared {
   volatile int abort;
   // barriers. Those of a tile complete once per tile, so that tile j waits for
   // phase j; those of a place once per use.
-  uint64_t full[kPlaces];     // a group is in its place in tensor memory: 4 warps
-  uint64_t empty[kPlaces];    // S^T over it is done
-  uint64_t raw;               // a tile's codes and scales have arrived
-  uint64_t raw_read;          // and been read: 8 warps
+  uint64_t full[kPlacesA];    // a group is in its place in tensor memory: 4 warps
+  uint64_t empty[kPlacesA];   // S^T over it is done
+  uint64_t raw[2];            // a tile's codes and scales have arrived
+  uint64_t raw_read[2];       // and been read: 16 warps
   uint64_t r_full[kPlaces];   // a group is in its place in shared memory: 4 warps
   uint64_t r_empty[kPlaces];  // its channels of O^T are done
   uint64_t q;                 // Q written: 8 warps (once per token)
@@ -214,7 +214,7 @@ struct __align__(16) Shared {
   uint64_t p;                 // P written, O^T rescaled (or read out): 8 warps
   uint64_t o;                 // O^T complete
   uint64_t info_full[kRing];
-  uint64_t info_used[kRing];  // 19 warps
+  uint64_t info_used[kRing];  // 27 warps
   uint64_t end[2];
 };
 // (no static shared memory: dynamic shared memory then starts 1,024-byte aligned)
@@ -245,14 +245,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = (int)gridDim.x, cta = (int)blockIdx.x;
 
   if (tid == 0) {
-    for (int i = 0; i < kPlaces; ++i) {
+    for (int i = 0; i < kPlacesA; ++i) {
       tc::mbar_init(sh.full + i, 4);
       tc::mbar_init(sh.empty + i, 1);
+    }
+    for (int i = 0; i < kPlaces; ++i) {
       tc::mbar_init(sh.r_full + i, 4);
       tc::mbar_init(sh.r_empty + i, 1);
     }
-    tc::mbar_init(&sh.raw, 1);
-    tc::mbar_init(&sh.raw_read, 8);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(sh.raw + i, 1);
+      tc::mbar_init(sh.raw_read + i, 16);
+    }
     tc::mbar_init(&sh.q, kSoftWarps);
     tc::mbar_init(&sh.s, 1);
     tc::mbar_init(&sh.s_read, kSoftWarps);
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) tc::mbar_init(sh.end + i, 1);
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(sh.info_full + i, 1);
-      tc::mbar_init(sh.info_used + i, 19);
+      tc::mbar_init(sh.info_used + i, 27);
     }
     sh.abort = 0;
     sh.seq = -1;
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                bd + (uint64_t)((k >> 2) * (kBlkQ >> 4) + (k & 3) * 2), idesc,
                                k ? 1u : (uint32_t)(g != 0));
           tc::mma_commit_one(elected, sh.empty + place);
-          place = place + 1 == kPlaces ? 0 : place + 1;
+          place = place + 1 == kPlacesA ? 0 : place + 1;
           use += place == 0 ? 1u : 0u;
         }
         tc::mma_commit_one(elected, &sh.s);
@@ -450,27 +454,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int32_t j = 0; j < n_run; ++j) {
         const Info& info = info_of(j);
-        if (j > 0) wait(&sh.raw_read, (uint32_t)(j - 1));
+        const int buf = j & 1;
+        if (j > 1) wait(sh.raw_read + buf, (uint32_t)(j >> 1) - 1u);
         // lane i: run i
         const int r0 = lane << run_shift;
         const int32_t page = r0 < kRows && r0 < info.rows ? info.page[r0 >> 4] : -1;
         const uint32_t there = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (lane == 0) tc::mbar_arrive_expect_tx(&sh.raw, there * (uint32_t)run * (kKvBytes + kKvScales));
+        if (lane == 0) tc::mbar_arrive_expect_tx(sh.raw + buf, there * (uint32_t)run * (kKvBytes + kKvScales));
         __syncwarp();
         if (page >= 0 && !sh.abort) {
           const int64_t row = ((int64_t)page << a.pages.shift) + ((info.at + r0) & (a.pages.page_size() - 1));
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            tc::tma_load_2d(sm + kOffRaw + g * kRawGroup + r0 * 64, &rows_map, g * 64, (int32_t)row, &sh.raw);
-          tc::bulk_load(sm + kOffRawSc + r0 * kKvScales, a.kv_scale + row * kKvScales, (uint32_t)(run * kKvScales),
-                        &sh.raw);
+            tc::tma_load_2d(sm + kOffRaw + (4 * buf + g) * kRawGroup + r0 * 64, &rows_map, g * 64, (int32_t)row,
+                            sh.raw + buf);
+          tc::bulk_load(sm + kOffRawSc + (buf * kRows + r0) * kKvScales, a.kv_scale + row * kKvScales,
+                        (uint32_t)(run * kKvScales), sh.raw + buf);
         }
         info_done(j);
       }
       // (the last copies are waited for by the warps that read them; those may not
       // have when a wait ran out)
-      for (uint32_t n = 0; n_run > 0 && sh.abort && n < (1u << 22); ++n)
-        if (tc::mbar_try_wait(&sh.raw, (uint32_t)(n_run - 1) & 1u)) break;
+      for (int32_t j = n_run > 1 ? n_run - 2 : 0; j < n_run && sh.abort; ++j)
+        for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.raw + (j & 1), (uint32_t)(j >> 1) & 1u); ++n) {
+        }
     }
     if ((warp == kSWarp || warp == kOWarp) && n_run > 0 && sh.abort) {
       // a wait ran out: products in flight end before tensor memory is freed
@@ -479,102 +486,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp >= kLoadWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
-    if (n_run > 0) {
-      // ---- dequantise: a thread takes the channels of groups half and half + 2
-      // (128 each: 64 bytes of codes, 8 of scales) of its row from where the copies
-      // put them (plain loads into registers made the warp wait for them at the
-      // next use of their scoreboard, 3,400 cycles a tile), and keeps them as they
-      // are for two tiles: tile t goes to tensor memory (for S^T) before tile t - 1
-      // goes to shared memory (for O^T) ----
-      struct Raw {
-        uint32_t w[16];
-        uint2 sc;
-      };
-      auto take = [&](Raw& r, int g, bool seen) {
-        const uint8_t* src = sm + kOffRaw + g * kRawGroup;
+  } else if (warp >= kFeedS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFeed));
+    // ---- dequantise: a thread takes the channels of groups half and half + 2
+    // (128 each: 64 bytes of codes, 8 of scales) of its row from where the copies
+    // put them, eight warps into tensor memory for S^T and eight into shared
+    // memory for O^T. (One set of eight for both read the codes once but had each
+    // conversion wait for the last: XX cycles a tile.) ----
+    struct Raw {
+      uint32_t w[16];
+      uint2 sc;
+    };
+    auto take = [&](Raw& r, int32_t t, int g, bool seen) {
+      const uint8_t* src = sm + kOffRaw + (4 * (t & 1) + g) * kRawGroup;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + tc::sw64_offset((uint32_t)my_row, (uint32_t)k));
-          r.w[4 * k] = v.x;
-          r.w[4 * k + 1] = v.y;
-          r.w[4 * k + 2] = v.z;
-          r.w[4 * k + 3] = v.w;
-        }
-        // (codes are finite whatever they are: times 0 they are zeros)
-        r.sc = *reinterpret_cast<const uint2*>(sm + kOffRawSc + my_row * kKvScales + g * 8);
-        if (!seen) r.sc = make_uint2(0u, 0u);
-      };
-      // channels 32 q .. +31 of a group as fp16 (exact; zeros for zero codes and scales)
-      auto convert = [&](const Raw& r, int q, uint32_t (&o)[16]) {
-        const uint32_t s2 = e4m3x2_to_f16x2(((q < 2 ? r.sc.x : r.sc.y) >> ((q & 1) * 16)) & 0xFFFFu);
+      for (int k = 0; k < 4; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + tc::sw64_offset((uint32_t)my_row, (uint32_t)k));
+        r.w[4 * k] = v.x;
+        r.w[4 * k + 1] = v.y;
+        r.w[4 * k + 2] = v.z;
+        r.w[4 * k + 3] = v.w;
+      }
+      // (codes are finite whatever they are: times 0 they are zeros)
+      r.sc = *reinterpret_cast<const uint2*>(sm + kOffRawSc + ((t & 1) * kRows + my_row) * kKvScales + g * 8);
+      if (!seen) r.sc = make_uint2(0u, 0u);
+    };
+    // channels 32 q .. +31 of a group as fp16 (exact; zeros for zero codes and scales)
+    auto convert = [&](const Raw& r, int q, uint32_t (&o)[16]) {
+      const uint32_t s2 = e4m3x2_to_f16x2(((q < 2 ? r.sc.x : r.sc.y) >> ((q & 1) * 16)) & 0xFFFFu);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t s = __byte_perm(s2, 0u, k < 2 ? 0x1010u : 0x3232u);
-          uint32_t o0, o1, o2, o3;
-          e2m1x8_to_f16(r.w[4 * q + k], o0, o1, o2, o3);
-          o[4 * k] = mul_f16x2(o0, s);
-          o[4 * k + 1] = mul_f16x2(o1, s);
-          o[4 * k + 2] = mul_f16x2(o2, s);
-          o[4 * k + 3] = mul_f16x2(o3, s);
-        }
-      };
-      // group g of tile t into its place in tensor memory
-      auto feed_s = [&](const Raw& r, int32_t t, int g) {
-        const uint32_t n = 4u * (uint32_t)t + (uint32_t)g, use = n / kPlaces, place = n - use * kPlaces;
-        if (use > 0) wait(sh.empty + place, use - 1u);
-        tc::tc_fence_after();
-        const uint32_t at = tmem + lanes + kColA + 64u * place;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t o[16];
-          convert(r, q, o);
-          tc::tmem_st_32x32b_x16(at + 16u * (uint32_t)q, o);
-        }
-        tc::tmem_st_wait();
-        tc::tc_fence_before();
-        arrive(sh.full + place);
-      };
-      // group g of tile t into its place in R (the eight lanes of a store phase are
-      // eight rows: eight bank groups)
-      auto feed_o = [&](const Raw& r, int32_t t, int g) {
-        const uint32_t n = 4u * (uint32_t)t + (uint32_t)g, use = n / kPlaces, place = n - use * kPlaces;
-        if (use > 0) wait(sh.r_empty + place, use - 1u);
-        uint8_t* blk = sR + place * (2 * kBlkR);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t o[16];
-          convert(r, q, o);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(blk + (q >> 1) * kBlkR +
-                                      tc::sw128_offset((uint32_t)my_row, (uint32_t)((q & 1) * 4 + k))) =
-                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
-        tc::fence_proxy_async_smem();
-        arrive(sh.r_full + place);
-      };
-      Raw c0, c1, p0, p1;  // tile t, tile t - 1
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t s = __byte_perm(s2, 0u, k < 2 ? 0x1010u : 0x3232u);
+        uint32_t o0, o1, o2, o3;
+        e2m1x8_to_f16(r.w[4 * q + k], o0, o1, o2, o3);
+        o[4 * k] = mul_f16x2(o0, s);
+        o[4 * k + 1] = mul_f16x2(o1, s);
+        o[4 * k + 2] = mul_f16x2(o2, s);
+        o[4 * k + 3] = mul_f16x2(o3, s);
+      }
+    };
+    if (warp < kFeedO) {
 #pragma unroll 1
-      for (int32_t t = 0; t <= n_run; ++t) {
-        if (t < n_run) {
-          const Info& info = info_of(t);
-          const bool seen = my_row < info.rows && info.page[my_row >> 4] >= 0;
-          wait(&sh.raw, (uint32_t)t);
-          take(c0, half, seen);
-          take(c1, half + 2, seen);
-          arrive(&sh.raw_read);
-          feed_s(c0, t, half);
-          feed_s(c1, t, half + 2);
-          info_done(t);
+      for (int32_t t = 0; t < n_run; ++t) {
+        const Info& info = info_of(t);
+        const bool seen = my_row < info.rows && info.page[my_row >> 4] >= 0;
+        wait(sh.raw + (t & 1), (uint32_t)(t >> 1));
+#pragma unroll 1
+        for (int g = half; g < 4; g += 2) {
+          Raw r;
+          take(r, t, g, seen);
+          if (g >= 2) arrive(sh.raw_read + (t & 1));
+          const uint32_t n = 4u * (uint32_t)t + (uint32_t)g, use = n / kPlacesA, place = n - use * kPlacesA;
+          if (use > 0) wait(sh.empty + place, use - 1u);
+          tc::tc_fence_after();
+          const uint32_t at = tmem + lanes + kColA + 64u * place;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[16];
+            convert(r, q, o);
+            tc::tmem_st_32x32b_x16(at + 16u * (uint32_t)q, o);
+          }
+          tc::tmem_st_wait();
+          tc::tc_fence_before();
+          arrive(sh.full + place);
         }
-        if (t > 0) {
-          feed_o(p0, t - 1, half);
-          feed_o(p1, t - 1, half + 2);
+        info_done(t);
+      }
+    } else {
+      // (a warp's groups all go to place half: the eight lanes of a store phase are
+      // eight rows, eight bank groups)
+#pragma unroll 1
+      for (int32_t t = 0; t < n_run; ++t) {
+        const Info& info = info_of(t);
+        const bool seen = my_row < info.rows && info.page[my_row >> 4] >= 0;
+        wait(sh.raw + (t & 1), (uint32_t)(t >> 1));
+#pragma unroll 1
+        for (int g = half; g < 4; g += 2) {
+          Raw r;
+          take(r, t, g, seen);
+          if (g >= 2) arrive(sh.raw_read + (t & 1));
+          const uint32_t use = 2u * (uint32_t)t + (uint32_t)(g >> 1);
+          if (use > 0) wait(sh.r_empty + half, use - 1u);
+          uint8_t* blk = sR + half * (2 * kBlkR);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[16];
+            convert(r, q, o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(blk + (q >> 1) * kBlkR +
+                                        tc::sw128_offset((uint32_t)my_row, (uint32_t)((q & 1) * 4 + k))) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+          tc::fence_proxy_async_smem();
+          arrive(sh.r_full + half);
         }
-        p0 = c0;
-        p1 = c1;
+        info_done(t);
       }
     }
   } else {
