@@ -65,9 +65,9 @@ constexpr int kOffR = 0;                                // 2 groups of 2 blocks,
 constexpr int kOffQ = kOffR + kPlaces * 2 * kBlkR;      // 8 blocks, 64 KiB
 constexpr int kOffP = kOffQ + 8 * kBlkQ;                // 16 KiB
 constexpr int kRawGroup = kRows * 64;                   // a group's codes, [128 rows][64 B] with the 64-byte swizzle
-constexpr int kOffRaw = kOffP + kBlkP;              // two tiles' codes, 64 KiB
-constexpr int kOffRawSc = kOffRaw + 8 * kRawGroup;      // and scales, [128 rows][32 B], 8 KiB
-constexpr int kOffMisc = kOffRawSc + 2 * kRows * kKvScales;
+constexpr int kOffRaw = kOffP + kBlkP;              // two tiles' codes, group by group, 64 KiB
+constexpr int kOffRawSc = kOffRaw + 8 * kRawGroup;      // and three tiles' scales, [128 rows][32 B], 12 KiB
+constexpr int kOffMisc = kOffRawSc + 3 * kRows * kKvScales;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;             // S^T: 64 columns (heads), lanes = rows
 constexpr uint32_t kColO = 64;            // O^T: 4 blocks x 64 columns, lanes = channels
@@ -204,8 +204,8 @@ struct __align__(16) Shared {
   // phase j; those of a place once per use.
   uint64_t full[kPlacesA];    // a group is in its place in tensor memory: 4 warps
   uint64_t empty[kPlacesA];   // S^T over it is done
-  uint64_t raw[2];            // a tile's codes and scales have arrived
-  uint64_t raw_read[2];       // and been read: 16 warps
+  uint64_t raw[8];            // a group's codes have arrived (group 0's: and the tile's scales)
+  uint64_t raw_read[8];       // and been read: 8 warps (group 0's: waited for by all 16, for the scales)
   uint64_t r_full[kPlaces];   // a group is in its place in shared memory: 4 warps
   uint64_t r_empty[kPlaces];  // its channels of O^T are done
   uint64_t q;                 // Q written: 8 warps (once per token)
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(sh.r_full + i, 4);
       tc::mbar_init(sh.r_empty + i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 8; ++i) {
       tc::mbar_init(sh.raw + i, 1);
-      tc::mbar_init(sh.raw_read + i, 16);
+      tc::mbar_init(sh.raw_read + i, i % 4 ? 8 : 16);
     }
     tc::mbar_init(&sh.q, kSoftWarps);
     tc::mbar_init(&sh.s, 1);
@@ -451,33 +451,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       // What a missing run leaves behind is never used (its scales count as 0).
       const int run_shift = a.pages.shift < 7 ? a.pages.shift : 7;
       const int run = 1 << run_shift;
+      const auto aborted = [&] { return __any_sync(0xffffffffu, sh.abort != 0); };
+      uint32_t armed = 0;  // groups whose barrier expects a copy: nothing expects one that is not issued
 #pragma unroll 1
-      for (int32_t j = 0; j < n_run; ++j) {
+      for (int32_t j = 0; j < n_run && !aborted(); ++j) {
         const Info& info = info_of(j);
-        const int buf = j & 1;
-        if (j > 1) wait(sh.raw_read + buf, (uint32_t)(j >> 1) - 1u);
         // lane i: run i
         const int r0 = lane << run_shift;
         const int32_t page = r0 < kRows && r0 < info.rows ? info.page[r0 >> 4] : -1;
         const uint32_t there = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (lane == 0) tc::mbar_arrive_expect_tx(sh.raw + buf, there * (uint32_t)run * (kKvBytes + kKvScales));
-        __syncwarp();
-        if (page >= 0 && !sh.abort) {
-          const int64_t row = ((int64_t)page << a.pages.shift) + ((info.at + r0) & (a.pages.page_size() - 1));
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            tc::tma_load_2d(sm + kOffRaw + (4 * buf + g) * kRawGroup + r0 * 64, &rows_map, g * 64, (int32_t)row,
-                            sh.raw + buf);
-          tc::bulk_load(sm + kOffRawSc + (buf * kRows + r0) * kKvScales, a.kv_scale + row * kKvScales,
-                        (uint32_t)(run * kKvScales), sh.raw + buf);
+        const int64_t row = ((int64_t)page << a.pages.shift) + ((info.at + r0) & (a.pages.page_size() - 1));
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          const int at = 4 * (j & 1) + g;
+          if (j > 1) wait(sh.raw_read + at, (uint32_t)(j >> 1) - 1u);
+          if (aborted()) break;
+          if (lane == 0) tc::mbar_arrive_expect_tx(sh.raw + at, there * (uint32_t)run * (g ? 64 : 64 + kKvScales));
+          __syncwarp();
+          if (page >= 0) {
+            tc::tma_load_2d(sm + kOffRaw + at * kRawGroup + r0 * 64, &rows_map, g * 64, (int32_t)row, sh.raw + at);
+            // (tile j - 3 is done with its scales: its groups were waited for before tile j - 1's were copied)
+            if (g == 0)
+              tc::bulk_load(sm + kOffRawSc + (j % 3 * kRows + r0) * kKvScales, a.kv_scale + row * kKvScales,
+                            (uint32_t)(run * kKvScales), sh.raw + at);
+          }
+          __syncwarp();
+          ++armed;
         }
         info_done(j);
       }
       // (the last copies are waited for by the warps that read them; those may not
       // have when a wait ran out)
-      for (int32_t j = n_run > 1 ? n_run - 2 : 0; j < n_run && sh.abort; ++j)
-        for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.raw + (j & 1), (uint32_t)(j >> 1) & 1u); ++n) {
-        }
+      if (aborted())
+        for (uint32_t i = armed > 8 ? armed - 8 : 0; i < armed; ++i)
+          for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.raw + i % 8, (i / 8) & 1u); ++n) {
+          }
     }
     if ((warp == kSWarp || warp == kOWarp) && n_run > 0 && sh.abort) {
       // a wait ran out: products in flight end before tensor memory is freed
@@ -508,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.w[4 * k + 3] = v.w;
       }
       // (codes are finite whatever they are: times 0 they are zeros)
-      r.sc = *reinterpret_cast<const uint2*>(sm + kOffRawSc + ((t & 1) * kRows + my_row) * kKvScales + g * 8);
+      r.sc = *reinterpret_cast<const uint2*>(sm + kOffRawSc + (t % 3 * kRows + my_row) * kKvScales + g * 8);
       if (!seen) r.sc = make_uint2(0u, 0u);
     };
     // channels 32 q .. +31 of a group as fp16 (exact; zeros for zero codes and scales)
@@ -530,12 +538,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t t = 0; t < n_run; ++t) {
         const Info& info = info_of(t);
         const bool seen = my_row < info.rows && info.page[my_row >> 4] >= 0;
-        wait(sh.raw + (t & 1), (uint32_t)(t >> 1));
+        wait(sh.raw + 4 * (t & 1), (uint32_t)(t >> 1));
+        if (half) arrive(sh.raw_read + 4 * (t & 1));  // (its own groups' codes come apart)
 #pragma unroll 1
         for (int g = half; g < 4; g += 2) {
           Raw r;
+          if (g) wait(sh.raw + 4 * (t & 1) + g, (uint32_t)(t >> 1));
           take(r, t, g, seen);
-          if (g >= 2) arrive(sh.raw_read + (t & 1));
+          arrive(sh.raw_read + 4 * (t & 1) + g);
           const uint32_t n = 4u * (uint32_t)t + (uint32_t)g, use = n / kPlacesA, place = n - use * kPlacesA;
           if (use > 0) wait(sh.empty + place, use - 1u);
           tc::tc_fence_after();
@@ -559,12 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t t = 0; t < n_run; ++t) {
         const Info& info = info_of(t);
         const bool seen = my_row < info.rows && info.page[my_row >> 4] >= 0;
-        wait(sh.raw + (t & 1), (uint32_t)(t >> 1));
+        wait(sh.raw + 4 * (t & 1), (uint32_t)(t >> 1));
+        if (half) arrive(sh.raw_read + 4 * (t & 1));  // (its own groups' codes come apart)
 #pragma unroll 1
         for (int g = half; g < 4; g += 2) {
           Raw r;
+          if (g) wait(sh.raw + 4 * (t & 1) + g, (uint32_t)(t >> 1));
           take(r, t, g, seen);
-          if (g >= 2) arrive(sh.raw_read + (t & 1));
+          arrive(sh.raw_read + 4 * (t & 1) + g);
           const uint32_t use = 2u * (uint32_t)t + (uint32_t)(g >> 1);
           if (use > 0) wait(sh.r_empty + half, use - 1u);
           uint8_t* blk = sR + half * (2 * kBlkR);
