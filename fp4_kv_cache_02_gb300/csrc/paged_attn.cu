@@ -331,11 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (Counted, not timed, and kept short: the code of all roles together has to
   // stay in the instruction cache.)
   const auto wait = [&](uint64_t* bar, uint32_t par) {
-    uint32_t n = 0;
-    while (!tc::mbar_try_wait(bar, par & 1u)) {
-      if (sh.abort || ++n >= (1u << 22)) {
-        sh.abort = 1;
-        break;
+    if (!tc::mbar_try_wait(bar, par & 1u)) {
+      uint32_t n = 0;
+      while (!tc::mbar_try_wait_sleep(bar, par & 1u, 200u)) {
+        if (sh.abort || ++n >= (1u << 22)) {
+          sh.abort = 1;
+          break;
+        }
       }
     }
     __syncwarp();
