@@ -10,6 +10,9 @@
 // 16-byte vector loads. The fused KV append (a new entry's main-KV latent,
 // quantised after RoPE, and its indexer key, written at the sequence's next
 // position) uses one warp per entry and the same block encoders.
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
 #include "codec_blocks.cuh"
 
 namespace csa2 {
@@ -36,24 +39,18 @@ __global__ void quant_mxfp4_kernel(const uint16_t* __restrict__ x, int64_t n_blo
   e8m0[blk] = e;
 }
 
+// One thread per four values, so that a warp stores 512 contiguous bytes (one
+// thread per block stored 16 of every 128 at a time: 77,808 x 128 values took
+// 13.0 us against 8.2).
 __global__ void dequant_mxfp4_kernel(const uint8_t* __restrict__ data,
-                                     const uint8_t* __restrict__ e8m0, int64_t n_blocks,
+                                     const uint8_t* __restrict__ e8m0, int64_t n_quads,
                                      float* __restrict__ out) {
-  int64_t blk = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (blk >= n_blocks) return;
-  uint4 v = *reinterpret_cast<const uint4*>(data + blk * 16);
-  float s = e8m0_to_f32(e8m0[blk]);
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float4* dst = reinterpret_cast<float4*>(out + blk * 32);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t b = w[i] >> (16 * j);
-      dst[2 * i + j] = make_float4(e2m1_to_f32(b & 0xF) * s, e2m1_to_f32((b >> 4) & 0xF) * s,
-                                   e2m1_to_f32((b >> 8) & 0xF) * s, e2m1_to_f32((b >> 12) & 0xF) * s);
-    }
-  }
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n_quads) return;
+  const uint32_t b = reinterpret_cast<const uint16_t*>(data)[i];
+  const float s = e8m0_to_f32(e8m0[i >> 3]);
+  reinterpret_cast<float4*>(out)[i] = make_float4(e2m1_to_f32(b & 0xF) * s, e2m1_to_f32((b >> 4) & 0xF) * s,
+                                                  e2m1_to_f32((b >> 8) & 0xF) * s, e2m1_to_f32(b >> 12) * s);
 }
 
 // ---- main KV: one thread per 16-channel block ----------------------------------
@@ -71,29 +68,26 @@ __global__ void pack_kv_fp4_kernel(const uint16_t* __restrict__ x, int64_t n_blo
   kv_scale[blk] = sc;
 }
 
+// One thread per half block, 16 contiguous bytes of the output (77,808 entries:
+// 20.1 us; 24.5 with a thread per block, which stores 16 of every 32 bytes at a time).
 __global__ void unpack_kv_fp4_kernel(const uint8_t* __restrict__ kv_data,
-                                     const uint8_t* __restrict__ kv_scale, int64_t n_blocks,
+                                     const uint8_t* __restrict__ kv_scale, int64_t n_halves,
                                      uint16_t* __restrict__ out) {
-  int64_t blk = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (blk >= n_blocks) return;
-  uint2 v = *reinterpret_cast<const uint2*>(kv_data + blk * 8);
-  float s = e4m3_to_f32(kv_scale[blk]);
-  uint32_t w[2] = {v.x, v.y};
-  uint32_t o[8];
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n_halves) return;
+  const uint32_t w = reinterpret_cast<const uint32_t*>(kv_data)[i];
+  const float s = e4m3_to_f32(kv_scale[i >> 1]);
+  uint32_t v[4], o[4];
+  attn_tc::e2m1x8_to_f16(w, v[0], v[1], v[2], v[3]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t b = (w[i] >> (8 * j)) & 0xFFu;
-      // product of an E2M1 value and an E4M3 scale has <= 6 significant bits:
-      // exact in bf16, so the round-to-nearest conversion is exact
-      __nv_bfloat162 p = __floats2bfloat162_rn(e2m1_to_f32(b & 0xF) * s, e2m1_to_f32(b >> 4) * s);
-      o[4 * i + j] = *reinterpret_cast<uint32_t*>(&p);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+    // product of an E2M1 value and an E4M3 scale has <= 6 significant bits:
+    // exact in bf16, so the round-to-nearest conversion is exact
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f.x * s, f.y * s);
+    o[j] = *reinterpret_cast<const uint32_t*>(&p);
   }
-  uint4* dst = reinterpret_cast<uint4*>(out + blk * 16);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  reinterpret_cast<uint4*>(out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // ---- FP8 E4M3: one thread per 8 elements (tail handled elementwise) -------------
@@ -358,7 +352,7 @@ extern "C" int csa2_dequant_mxfp4(const uint8_t* data, const uint8_t* e8m0, int6
   if (!csa2_aligned(data, 16) || !csa2_aligned(out, 16)) return CSA2_ERR_ALIGNMENT;
   int64_t nb = rows * (cols / 32);
   if (nb == 0) return CSA2_OK;
-  dequant_mxfp4_kernel<<<grid_for(nb, 256), 256, 0, (cudaStream_t)stream>>>(data, e8m0, nb, out);
+  dequant_mxfp4_kernel<<<grid_for(nb * 8, 256), 256, 0, (cudaStream_t)stream>>>(data, e8m0, nb * 8, out);
   CSA2_CHECK_LAUNCH();
   return CSA2_OK;
 }
@@ -381,8 +375,8 @@ extern "C" int csa2_unpack_kv_fp4(const uint8_t* kv_data, const uint8_t* kv_scal
   if (!csa2_aligned(kv_data, 8) || !csa2_aligned(out_bf16, 16)) return CSA2_ERR_ALIGNMENT;
   int64_t nb = n * (kHeadDim / 16);
   if (nb == 0) return CSA2_OK;
-  unpack_kv_fp4_kernel<<<grid_for(nb, 256), 256, 0, (cudaStream_t)stream>>>(
-      kv_data, kv_scale, nb, (uint16_t*)out_bf16);
+  unpack_kv_fp4_kernel<<<grid_for(nb * 2, 256), 256, 0, (cudaStream_t)stream>>>(
+      kv_data, kv_scale, nb * 2, (uint16_t*)out_bf16);
   CSA2_CHECK_LAUNCH();
   return CSA2_OK;
 }
