@@ -533,8 +533,8 @@ def csa2_rope(x, rope, positions, out, interleaved=False, inverse=False, stream=
     rope_at, n_rope, rope_dim = _rope_table(rope, dev)
     n, heads, dim = shape
     _call("csa2_rope", x_at, n, heads, dim, rope_at, n_rope, rope_dim,
-          _optional(positions, torch.int32, (n,), "positions", dev), 1 if interleaved else 0, 1 if inverse else 0, out_at,
-          _s(stream))
+          _optional(positions, torch.int32, (n,), "positions", dev), 1 if interleaved else 0, 1 if inverse else 0,
+          out_at, _s(stream))
 
 
 def csa2_paged_kv_append(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_table, n_visible, n_visible_out=None,
@@ -549,8 +549,8 @@ def csa2_paged_kv_append(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_tabl
     if kv.shape != (n, HEAD_DIM) or ik.shape != (n, IDX_DIM):
         raise ValueError("kv must be [n_tokens, 512] and ik [n_tokens, 128]")
     at, n_pages, page, table, B, max_pages, counts = _pool(
-        dev, ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"), (ik_scale, 4, "ik_scale")),
-        page_table, n_visible)
+        dev, ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"),
+              (ik_scale, 4, "ik_scale")), page_table, n_visible)
     rope_at, n_rope, rope_dim = (None, 0, 0) if rope is None else _rope_table(rope, dev)
     _call("csa2_paged_kv_append", kv_at, ik_at, n, _optional(cu_tokens, torch.int32, (B + 1,), "cu_tokens", dev), B,
           rope_at, n_rope, rope_dim, _optional(positions, torch.int32, (n,), "positions", dev), 1 if interleaved else 0,
@@ -604,7 +604,8 @@ def csa2_paged_sparse_attn_decode(q, kv_data, kv_scale, page_table, n_visible, i
             raise ValueError("swa must be [B, L, n_swa, 512]")
     _call("csa2_paged_sparse_attn_decode", q_at, B, L, *at, n_pages, page, table, max_pages, counts, idx_at,
           idx.shape[1], swa_at, n_swa, float(sm_scale), _shaped(out, torch.bfloat16, shape, "out", dev),
-          _optional(out_f32, torch.float32, shape, "out_f32", dev), _optional(lse, torch.float32, shape[:3], "lse", dev),
+          _optional(out_f32, torch.float32, shape, "out_f32", dev),
+          _optional(lse, torch.float32, shape[:3], "lse", dev),
           ws_at, workspace.numel(), _s(stream))
 
 
@@ -621,8 +622,9 @@ def csa2_paged_attn(q, kv_data, kv_scale, page_table, n_visible, out, workspace,
     if len(shape) != 3 or shape[1] != HEADS or shape[2] != HEAD_DIM:
         raise ValueError("q must be [n_tokens, 64, 512]")
     _call("csa2_paged_attn", q_at, shape[0], _optional(cu_q, torch.int32, (B + 1,), "cu_q", dev), B, *at, n_pages, page,
-          table, max_pages, counts, 1 if causal else 0, float(sm_scale), _shaped(out, torch.bfloat16, shape, "out", dev),
-          _optional(out_f32, torch.float32, shape, "out_f32", dev), _optional(lse, torch.float32, shape[:2], "lse", dev),
+          table, max_pages, counts, 1 if causal else 0, float(sm_scale),
+          _shaped(out, torch.bfloat16, shape, "out", dev), _optional(out_f32, torch.float32, shape, "out_f32", dev),
+          _optional(lse, torch.float32, shape[:2], "lse", dev),
           ws_at, workspace.numel(), _s(stream))
 
 

@@ -114,7 +114,9 @@ struct Params {
 __device__ __forceinline__ bool paged_share(const Params& p, int lane, int& b, int& chunk, int& n_chunks) {
   const int B = p.B;
   if (p.spread == 0) {
-    b = (int)(blockIdx.x % (uint32_t)B), chunk = (int)(blockIdx.x / (uint32_t)B), n_chunks = (int)(gridDim.x / (uint32_t)B);
+    b = (int)(blockIdx.x % (uint32_t)B);
+    chunk = (int)(blockIdx.x / (uint32_t)B);
+    n_chunks = (int)(gridDim.x / (uint32_t)B);
     return true;
   }
   const int spare = (int)gridDim.x - B;
@@ -314,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int run = 1 << run_shift;
     const int g = lane >> 3, j = lane & 7;
     const int32_t* places = p.pages.table + (int64_t)b * p.pages.max_pages;
-    // Seven eighths of the tiles are fixed ranges, the last eighth is claimed:
-    // that evens out the CTAs' different shares of the bandwidth (28.8 us over 32 sequences of
-    // 65,536 entries; 29.4
-    // with three quarters fixed, 31.4 with six tiles each, 30.5 with all fixed).
+    // Seven eighths of the tiles are fixed ranges, the last eighth is claimed: that
+    // evens out the CTAs' different shares of the bandwidth (28.8 us over 32
+    // sequences of 65,536 entries; 29.4 with three quarters fixed, 31.4 with six
+    // tiles each, 30.5 with all fixed).
     const int64_t part = (int64_t)t_vis * 7 / 8 / n_chunks;
     const int64_t own = !claimed || n_chunks == 1 ? per : part > 0 ? part : 1;
     const int64_t fixed0 = (int64_t)chunk * own;
@@ -341,7 +343,9 @@ __global__ void __launch_bounds__(kThreads, 3)
       return t;
     };
     // (a pair of the fixed range ends with the range: the tile behind it is another CTA's)
-    const auto end_of = [&](int32_t t) { return t < fixed_end && t >= fixed0 ? fixed_end : claimed ? (int64_t)t_vis : 0; };
+    const auto end_of = [&](int32_t t) {
+      return t < fixed_end && t >= fixed0 ? fixed_end : claimed ? (int64_t)t_vis : 0;
+    };
     const auto row_of = [&](int32_t t) { return ((int64_t)t + g) * kTileRows + (int64_t)j * run; };
     const auto wanted = [&](int32_t t) {
       return g < 2 && j < (kTileRows >> run_shift) && (int64_t)t + g < end_of(t) && row_of(t) < nv;

@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   }
   const float sign = a.inverse ? -1.0f : 1.0f;
   for (int u = 0; u < kRopeRows * a.units; u += 32) {
-    const int r = min((u + lane) / a.units, kRopeRows - 1), c = (u + lane - r * a.units) * 8;  // place in the turned part
+    const int r = min((u + lane) / a.units, kRopeRows - 1);
+    const int c = (u + lane - r * a.units) * 8;  // place in the turned part
     const int64_t at_pos = __shfl_sync(0xffffffffu, pos, r);
     if (c >= a.units * 8 || at_pos < 0) continue;
     const int64_t at = (int64_t)r * a.dim + (a.dim - a.rope_dim) + c;

@@ -17,8 +17,25 @@
 //
 // What bounds it: an entry costs 288 bytes and, per token, 131,072 FLOP, so the
 // tensor cores (fp16) bind before HBM already at one token per sequence. With
-// 64 heads on N, an SM's shared memory does: per tile it takes 128 KiB of
-// writes (the dequantised rows) and 384 KiB of operand reads.
+// 64 heads on N they take 2,560 cycles a tile: S^T with the rows from tensor
+// memory 1,024 (32 a product, 48 from shared memory), O^T 1,536 (48: A and B
+// both from shared memory). Beside them a tile costs 2,858 wavefronts of shared
+// memory (the rows as fp16 written once, the codes read twice, P, the waits) and
+// 2,700 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
+// Measured 4,700 to 4,950 cycles a tile: 32 sequences of 65,536 entries 291 us
+// (942 TFLOP/s, 48 % of the measured bf16 rate; 2.1 TB/s), 2,048 tokens of a
+// prompt behind 6,144 entries 1.95 ms (983 TFLOP/s), 24 sequences of 1 to 4
+// tokens over up to 16,385 entries 115 us, one token over 317 entries 17 us.
+// Of those 17, 2.5 are the set-up, 3 the queries, 5 the tile's chain, 2 the
+// output and 4 the joining kernel.
+//
+// Tried and not kept (us for the 32 sequences at the time): all 16 warps in one
+// role after another 470, with S^T from tensor memory 429; one warp for both
+// products 549 (an issue blocks while the queue is full); rows by cp.async into
+// private staging 418 (347 by tensor copies); eight warps that dequantise for S
+// and O in turn 317 against 302 apart; every group by all eight of a set 303
+// against 291 (twice the waits, 250 cycles each under load); one loop for both
+// sets 330 against 295.
 //
 // Work split: the tiles of all tokens in batch order form one list, cut into
 // one equal run per SM. A run may begin and end inside a token; the parts of
@@ -45,11 +62,12 @@ using attn_tc::mul_f16x2;
 using attn_tc::named_barrier;
 using attn_tc::warp_transpose_reduce16;
 
-// Roles: warps 0 .. 7 take the softmax and the outputs, 8 .. 15 load and
-// dequantise, 16 and 17 issue the products for S^T and for O^T, 18 walks the
-// list and looks pages up, 19 copies the rows into shared memory. A warp's
-// tensor-memory lanes are the quadrant warp % 4; the two warps of a quadrant in a
-// role share its rows by heads (softmax) or channels (dequantisation).
+// Roles: warps 0 .. 7 take the softmax and the outputs, 8 .. 15 dequantise for
+// S^T and 16 .. 23 for O^T, 24 and 25 issue the products for S^T and for O^T, 26
+// walks the list and looks pages up, 27 copies the rows into shared memory. A
+// warp's tensor-memory lanes are the quadrant warp % 4; the two warps of a
+// quadrant in a role share its rows by heads (softmax) or by every second group
+// of channels (dequantisation).
 constexpr int kSoftWarps = 8, kFeedS = 8, kFeedO = 16, kSWarp = 24, kOWarp = 25, kWalkWarp = 26, kCopyWarp = 27;
 constexpr int kThreads = 896;
 constexpr int kWarps = kThreads / 32;
@@ -327,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A wait that runs out (2^22 tries, a tenth of a second at least) raises
   // sh.abort, on which every later wait gives up at once and nothing more is
   // issued. The loops then run to their ends all the same, so that no warp is
-  // missing at a barrier; the outputs are worthless and TIMEOUT is recorded.
+  // missing at a barrier, but write no more outputs (an Info that was not waited
+  // for names no token), and TIMEOUT is recorded.
   // (Counted, not timed, and kept short: the code of all roles together has to
   // stay in the instruction cache.)
   const auto wait = [&](uint64_t* bar, uint32_t par) {
@@ -360,11 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // The two issuing warps. An issue blocks while the tensor pipe's queue is
     // full, and S^T of a tile and O^T of the one before depend on different
-    // things: one warp for both waited for each in turn (measured 8,700 cycles a
-    // tile, of which the products are 2,560). The votes say what is so: every
-    // branch around the products is the whole warp's. Only then does the compiler
-    // keep their operands in uniform registers; else each product costs moves
-    // there, 80 to 100 cycles against the 32 or 48 of the tensor pipe.
+    // things: one warp for both would wait for each in turn. The votes say what is
+    // so: every branch around the products is the whole warp's. Only then does the
+    // compiler keep their operands in uniform registers; else each product costs
+    // moves there, 80 to 100 cycles against the 32 or 48 of the tensor pipe.
     const auto all = [](bool c) { return __any_sync(0xffffffffu, c) != 0; };
     const uint32_t elected = tc::elect_one();
     if (warp == kSWarp) {
@@ -501,8 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- dequantise: a thread takes the channels of groups half and half + 2
     // (128 each: 64 bytes of codes, 8 of scales) of its row from where the copies
     // put them, eight warps into tensor memory for S^T and eight into shared
-    // memory for O^T. (One set of eight for both read the codes once but had each
-    // conversion wait for the last: XX cycles a tile.) ----
+    // memory for O^T. (Plain loads from the pool into registers made a warp wait
+    // for them at the next use of their scoreboard, 3,400 cycles a tile.) The
+    // codes are given back as soon as they are in registers: the next tile's
+    // copies do not wait for this tile's products ----
     struct Raw {
       uint32_t w[16];
       uint2 sc;
@@ -608,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 16-byte columns c and c + 4 of each 64-channel block, in two passes (the
       // second from L1: all its 64 words would not fit the registers)
       auto write_q = [&](int64_t token) {
+        if (sh.abort) token = 0;
         const int h = tid >> 2, c = tid & 3;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (token * kHeads + h) * kHeadDim) + c;
         uint32_t amax = 0;
@@ -776,9 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < 16) sh.red[quad][h0 + u + lane] = lsum;
           }
           named_barrier(8, kSoftWarps * 32);
-          const bool complete = whole && last_of_token;
+          const bool complete = whole && last_of_token, lost = sh.abort != 0;
           const int64_t token = info.token;
-          if (tid < kHeads) {
+          if (tid < kHeads && !lost) {
             const float l = sh.red[0][tid] + sh.red[1][tid] + sh.red[2][tid] + sh.red[3][tid];
             sh.up[tid] = !complete ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
             if (!complete) a.part_ml[(int64_t)slot * kHeads + tid] = make_float2(sh.ref[tid], l);
@@ -793,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&sh.o, (uint32_t)j);  // O^T of this tile is complete
           tc::tc_fence_after();
 #pragma unroll 1
-          for (int x = 0; x < 8; ++x) {  // channel block 2 half + x / 4, heads 16 (x % 4) ..
+          for (int x = 0; x < 8 && !lost; ++x) {  // channel block 2 half + x / 4, heads 16 (x % 4) ..
             const int mb = 2 * half + (x >> 2), hh = (x & 3) * 16;
             const int c = 128 * mb + my_row;
             uint32_t ov[16];
@@ -815,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // every block of O^T is read before the next token's products replace it
           tc::tc_fence_before();
-          if (tid == 0 && whole && !last_of_token) {
+          if (tid == 0 && whole && !last_of_token && !lost) {
             // the token's first part: its other parts lie with the next CTAs
             const int64_t last = f1 - 1 + info.left;  // the token's last tile in the list
             PartList pl;
@@ -852,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // works out the weights for itself, so that a block only meets for its two sums:
 // a split token has two parts more often than many, and there may be one per SM
 // (64 heads of each), so the chain of dependent reads of an item is what counts.
-// (One block of 512 threads per item with the weights in shared memory: 70 us
-// after 2,048 tokens of one prompt, against XX.)
+// (Blocks of 512 threads, two per SM, with the weights in shared memory took 70
+// us after 2,048 tokens of one prompt; all of these calls are 4 to 12 % faster.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBlocks = 8;  // per SM
 
@@ -1057,7 +1078,7 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   cudaStream_t s = (cudaStream_t)stream;
   CSA2_LAUNCH_PDL(pattn::paged_attn_kernel, dim3((unsigned)G), dim3(pattn::kThreads), (size_t)pattn::kSmemBytes, s,
                   rows_map, a);
-  CSA2_LAUNCH_PDL(pattn::paged_attn_join_kernel, dim3((unsigned)(pattn::kJoinBlocks * G)), dim3(pattn::kJoinThreads), (size_t)0, s, a,
-                  (int32_t)G);
+  CSA2_LAUNCH_PDL(pattn::paged_attn_join_kernel, dim3((unsigned)(pattn::kJoinBlocks * G)), dim3(pattn::kJoinThreads),
+                  (size_t)0, s, a, (int32_t)G);
   return CSA2_OK;
 }

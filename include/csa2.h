@@ -657,7 +657,9 @@ int csa2_paged_kv_append(const void* kv_bf16, const void* ik_bf16,
  * pool (reported as DEVICE). n_pos <= max_pages * page_size.
  *   tile_counters: NULL, or [2 * B] int32 as in csa2_index_score_claimed (the
  *   CTAs of a sequence then claim its tiles; all zero before the first call,
- *   left zero by every call, one buffer per call that may run at the same time).
+ *   left zero by every call, one buffer per call that may run at the same time;
+ *   a negative counter is reported as DEVICE and the scores of that sequence are
+ *   not complete).
  * The scores feed csa2_topk and csa2_block_pool (with n_visible) as usual.
  * Errors: as csa2_index_score.
  */
