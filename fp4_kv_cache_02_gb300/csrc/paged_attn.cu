@@ -226,7 +226,8 @@ struct __align__(16) Shared {
   uint64_t raw_read[8];       // and been read: 8 warps (group 0's: waited for by all 16, for the scales)
   uint64_t r_full[kPlaces];   // a group is in its place in shared memory: 4 warps
   uint64_t r_empty[kPlaces];  // its channels of O^T are done
-  uint64_t q;                 // Q written: 8 warps (once per token)
+  uint64_t q_raw;             // a token's queries have arrived as they are
+  uint64_t q;                 // and are fp16: 8 warps
   uint64_t s;                 // S^T complete
   uint64_t s_read;            // S^T read: 8 warps
   uint64_t p;                 // P written, O^T rescaled (or read out): 8 warps
@@ -251,8 +252,29 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
   return r != 0;
 }
 
+// A token's queries on their way to q_smem, issued by the elected thread without
+// a branch (the issuing loop has to stay uniform).
+__device__ __forceinline__ void load_q_one(uint32_t elected, uint32_t q_smem, const CUtensorMap* map, int32_t token,
+                                           uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n\t}" ::"r"(elected),
+      "r"(tc::smem_u32(bar)), "r"(8 * kBlkQ)
+      : "memory");
+#pragma unroll
+  for (int b = 0; b < 8; ++b)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+        "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%1], "
+        "[%2, {%3, %4, %5}], [%6];\n\t}" ::"r"(elected),
+        "r"(q_smem + b * kBlkQ), "l"(reinterpret_cast<uint64_t>(map)), "r"(64 * b), "r"(0), "r"(token),
+        "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap rows_map, Args a) {
+    paged_attn_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap q_map,
+                      Args a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sR = sm + kOffR;
   uint8_t* sQ = sm + kOffQ;
@@ -275,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(sh.raw + i, 1);
       tc::mbar_init(sh.raw_read + i, i % 4 ? 8 : 16);
     }
+    tc::mbar_init(&sh.q_raw, 1);
     tc::mbar_init(&sh.q, kSoftWarps);
     tc::mbar_init(&sh.s, 1);
     tc::mbar_init(&sh.s_read, kSoftWarps);
@@ -385,16 +408,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // moves there, 80 to 100 cycles against the 32 or 48 of the tensor pipe.
     const auto all = [](bool c) { return __any_sync(0xffffffffu, c) != 0; };
     const uint32_t elected = tc::elect_one();
+    uint32_t tokens = 0;  // of the run, begun by the warp that issues S^T
     if (warp == kSWarp) {
       constexpr uint32_t idesc = idesc_f16(128, 64, 0, 0);
       const uint32_t q_lo = tc::smem_u32(sQ);
       uint32_t place = 0, use = 0;  // the ring's next place, and how often it went round
-      uint32_t tokens = 0;
 #pragma unroll 1
       for (int32_t j = 0; all(j < n_run); ++j) {
-        if (all(info_of(j).at == 0 || j == 0)) wait(&sh.q, tokens++);
+        const Info& info = info_of(j);
         if (all(j > 0)) wait(&sh.s_read, (uint32_t)(j - 1));
         if (all(sh.abort != 0)) break;
+        if (all(info.at == 0 || j == 0)) {
+          // a new token: its queries take the place of the last one's (S^T of whose
+          // last tile has been read, so it is complete) while that token's last
+          // softmax runs
+          load_q_one(elected, q_lo, &q_map, info.token, &sh.q_raw);
+          wait(&sh.q, tokens++);
+          if (all(sh.abort != 0)) break;
+        }
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {  // channels 128 g ..
           wait(sh.full + place, use);
@@ -462,6 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           to.token = w.seq.first + w.tok;
           to.left = w.tiles - 1 - w.tile;
         }
+        // (a later token's queries into L2, up to kRing tiles before they are needed)
+        if (lane == 0 && j > 0 && w.tile == 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.q + (int64_t)to.token * kPartFloats),
+                       "r"(kPartFloats * 2)
+                       : "memory");
         arrive(sh.info_full + j % kRing);
         if (j + 1 < n_run) w.step(a);
       }
@@ -511,6 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a wait ran out: products in flight end before tensor memory is freed
       tc::mma_commit_one(elected, sh.end + (warp - kSWarp));
       for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.end + (warp - kSWarp), 0); ++n) {
+      }
+      for (uint32_t n = 0; n < (1u << 22) && tokens > 0 && !tc::mbar_try_wait(&sh.q_raw, (tokens - 1u) & 1u); ++n) {
       }
       __syncwarp();
     }
@@ -623,50 +661,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n_run > 0) {
       // ---- softmax: a thread takes heads 32 half .. +31 of its row ----
       const int h0 = half * 32;
-      // the token's queries as fp16 with a power-of-two scale per head (exact but
-      // for values below 2^-28 of the head's largest): thread (h, c) takes the
-      // 16-byte columns c and c + 4 of each 64-channel block, in two passes (the
-      // second from L1: all its 64 words would not fit the registers)
-      auto write_q = [&](int64_t token) {
-        if (sh.abort) token = 0;
-        const int h = tid >> 2, c = tid & 3;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (token * kHeads + h) * kHeadDim) + c;
-        uint32_t amax = 0;
+      // the token's queries, once they have arrived, as fp16 with a power-of-two
+      // scale per head (exact but for values below 2^-28 of the head's largest), in
+      // place: eight threads to a head, thread c with the 16-byte column c of each
+      // 64-channel block (eight bank groups a row); 32 heads, then the other 32
+      auto convert_q = [&](uint32_t token) {
+        wait(&sh.q_raw, token);
 #pragma unroll 1
-        for (int k = 0; k < 8; k += 4) {
+        for (int h = tid >> 3; h < kHeads; h += 32) {
+          uint8_t* at = sQ + tc::sw128_offset((uint32_t)h, (uint32_t)tid & 7u);
+          uint32_t m2 = 0;  // the largest of the even and of the odd channels
           uint4 v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = src[(k + (i >> 1)) * 8 + (i & 1) * 4];
+          for (int b = 0; b < 8; ++b) v[b] = *reinterpret_cast<const uint4*>(at + b * kBlkQ);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+          for (int b = 0; b < 8; ++b) {
+            m2 = __vmaxu2(__vmaxu2(m2, v[b].x & 0x7FFF7FFFu), v[b].y & 0x7FFF7FFFu);
+            m2 = __vmaxu2(__vmaxu2(m2, v[b].z & 0x7FFF7FFFu), v[b].w & 0x7FFF7FFFu);
           }
-        }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int k2 = 0;
-        if (amax != 0u) k2 = min(max(14 - ((int)(amax >> 7) - 127), -100), 100);
-        const float up = __int_as_float((127 + k2) << 23);
-#pragma unroll 1
-        for (int k = 0; k < 8; k += 2) {
-          uint4 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = src[(k + (i >> 1)) * 8 + (i & 1) * 4];
+          for (int o = 1; o < 8; o <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+          const uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
+          int k2 = 0;
+          if (amax != 0u) k2 = min(max(14 - ((int)(amax >> 7) - 127), -100), 100);
+          const float up = __int_as_float((127 + k2) << 23);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int b = 0; b < 8; ++b) {
+            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               o[e] = f32x2_to_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-            *reinterpret_cast<uint4*>(sQ + (k + (i >> 1)) * kBlkQ +
-                                      tc::sw128_offset((uint32_t)h, (uint32_t)(c + (i & 1) * 4))) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(at + b * kBlkQ) = make_uint4(o[0], o[1], o[2], o[3]);
           }
+          if ((tid & 7) == 0) sh.mul[h] = a.scale_log2 * __int_as_float((127 - k2) << 23);
         }
-        if (c == 0) sh.mul[h] = a.scale_log2 * __int_as_float((127 - k2) << 23);
         tc::fence_proxy_async_smem();
         arrive(&sh.q);
       };
@@ -675,7 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i) l_acc[i] = 0.0f;
       if (tid < kHeads) sh.ref[tid] = 0.0f;
-      write_q(info_of(0).token);
+      uint32_t tokens = 0;  // of the run, with queries converted
+      convert_q(tokens++);
       named_barrier(8, kSoftWarps * 32);  // mul, ref
       int slot = 2 * cta;               // where a part of the present token goes
       bool whole = info_of(0).at == 0;  // the CTA has the token from its first tile on
@@ -808,9 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.ref[tid] = 0.0f;
           }
           named_barrier(8, kSoftWarps * 32);
-          // S^T of the token is complete: the next token's queries, before its O^T
-          // is waited for
-          if (j + 1 < n_run) write_q(info_of(j + 1).token);
+          // the next token's queries have come meanwhile; its O^T only after them
+          if (j + 1 < n_run) convert_q(tokens++);
           wait(&sh.o, (uint32_t)j);  // O^T of this tile is complete
           tc::tc_fence_after();
 #pragma unroll 1
@@ -1073,11 +1102,21 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return CSA2_ERR_CUDA;
+  // the queries, in boxes of a token's 64 heads by 64 channels
+  CUtensorMap q_map;
+  cuuint64_t q_dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)kHeads, (cuuint64_t)n_tokens};
+  cuuint64_t q_strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)kHeadDim * kHeads * 2};
+  cuuint32_t q_box[3] = {64, (cuuint32_t)kHeads, 1};
+  cuuint32_t q_estr[3] = {1, 1, 1};
+  if (encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)q_bf16, q_dims, q_strides, q_box, q_estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return CSA2_ERR_CUDA;
   static Csa2PerDeviceOnce optin;
   if (csa2_smem_optin((const void*)pattn::paged_attn_kernel, pattn::kSmemBytes, optin) != CSA2_OK) return CSA2_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   CSA2_LAUNCH_PDL(pattn::paged_attn_kernel, dim3((unsigned)G), dim3(pattn::kThreads), (size_t)pattn::kSmemBytes, s,
-                  rows_map, a);
+                  rows_map, q_map, a);
   CSA2_LAUNCH_PDL(pattn::paged_attn_join_kernel, dim3((unsigned)(pattn::kJoinBlocks * G)), dim3(pattn::kJoinThreads),
                   (size_t)0, s, a, (int32_t)G);
   return CSA2_OK;
