@@ -22,12 +22,15 @@
 // both from shared memory). Beside them a tile costs 2,858 wavefronts of shared
 // memory (the rows as fp16 written once, the codes read twice, P, the waits) and
 // 2,700 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
-// Measured 4,700 to 4,950 cycles a tile: 32 sequences of 65,536 entries 291 us
-// (942 TFLOP/s, 48 % of the measured bf16 rate; 2.1 TB/s), 2,048 tokens of a
-// prompt behind 6,144 entries 1.95 ms (983 TFLOP/s), 24 sequences of 1 to 4
-// tokens over up to 16,385 entries 115 us, one token over 317 entries 17 us.
-// Of those 17, 2.5 are the set-up, 3 the queries, 5 the tile's chain, 2 the
-// output and 4 the joining kernel.
+// Measured 4,600 to 4,900 cycles a tile: 32 sequences of 65,536 entries 288 us
+// (954 TFLOP/s, 49 % of the measured bf16 rate; 2.1 TB/s), 2,048 tokens of a
+// prompt behind 6,144 entries 1.94 ms (994 TFLOP/s), 24 sequences of 1 to 4
+// tokens over up to 16,385 entries 108 us, one token over 317 entries 17 us (2.5
+// the set-up, 2 the queries, 5 the tile's chain, 2 the output, 4 the joining
+// kernel). A token costs 9,000 cycles beside its tiles, while the pipeline runs
+// empty and full again (its queries converted 1,500, the first references 2,400,
+// the output 3,600): four prompts of 512 tokens from their start, 2.5 tiles a
+// token, take 183 us, twice what their tiles would.
 //
 // Tried and not kept (us for the 32 sequences at the time): all 16 warps in one
 // role after another 470, with S^T from tensor memory 429; one warp for both
@@ -35,11 +38,16 @@
 // private staging 418 (347 by tensor copies); eight warps that dequantise for S
 // and O in turn 317 against 302 apart; every group by all eight of a set 303
 // against 291 (twice the waits, 250 cycles each under load); one loop for both
-// sets 330 against 295.
+// sets 330 against 295; a third place for O's groups and half the codes staged
+// 316 against 291; the queries converted by the warps that feed S^T 332 against
+// 291 (their loop then keeps less in registers).
 //
-// Work split: the tiles of all tokens in batch order form one list, cut into
-// one equal run per SM. A run may begin and end inside a token; the parts of
-// such a token go to the workspace and a second kernel joins them in order.
+// Work split: the tiles of all tokens in batch order form one list of units, cut
+// into one equal run per SM. A token's first tile counts kTokenUnits units more
+// than the others, about what a token costs beside its tiles (four prompts of 512
+// tokens: 248 us with none, 187 with one, 179 with two, 184 with three). A run
+// may begin and end inside a token; the parts of such a token go to the workspace
+// and a second kernel joins them in order.
 // Few long sequences and many short ones load the SMs alike, and the workspace
 // (two parts per SM) does not grow with the batch.
 #include <cudaTypedefs.h>
@@ -71,8 +79,8 @@ using attn_tc::warp_transpose_reduce16;
 constexpr int kSoftWarps = 8, kFeedS = 8, kFeedO = 16, kSWarp = 24, kOWarp = 25, kWalkWarp = 26, kCopyWarp = 27;
 constexpr int kThreads = 896;
 constexpr int kWarps = kThreads / 32;
-// Registers: 896 threads start with 72 each (64,512 in all).
-constexpr int kRegsSoft = 112, kRegsFeed = 56, kRegsIssue = 40;
+// Registers: 896 threads start with 72 each (64,512 in all, and all of them shared out).
+constexpr int kRegsSoft = 112, kRegsFeed = 56, kRegsIssue = 56;
 static_assert(256 * kRegsSoft + 512 * kRegsFeed + 128 * kRegsIssue <= kThreads * 72, "register split");
 constexpr int kRows = 128;
 constexpr int kPlacesA = 3, kPlaces = 2;  // rings of 128-channel groups of R, in tensor and in shared memory
@@ -106,7 +114,7 @@ struct PartList {
   int32_t token;       // -1: this CTA begins no such token
   int32_t first_slot;  // slot of the first part
   int32_t cta0, cta1;  // its first and last tile's CTAs
-  int64_t tiles;       // tiles of the whole call
+  int64_t units;       // of the whole call
 };
 
 struct Args {
@@ -128,6 +136,10 @@ struct Args {
 };
 
 // ---- the list of tiles --------------------------------------------------------
+// Unit u of a token with n tiles, u = 0 .. n + kTokenUnits - 1: tile i is at unit
+// i + kTokenUnits, the ones before belong to its first tile's cost. A CTA has the
+// tiles whose units are in its run.
+constexpr int kTokenUnits = 2;
 __device__ __forceinline__ int32_t tiles_of(int32_t visible) {  // a token without entries has one empty tile
   return visible <= kRows ? 1 : (int32_t)(((uint32_t)visible + kRows - 1) / kRows);
 }
@@ -162,22 +174,32 @@ __device__ __forceinline__ int64_t tiles_before(const Args& a, const Seq& s, int
   return blind + (hi > 0 ? tiles_upto(hi) - tiles_upto(v0 > 1 ? v0 - 1 : 0) : 0);
 }
 
+// The place of unit `at` of a sequence: its token, and how many of that token's
+// tiles lie before the unit.
+struct Place {
+  int32_t tok, tile;
+};
+__device__ __forceinline__ Place place_of(const Args& a, const Seq& s, int64_t at) {
+  int32_t lo = 0, hi = s.count;  // units before lo <= at < units before hi
+  while (hi - lo > 1) {
+    const int32_t mid = lo + (hi - lo) / 2;
+    if (tiles_before(a, s, mid) + (int64_t)kTokenUnits * mid <= at) lo = mid;
+    else hi = mid;
+  }
+  const int64_t off = at - tiles_before(a, s, lo) - (int64_t)kTokenUnits * lo - kTokenUnits;
+  return {lo, off > 0 ? (int32_t)off : 0};
+}
+
 // A walk along the list.
 struct Walk {
   int32_t b, tok;
   Seq seq;
   int32_t tile, visible, tiles;  // the place in the token, its entries and tiles
-  __device__ __forceinline__ void start(const Args& a, int32_t b_, int64_t at) {
+  __device__ __forceinline__ void start(const Args& a, int32_t b_, int32_t tok_, int32_t tile_) {
     b = b_;
     seq = load_seq(a, b, false);
-    int32_t lo = 0, hi = seq.count;  // tiles_before(lo) <= at < tiles_before(hi)
-    while (hi - lo > 1) {
-      const int32_t mid = lo + (hi - lo) / 2;
-      if (tiles_before(a, seq, mid) <= at) lo = mid;
-      else hi = mid;
-    }
-    tok = lo;
-    tile = (int32_t)(at - tiles_before(a, seq, lo));
+    tok = tok_;
+    tile = tile_;
     visible = visible_of(a, seq, tok);
     tiles = tiles_of(visible);
   }
@@ -213,9 +235,12 @@ struct __align__(16) Shared {
   float red[4][kHeads];   // per-quadrant maxima, then sums
   float up[kHeads];       // how far a reference moves; at a token's end what O^T is multiplied with
   float shrink[kHeads];   // what O^T and l shrink by when a reference moves
-  int64_t scan[kWarps];
-  int64_t at;             // first tile of the run, within its sequence
-  int32_t seq;            // the sequence of the run's first tile
+  int64_t scan[kWarps];   // tiles of the warps' sequences
+  int32_t scan_tok[kWarps];  // and tokens
+  int64_t tile0, tile1;   // tiles of the list before the run and at its end
+  int64_t units, end_unit;  // of the list; behind the run
+  Place first;            // the run's first tile, within its sequence
+  int32_t seq;            // that sequence
   uint32_t tmem;
   volatile int abort;
   // barriers. Those of a tile complete once per tile, so that tile j waits for
@@ -315,55 +340,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tc::tmem_alloc(&sh.tmem, kTmemCols);
   pdl_begin();
 
-  // ---- this CTA's run [f0, f1) of the list: a scan over the sequences' tiles,
-  // kThreads at a time. The total is known behind the last ones only, so where
-  // there are more sequences than threads they are gone through once more ----
-  int64_t total = 0, n = 0, lo = 0;  // lo: tiles before this thread's sequence, n: its own
+  // ---- this CTA's run [f0, f1) of the list's units: a scan over the sequences'
+  // tiles and tokens, kThreads at a time. The total is known behind the last ones
+  // only, so where there are more sequences than threads they are gone through
+  // once more ----
+  int64_t tiles = 0, n = 0, lo = 0;    // lo: tiles before this thread's sequence, n: its own
+  int32_t tokens_all = 0, lo_tok = 0;  // and tokens
+  Seq own{};
   const auto scan = [&](int32_t b, bool report) {
-    n = 0;
-    if (b < a.B) {
-      const Seq s = load_seq(a, b, report);
-      n = tiles_before(a, s, s.count);
-    }
+    own = b < a.B ? load_seq(a, b, report) : Seq{0, 0, 0};
+    n = tiles_before(a, own, own.count);
     int64_t incl = n;
+    int32_t incl_tok = own.count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int32_t w = __shfl_up_sync(0xffffffffu, incl_tok, o);
+      if (lane >= o) incl += v, incl_tok += w;
     }
-    if (lane == 31) sh.scan[warp] = incl;
+    if (lane == 31) sh.scan[warp] = incl, sh.scan_tok[warp] = incl_tok;
     __syncthreads();
     const int64_t of_warp = lane < kWarps ? sh.scan[lane] : 0;
+    const int32_t of_warp_tok = lane < kWarps ? sh.scan_tok[lane] : 0;
     int64_t before = of_warp;
+    int32_t before_tok = of_warp_tok;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += v;
+      const int32_t w = __shfl_up_sync(0xffffffffu, before_tok, o);
+      if (lane >= o) before += v, before_tok += w;
     }
-    lo = total + incl - n + __shfl_sync(0xffffffffu, before - of_warp, warp);
-    total += __shfl_sync(0xffffffffu, before, kWarps - 1);
+    lo = tiles + incl - n + __shfl_sync(0xffffffffu, before - of_warp, warp);
+    lo_tok = tokens_all + incl_tok - own.count + __shfl_sync(0xffffffffu, before_tok - of_warp_tok, warp);
+    tiles += __shfl_sync(0xffffffffu, before, kWarps - 1);
+    tokens_all += __shfl_sync(0xffffffffu, before_tok, kWarps - 1);
     __syncthreads();
   };
   for (int32_t b0 = 0; b0 < a.B; b0 += kThreads) scan(b0 + tid, cta == 0);
-  const int64_t all = total, f0 = all * cta / G, f1 = all * (cta + 1) / G;
-  if (tid == 0) a.lists[cta].token = -1;
-  if (f0 < f1) {
-    int32_t b0 = 0;
-    if (a.B > kThreads) {
-      total = 0;
-      for (; total <= f0; b0 += kThreads) scan(b0 + tid, false);
-      b0 -= kThreads;
+  const int64_t all = tiles + (int64_t)kTokenUnits * tokens_all, f0 = all * cta / G, f1 = all * (cta + 1) / G;
+  if (tid == 0) {
+    a.lists[cta].token = -1;
+    sh.tile0 = sh.tile1 = tiles;  // (a run that ends with the list)
+    sh.units = all;
+    sh.end_unit = f1;
+  }
+  __syncthreads();
+  const auto place = [&](int32_t b) {
+    const int64_t u = lo + (int64_t)kTokenUnits * lo_tok, end = u + n + (int64_t)kTokenUnits * own.count;
+    if (f0 >= u && f0 < end) {
+      const Place at = place_of(a, own, f0 - u);
+      sh.seq = b;
+      sh.first = at;
+      sh.tile0 = lo + tiles_before(a, own, at.tok) + at.tile;
     }
-    if (f0 >= lo && f0 < lo + n) {
-      sh.seq = b0 + tid;
-      sh.at = f0 - lo;
+    if (f1 >= u && f1 < end) {
+      const Place at = place_of(a, own, f1 - u);
+      sh.tile1 = lo + tiles_before(a, own, at.tok) + at.tile;
+    }
+  };
+  if (a.B <= kThreads) {
+    place(tid);
+  } else if (f0 < f1) {
+    tiles = 0;
+    tokens_all = 0;
+    for (int32_t b0 = 0; b0 < a.B && tiles + (int64_t)kTokenUnits * tokens_all <= f1; b0 += kThreads) {
+      scan(b0 + tid, false);
+      place(b0 + tid);
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int32_t n_run = (int32_t)(f1 - f0);  // tiles of this CTA (the host has checked the range)
+  // tiles of this CTA (the host has checked the range); reduced over equal values,
+  // so that the compiler knows it as the warp's: the loops below cost 3 % more else
+  const int32_t n_run = (int32_t)__reduce_max_sync(0xffffffffu, (uint32_t)(sh.tile1 - sh.tile0));
 
   // A wait that runs out (2^22 tries, a tenth of a second at least) raises
   // sh.abort, on which every later wait gives up at once and nothing more is
@@ -472,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kWalkWarp && n_run > 0) {
       Walk w;
-      w.start(a, sh.seq, sh.at);
+      w.start(a, sh.seq, sh.first.tok, sh.first.tile);
 #pragma unroll 1
       for (int32_t j = 0; j < n_run; ++j) {
         const int32_t e = w.tile * kRows + 16 * lane;
@@ -842,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < n_run) convert_q(tokens++);
           wait(&sh.o, (uint32_t)j);  // O^T of this tile is complete
           tc::tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
           for (int x = 0; x < 8 && !lost; ++x) {  // channel block 2 half + x / 4, heads 16 (x % 4) ..
             const int mb = 2 * half + (x >> 2), hh = (x & 3) * 16;
             const int c = 128 * mb + my_row;
@@ -867,14 +918,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tc_fence_before();
           if (tid == 0 && whole && !last_of_token && !lost) {
             // the token's first part: its other parts lie with the next CTAs
-            const int64_t last = f1 - 1 + info.left;  // the token's last tile in the list
+            const int64_t all = sh.units, last = sh.end_unit - 1 + info.left;  // the unit of the token's last tile
             PartList pl;
             pl.token = (int32_t)token;
             pl.first_slot = slot;
-            pl.cta0 = cta;
-            pl.cta1 = (int32_t)(((last + 1) * G + all - 1) / all - 1);
-            pl.tiles = all;
-            a.lists[cta] = pl;
+            pl.cta0 = (int32_t)blockIdx.x;
+            pl.cta1 = (int32_t)(((last + 1) * (int32_t)gridDim.x + all - 1) / all - 1);
+            pl.units = all;
+            a.lists[blockIdx.x] = pl;
           }
           first = true;
           open = true;
@@ -931,11 +982,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(Args a, i
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const PartList pl = a.lists[s_list[it / kHeads]];
     const int h = it % kHeads;
-    // Part j lies with the j-th CTA that has tiles: with fewer tiles than CTAs
-    // the one that holds tile first + j, else simply the next.
-    const bool sparse = pl.tiles < G;
-    const int64_t first = sparse ? pl.tiles * pl.cta0 / G : 0;
-    const int n = sparse ? (int)(pl.tiles * pl.cta1 / G - first) + 1 : pl.cta1 - pl.cta0 + 1;
+    // Part j lies with the j-th CTA that has tiles: with fewer units than CTAs
+    // the one that holds unit first + j, else simply the next.
+    const bool sparse = pl.units < G;
+    const int64_t first = sparse ? pl.units * pl.cta0 / G : 0;
+    const int n = sparse ? (int)(pl.units * pl.cta1 / G - first) + 1 : pl.cta1 - pl.cta0 + 1;
     float M = -INFINITY, L = 0.0f;  // L: this lane's share
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j0 = 0; j0 < n; j0 += 32) {
@@ -943,7 +994,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(Args a, i
       int slot = 0;
       float2 ml = make_float2(-INFINITY, 0.0f);
       if (j < n) {
-        const int c = sparse ? (int)(((first + j + 1) * G + pl.tiles - 1) / pl.tiles) - 1 : pl.cta0 + j;
+        const int c = sparse ? (int)(((first + j + 1) * G + pl.units - 1) / pl.units) - 1 : pl.cta0 + j;
         slot = j == 0 ? pl.first_slot : 2 * c;
         ml = a.part_ml[(int64_t)slot * kHeads + h];
       }
