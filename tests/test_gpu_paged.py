@@ -665,6 +665,64 @@ def test_dense_many_sequences(csa2):
         assert torch.all((f32[i].double() - o).abs() <= (2.0 ** -11 + 3 * d + 2.0 ** -18) * a + 1e-30), i
 
 
+def test_dense_many_ragged_sequences(csa2):
+    """More sequences than threads, zero to five tokens each, and two with counts that are refused."""
+    B = 1100
+    runs = [(7 * i) % 6 for i in range(B)]
+    lens = [(53 * i) % 400 for i in range(B)]
+    bad = {17: -1, 1043: 401}
+    c = Cache(csa2, [400] * 2, 16, 71)  # every sequence shares the pages of these two
+    table = c.table[torch.arange(B, device="cuda") % 2].contiguous()
+    n = sum(runs)
+    q = normal(gen(72), n, 64, 512, scale=512 ** -0.5)
+    out, f32 = torch.full_like(q, 7.0), torch.full(q.shape, 7.0, device="cuda")
+    csa2.csa2_paged_attn(q, c.kv_data, c.kv_scale, table, ints([bad.get(i, v) for i, v in enumerate(lens)]), out,
+                         csa2.paged_attn_workspace(n, B), cu_q=starts(runs), out_f32=f32)
+    assert csa2.csa2_get_last_error() == DEVICE_ERROR
+    rows = [c.latents(csa2, 0), c.latents(csa2, 1)]
+    at = 0
+    for b, T in enumerate(runs):
+        for j in range(T):
+            if b in bad:
+                assert torch.all(f32[at] == 7.0) and torch.all(out[at] == 7.0)
+            elif b % 53 == 0 or b > B - 4 or 894 <= b <= 898 or b in (16, 18, 1042, 1044):
+                o, _, a, d = dense_reference(q[at], rows[b % 2][:max(0, lens[b] - T + 1 + j)], 1.0)
+                assert torch.all((f32[at].double() - o).abs() <= (2.0 ** -11 + 3 * d + 2.0 ** -18) * a + 1e-30), (b, j)
+            at += 1
+
+
+@pytest.mark.parametrize("runs,past", [([300, 1, 0, 517, 2], 0), ([90, 700], 70), ([1] * 400, 3)])
+def test_dense_prompts_and_short_steps(csa2, runs, past):
+    """Tokens of one to seven tiles: runs of an SM that begin and end inside tokens and between them."""
+    lens = [T + (past if T > 1 else 5 * i + past) for i, T in enumerate(runs)]
+    c = Cache(csa2, lens, 32, 73 + past)
+    q = normal(gen(74), sum(runs), 64, 512, scale=512 ** -0.5)
+    got = run_dense(csa2, c, q, cu=starts(runs))
+    assert csa2.csa2_get_last_error() == 0
+    check_dense(csa2, c, q, runs, 0, True, 1.0, got)
+
+
+def test_dense_two_calls_at_once(csa2):
+    """Two streams with a workspace each, many times over, give the bits of the calls alone."""
+    calls = []
+    for i, (runs, lens) in enumerate([([4, 1, 9], [3000, 20, 700]), ([1] * 40, [150 + 7 * j for j in range(40)])]):
+        c = Cache(csa2, lens, 64, 75 + i)
+        q = normal(gen(77 + i), sum(runs), 64, 512, scale=512 ** -0.5)
+        alone = run_dense(csa2, c, q, cu=starts(runs))
+        outs = torch.empty_like(q), torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+        calls.append((c, q, starts(runs), alone, outs, csa2.paged_attn_workspace(q.shape[0], len(runs)), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, cu, _, (out, f32, lse), ws, stream in calls:
+            csa2.csa2_paged_attn(q, c.kv_data, c.kv_scale, c.table, c.n_visible, out, ws, cu_q=cu, out_f32=f32, lse=lse,
+                                 stream=stream)
+    torch.cuda.synchronize()
+    assert csa2.csa2_get_last_error() == 0
+    for _, _, _, alone, outs, _, _ in calls:
+        for x, y in zip(alone, outs):
+            assert torch.equal(x, y)
+
+
 def test_dense_rows_past_32_bits(csa2):
     """Pages whose bytes lie more than 2^32 behind the plane's start."""
     page, n = 128, 700
