@@ -138,6 +138,59 @@ class Cache:
         return out
 
 
+# ---- the latents' encoder --------------------------------------------------------
+
+
+def test_latent_codes_are_those_of_the_rounded_quotient(csa2):
+    """Codes and scales of blocks of every size of bf16, signed zeros and subnormals among them, against the quotients rounded
+    to fp32: the encoder divides by a corrected reciprocal."""
+    g = gen(3)
+    n = 1 << 14
+    bits = torch.randint(0, 1 << 16, (n, 512), generator=g, device="cuda", dtype=torch.int32)
+    # the blocks' values within a few octaves below a top that goes through all exponents
+    top = torch.randint(0, 0x7F80, (n, 32, 1), generator=g, device="cuda", dtype=torch.int32)
+    less = torch.randint(0, 4 << 7, (n, 32, 16), generator=g, device="cuda", dtype=torch.int32)
+    near = (bits.view(n, 32, 16) & 0x8000) | (top - less).clamp(min=0)
+    x = torch.where(torch.arange(n, device="cuda")[:, None, None] % 8 == 0, bits.view(n, 32, 16), near)
+    x = torch.where((x & 0x7F80) == 0x7F80, x & 0x8000, x)  # finite
+    v = (x << 16).view(torch.float32).view(n, 32, 16)
+    data, scale = csa2.pack_kv_fp4(v.view(n, 512).bfloat16())
+    amax = v.abs().amax(-1)
+    want = (amax / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    assert torch.equal(scale.view(torch.uint8).view(n, 32), want.view(torch.uint8))
+    s = want.float()[..., None]
+    quotient = v / torch.where(s > 0, s, torch.ones_like(s))
+    a = quotient.abs()
+    code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int() + (a >= 3.5).int()
+            + (a > 5.0).int() + 8 * torch.signbit(quotient).int())
+    code = torch.where(s > 0, code, torch.zeros_like(code)).view(n, 256, 2)
+    assert torch.equal(data.view(n, 256).int(), code[..., 0] + 16 * code[..., 1])
+
+
+def test_latent_codes_beside_infinities_and_nans(csa2):
+    """An infinity takes its block's scale to the largest and saturates; a NaN leaves its neighbours as they are."""
+    x = normal(gen(4), 3, 512)
+    plain, plain_scale = csa2.pack_kv_fp4(x)
+    y = x.clone()
+    y[0, 5], y[1, 37] = float("inf"), -float("inf")
+    y[2, 100] = float("nan")
+    data, scale = csa2.pack_kv_fp4(y)
+    codes = torch.stack([data & 15, data >> 4], -1).view(3, 512)
+    before = torch.stack([plain & 15, plain >> 4], -1).view(3, 512)
+    assert int(scale[0, 0]) == int(scale[1, 2]) == 0x7E
+    assert int(codes[0, 5]) == 7 and int(codes[1, 37]) == 15
+    rest = torch.ones(3, 512, dtype=torch.bool, device="cuda")
+    rest[0, :16], rest[1, 32:48], rest[2, 96:112] = False, False, False
+    assert torch.equal(codes[rest], before[rest])
+    z = x.clone()
+    z[2, 100] = 0.0
+    other, other_scale = csa2.pack_kv_fp4(z)
+    other = torch.stack([other & 15, other >> 4], -1).view(3, 512)
+    assert torch.equal(scale[2], other_scale[2])
+    kept = torch.arange(512, device="cuda") != 100
+    assert torch.equal(codes[2][kept], other[2][kept])
+
+
 # ---- append ----------------------------------------------------------------------
 
 
@@ -261,6 +314,37 @@ def test_append_passes_over_what_does_not_fit(csa2, mode):
     csa2.csa2_paged_kv_append(kv, ik, *planes, table[:2], nv, out, cu_tokens=ints([-3, 35, 20]))
     assert csa2.csa2_get_last_error() == DEVICE_ERROR and out.tolist() == [0, 0]
     assert all(torch.equal(a, b) for a, b in zip(planes, before))
+
+
+@pytest.mark.parametrize("rope_dim,interleaved", [(0, False), (64, True), (96, False), (128, True)])
+def test_append_of_many_tokens_equals_the_sequences_alone(csa2, rope_dim, interleaved):
+    """A call with several tokens to a warp writes what one call per sequence writes; rows of no sequence are not read."""
+    g = gen(13 + rope_dim)
+    runs = [30 + (97 * i * i + 5) % 301 for i in range(40)]
+    runs[3] = runs[20] = 0
+    runs[21] = 1
+    first, n = 3, sum(runs)
+    assert n > 5000
+    past = [(29 * i) % 70 for i in range(40)]
+    page = 32
+    table, pages = tables([a + t for a, t in zip(past, runs)], page, g)
+    kv, ik = normal(g, first + n + 6, 512), normal(g, first + n + 6, 128)
+    kv[:first] = kv[first + n:] = float("nan")
+    rope = angles(500, rope_dim) if rope_dim else None
+    kept = [torch.randint(0, 256, (pages, page, w), generator=g, device="cuda", dtype=torch.uint8) for w in (256, 32, 64, 4)]
+    together, alone = [p.clone() for p in kept], [p.clone() for p in kept]
+    out = torch.empty(40, dtype=torch.int32, device="cuda")
+    csa2.csa2_paged_kv_append(kv, ik, *together, table, ints(past), out, cu_tokens=starts(runs, first), rope=rope,
+                              interleaved=interleaved)
+    at = first
+    for b, t in enumerate(runs):
+        csa2.csa2_paged_kv_append(kv[at:at + t], ik[at:at + t], *alone, table[b:b + 1], ints(past[b:b + 1]), rope=rope,
+                                  interleaved=interleaved)
+        at += t
+    assert csa2.csa2_get_last_error() == 0
+    assert out.tolist() == [a + t for a, t in zip(past, runs)]
+    for a, b in zip(together, alone):
+        assert torch.equal(a, b)
 
 
 def test_append_of_nothing(csa2):
