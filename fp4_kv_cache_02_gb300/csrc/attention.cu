@@ -43,8 +43,7 @@ struct AttnArgs {
   uint16_t* out;            // [n_q][64][512] bf16
   float* out_f32;           // nullable
   float* lse;               // nullable
-  bool paged;               // idx names entries in pages: their rows of the plane are looked up
-  PageTable pages;
+  PageTable pages;          // kPaged: idx names entries in pages, their rows of the plane are looked up
   const int32_t* paged_visible;
 };
 
@@ -81,11 +80,15 @@ int csa2_read_and_clear_attn_error(cudaStream_t s) {
 
 // Opts the kernels into their dynamic shared memory, once per device.
 static int attn_kernel_attr() {
-  static Csa2PerDeviceOnce optin, optin_reuse, optin_seq;
+  static Csa2PerDeviceOnce optin, optin_reuse, optin_seq, optin_paged, optin_paged_seq;
   if (csa2_smem_optin((const void*)attn_tc::attn_tc_kernel<attn_tc::kModeCluster>, attn_tc::kSmemBytes, optin) !=
           CSA2_OK ||
       csa2_smem_optin((const void*)attn_tc::attn_tc_kernel<attn_tc::kModeSeq>, attn_tc::kSmemBytes, optin_seq) !=
-          CSA2_OK)
+          CSA2_OK ||
+      csa2_smem_optin((const void*)attn_tc::attn_tc_kernel<attn_tc::kModeCluster, true>, attn_tc::kSmemBytes,
+                      optin_paged) != CSA2_OK ||
+      csa2_smem_optin((const void*)attn_tc::attn_tc_kernel<attn_tc::kModeSeq, true>, attn_tc::kSmemBytes,
+                      optin_paged_seq) != CSA2_OK)
     return CSA2_ERR_CUDA;
   return csa2_smem_optin((const void*)attn_tc::attn_tc_kernel<attn_tc::kModeReuse>, attn_tc::kSmemBytes, optin_reuse);
 }
@@ -211,7 +214,7 @@ extern "C" int csa2_sparse_attn_kernel_launches(int32_t n_queries, int32_t k, in
 }
 
 static int launch_attn(AttnArgs a, const void* q_bf16, int32_t n_q, uint16_t* out, float* out_f32, float* lse,
-                       void* ws, size_t ws_bytes, cudaStream_t stream, bool reuse = false) {
+                       void* ws, size_t ws_bytes, cudaStream_t stream, bool reuse = false, bool paged = false) {
   if (attn_kernel_attr() != CSA2_OK) return CSA2_ERR_CUDA;
   AttnPlan plan = attn_plan(attn_queries_per_launch(n_q), a.k, a.n_swa, true);
   if (plan.n_part > attn_tc::kMaxPartials) return CSA2_ERR_UNSUPPORTED_SHAPE;
@@ -258,8 +261,10 @@ static int launch_attn(AttnArgs a, const void* q_bf16, int32_t n_q, uint16_t* ou
   for (int32_t q0 = 0; q0 < n_q; q0 += kQueriesPerLaunch) {
     const int32_t nq = n_q - q0 < kQueriesPerLaunch ? n_q - q0 : kQueriesPerLaunch;
     a.q0 = q0;
-    const auto kern = plan.seq ? attn_tc::attn_tc_kernel<attn_tc::kModeSeq>
-                               : attn_tc::attn_tc_kernel<attn_tc::kModeCluster>;
+    const auto kern = paged ? (plan.seq ? attn_tc::attn_tc_kernel<attn_tc::kModeSeq, true>
+                                        : attn_tc::attn_tc_kernel<attn_tc::kModeCluster, true>)
+                      : plan.seq ? attn_tc::attn_tc_kernel<attn_tc::kModeSeq>
+                                 : attn_tc::attn_tc_kernel<attn_tc::kModeCluster>;
     if (csa2_launch_pdl_cluster(kern, dim3((unsigned)plan.cluster, (unsigned)nq), dim3(attn_tc::kThreads),
                                 (size_t)attn_tc::kSmemBytes, stream, (unsigned)plan.cluster, qmap, a) != cudaSuccess) {
       (void)cudaGetLastError();
@@ -393,7 +398,6 @@ extern "C" int csa2_paged_sparse_attn_decode(const void* q_bf16, int32_t B, int3
   a.kv_seq_stride = 0;
   a.n_visible = nullptr;
   a.nv_const = n_pages << pages.shift;
-  a.paged = true;
   a.pages = pages;
   a.paged_visible = n_visible;
   a.idx = idx;
@@ -406,5 +410,5 @@ extern "C" int csa2_paged_sparse_attn_decode(const void* q_bf16, int32_t B, int3
   a.swa_first_row = INT32_MIN;
   a.sm_scale = sm_scale;
   return launch_attn(a, q_bf16, B * L, (uint16_t*)out_bf16, out_f32, lse, workspace, workspace_bytes,
-                     (cudaStream_t)stream);
+                     (cudaStream_t)stream, false, true);
 }

@@ -120,7 +120,9 @@ enum : int { kModeCluster = 0, kModeReuse = 1, kModeSeq = 2 };
 // memory and is rescaled by 2^(m_old - m_new) before each tile's PV product
 // accumulates onto it, and the CTA writes the normalised output itself, with
 // no partials and no merge.
-template <int kMode>
+// kPaged: the listed entries lie in pages (instances of its own: beside the table's
+// lookup the others lose 1 to 4 %).
+template <int kMode, bool kPaged = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, AttnArgs a) {
   constexpr bool kReuse = kMode == kModeReuse;
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // which stands for an entry that has none: refused like one past the end)
   auto listed = [&](const int t) -> int32_t {
     const int32_t e = a.idx[(int64_t)seq * a.k + t];
-    if (!a.paged || e < 0) return e;
+    if (!kPaged || e < 0) return e;
     const int64_t row = e < a.paged_visible[seq] && e < a.pages.capacity() ? a.pages.row(seq, e) : -1;
     return row < 0 ? 0x7FFFFFFF : (int32_t)row;
   };
