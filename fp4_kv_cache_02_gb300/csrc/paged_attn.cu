@@ -19,9 +19,9 @@
 // tensor cores (fp16) bind before HBM already at one token per sequence. With
 // 64 heads on N they take 2,560 cycles a tile: S^T with the rows from tensor
 // memory 1,024 (32 a product, 48 from shared memory), O^T 1,536 (48: A and B
-// both from shared memory). Beside them a tile costs 2,858 wavefronts of shared
+// both from shared memory). Beside them a tile costs 2,880 wavefronts of shared
 // memory (the rows as fp16 written once, the codes read twice, P, the waits) and
-// 2,700 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
+// 3,050 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
 // Measured 4,600 to 4,900 cycles a tile: 32 sequences of 65,536 entries 288 us
 // (954 TFLOP/s, 49 % of the measured bf16 rate; 2.1 TB/s), 2,048 tokens of a
 // prompt behind 6,144 entries 1.94 ms (994 TFLOP/s), 24 sequences of 1 to 4
