@@ -309,9 +309,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     // 8g + j has run j of tile g of the pair. While a pair's copies are issued,
     // the next pair's pages are being looked up and the pair after that is being
     // claimed: in turn the three would take two round trips to L2 and the wait
-    // for a stage for each pair (50.5 us over 32 sequences of 65,536 entries,
-    // against 31.5 as here with the same ranges). Pages past the visible entries are not looked up; what a
-    // missing page leaves in the stage is never scored (s_mask).
+    // for a stage for each pair (50.5 us over 32 sequences of 65,536 entries, against
+    // 31.5 as here with the same ranges). Pages past the visible entries are not
+    // looked up; what a missing page leaves in the stage is never scored (s_mask).
     const int run_shift = p.pages.shift < 7 ? p.pages.shift : 7;
     const int run = 1 << run_shift;
     const int g = lane >> 3, j = lane & 7;
