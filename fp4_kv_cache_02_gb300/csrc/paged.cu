@@ -17,7 +17,8 @@ __device__ int g_paged_error = 0;
 // into its value and error (Knuth's two-sum), so that the last addition is the
 // only rounding that counts. The codes are decided on this value: with the
 // usual two or three roundings, values next to a rounding border of 4 bits
-// would depend on the order of operations.
+// would depend on the order of operations. An infinite channel or product has no
+// error terms (they are NaN): the difference of the products is then the result.
 __device__ __forceinline__ float diff_of_products(float x, float c, float y, float s) {
   const float p = __fmul_rn(x, c), q = __fmul_rn(y, s);
   const float pe = __fmaf_rn(x, c, -p), qe = __fmaf_rn(y, s, -q);
@@ -25,7 +26,7 @@ __device__ __forceinline__ float diff_of_products(float x, float c, float y, flo
   const float z = __fsub_rn(h, p);
   const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(h, z)), __fadd_rn(q, z));
   const float r = __fadd_rn(h, __fadd_rn(e, __fsub_rn(pe, qe)));
-  return r != 0.0f ? r : h;  // (a zero keeps the sign that the difference has)
+  return fabsf(r) > 0.0f ? r : h;  // (r NaN, or a zero, which keeps the sign that the difference has)
 }
 
 // (u, v) turned by the angle (cos, sin)

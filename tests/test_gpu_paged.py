@@ -399,6 +399,65 @@ def test_rope_rows_without_positions_or_with_bad_ones(csa2):
     assert torch.all((out.double() - ref).abs()[good] <= ref.abs()[good] * 2.0 ** -8 * (1 + 2.0 ** -14) + 1e-38)
 
 
+def overflowing(n, heads, dim, rope_dim):
+    """(x, rope, positions): rows with infinities among the turned channels, beside finite values and beside each other, and
+    with finite pairs whose turned values pass fp32's range."""
+    x = normal(gen(95), n, heads, dim)
+    top = float(torch.finfo(torch.bfloat16).max)
+    special = [float("inf"), -float("inf"), top, -top]
+    t = x[..., -rope_dim:]
+    for i in range(n):
+        t[i, :, i % rope_dim] = special[i % 4]
+        t[i, :, (i + rope_dim // 2) % rope_dim] = special[(i // 4) % 4]
+        t[i, :, (i + 1) % rope_dim] = special[(i // 16) % 4]
+    rope = angles(n, rope_dim)
+    return x, rope, torch.arange(n, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rope_of_infinities_and_of_what_overflows(csa2, interleaved):
+    """An infinite channel, or a pair whose turned value passes fp32's range, gives the infinities of the formula (NaN only
+    where that is a difference of infinities), and other pairs are not touched by it."""
+    x, rope, positions = overflowing(64, 3, 512, 64)
+    out = torch.empty_like(x)
+    csa2.csa2_rope(x, rope, positions, out, interleaved=interleaved)
+    assert csa2.csa2_get_last_error() == 0
+    # (in 64 bits a finite pair stays finite: what rounds past fp32's largest is infinite)
+    ref = rotated(x, rope, positions, interleaved).float()
+    assert int(torch.isinf(ref).sum()) > 400 and int(torch.isnan(ref).sum()) > 20
+    assert int((torch.isinf(ref) & torch.isfinite(rotated(x, rope, positions, interleaved))).sum()) > 20
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    far = torch.isinf(ref) | torch.isnan(ref)
+    assert torch.equal(out[torch.isinf(ref)].float(), ref[torch.isinf(ref)])
+    # (a value within fp32's range may round past bf16's: the infinity that one rounding to bf16 gives)
+    near = ref.bfloat16()
+    over = torch.isinf(near) & ~far
+    assert torch.equal(out[over], near[over])
+    rest = ~far & ~over
+    assert torch.all((out.double() - ref.double()).abs()[rest] <= ref.double().abs()[rest] * 2.0 ** -8 * (1 + 2.0 ** -14) + 1e-38)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_append_of_infinities_and_of_what_overflows(csa2, interleaved):
+    """The same through the append: a block with an infinity has the largest scale, the infinity's code is the largest of its
+    sign, and so for the keys."""
+    kv, rope, positions = overflowing(64, 1, 512, 64)
+    ik, _, _ = overflowing(64, 1, 128, 64)
+    kv, ik = kv[:, 0].contiguous(), ik[:, 0].contiguous()
+    planes = [torch.zeros(4, 16, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    csa2.csa2_paged_kv_append(kv, ik, *planes, table, ints([0]), rope=rope, interleaved=interleaved)
+    assert csa2.csa2_get_last_error() == 0
+    for x, data, scale, block, largest in ((kv, planes[0], planes[1], 16, 0x7E), (ik, planes[2], planes[3], 32, 253)):
+        y = rotated(x, rope, positions, interleaved).float()
+        codes = torch.stack([data & 15, data >> 4], -1).view(64, -1)
+        infinite = torch.isinf(y)
+        assert int(infinite.sum()) > 50
+        assert torch.equal(codes[infinite], torch.where(y[infinite] > 0, 7, 15).to(torch.uint8))
+        blocks = infinite.view(64, -1, block).any(-1)
+        assert torch.all(scale.view(64, -1)[blocks] == largest)
+
+
 # ---- index scores ---------------------------------------------------------------------
 
 
