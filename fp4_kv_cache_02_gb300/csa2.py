@@ -552,6 +552,9 @@ def csa2_paged_kv_append(kv, ik, kv_data, kv_scale, ik_data, ik_scale, page_tabl
         dev, ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"),
               (ik_scale, 4, "ik_scale")), page_table, n_visible)
     rope_at, n_rope, rope_dim = (None, 0, 0) if rope is None else _rope_table(rope, dev)
+    if n and rope_dim and not n_rope:
+        # (an empty tensor's address is null, and that means: do not rotate)
+        raise ValueError("rope holds no position (rope=None takes the rows as they are)")
     _call("csa2_paged_kv_append", kv_at, ik_at, n, _optional(cu_tokens, torch.int32, (B + 1,), "cu_tokens", dev), B,
           rope_at, n_rope, rope_dim, _optional(positions, torch.int32, (n,), "positions", dev), 1 if interleaved else 0,
           *at, n_pages, page, table, max_pages, counts,

@@ -355,6 +355,21 @@ def test_append_of_nothing(csa2):
     assert out.tolist() == [4, 9] and csa2.csa2_get_last_error() == 0
 
 
+def test_append_refuses_an_empty_angle_table(csa2):
+    """A table without positions is not a missing one: nothing is written unrotated. Without tokens there is nothing to turn."""
+    planes = [torch.zeros(2, 16, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
+    kv, ik = normal(gen(96), 2, 512), normal(gen(96), 2, 128)
+    none = torch.empty(0, 32, 2, device="cuda")
+    out = torch.full((2,), -5, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="no position"):
+        csa2.csa2_paged_kv_append(kv, ik, *planes, ints([[0], [1]]), ints([4, 9]), out, rope=none)
+    assert out.tolist() == [-5, -5] and not any(p.any() for p in planes)
+    with pytest.raises(csa2.Csa2Error):
+        csa2.csa2_rope(kv[:, None], none, None, kv[:, None])
+    csa2.csa2_paged_kv_append(kv[:0], ik[:0], *planes, ints([[0], [1]]), ints([4, 9]), out, rope=none)
+    assert out.tolist() == [4, 9] and csa2.csa2_get_last_error() == 0
+
+
 # ---- rotation ----------------------------------------------------------------------
 
 
