@@ -91,6 +91,18 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   return r;
 }
 
+// The largest magnitude, NaN where one is.
+__device__ __forceinline__ float max_abs3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Two fp32 values -> two E4M3 bytes: `lo` in bits 0..7.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   uint16_t r;

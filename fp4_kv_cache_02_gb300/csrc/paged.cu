@@ -201,9 +201,10 @@ __global__ void __launch_bounds__(kPagedWarps * 32) paged_append_kernel(AppendAr
     encode_kv_fp4_values(f, d, sc);
     *reinterpret_cast<uint2*>(a.kv_data + row * kKvBytes + lane * 8) = d;
     a.kv_scale[row * kKvScales + lane] = sc;
-    float amax = fmaxf(fmaxf(fabsf(g.x), fabsf(g.y)), fmaxf(fabsf(g.z), fabsf(g.w)));
+    // (a NaN counts as the largest, as in csa2_quant_mxfp4, which compares bit patterns)
+    float amax = max_abs3_nan(g.x, g.y, max_abs3_nan(g.z, g.w, 0.0f));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = 1; o < 8; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     float inv;
     // (the exponent field of the fp32 value is the one its upper half has as bf16)
     const int X = mxfp4_exponent(__float_as_uint(amax) >> 16, inv);

@@ -261,6 +261,34 @@ def test_append_of_equal_runs_equals_the_flat_append(csa2, mode, T):
     assert csa2.csa2_get_last_error() == 0
 
 
+@pytest.mark.parametrize("tokens", [1, 200])  # one and several tokens to a warp are told apart by the whole call's tokens
+def test_append_of_nans_and_infinities_equals_the_flat_append(csa2, tokens):
+    """Without a rotation the bytes are csa2_kv_append's for any inputs, and those of the encoders."""
+    g = gen(97)
+    B = 32
+    kv, ik = normal(g, B * tokens, 512), normal(g, B * tokens, 128)
+    for x, block in ((kv, 16), (ik, 32)):
+        blocks = x.view(-1, block)
+        for i, v in enumerate((float("nan"), float("inf"), -float("inf"))):
+            rows = torch.arange(i, blocks.shape[0], 7, device="cuda")
+            blocks[rows, torch.randint(0, block, rows.shape, generator=g, device="cuda")] = v
+        blocks[5::11] = float("nan")
+        blocks[6::13] *= 0
+        bits = torch.randint(0, 1 << 16, blocks[8::17].shape, generator=g, device="cuda", dtype=torch.int32)
+        blocks[8::17] = (bits - (1 << 15)).short().view(torch.bfloat16)
+    page = 256
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    flat = [torch.zeros(B, page, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
+    paged = [f.clone() for f in flat]
+    csa2.csa2_kv_append(kv.view(B, tokens, 512), ik.view(B, tokens, 128), *flat, ints([3] * B))
+    csa2.csa2_paged_kv_append(kv, ik, *paged, table, ints([3] * B))
+    assert csa2.csa2_get_last_error() == 0
+    want = *csa2.pack_kv_fp4(kv), *csa2.quant_mxfp4(ik)
+    for a, b, c in zip(flat, paged, want):
+        assert torch.equal(a, b)
+        assert torch.equal(b[:, 3:3 + tokens].reshape(B * tokens, -1), c.view(torch.uint8).view(B * tokens, -1))
+
+
 def test_append_at_given_positions(csa2):
     g = gen(11)
     runs, past, page = [4, 9], [30, 2], 16
