@@ -109,6 +109,15 @@ constexpr float kTop = 11.0f, kSlack = 4.0f;
 
 constexpr int kPartFloats = kHeads * kHeadDim;
 
+// Tries of a wait (200 ns each) before it gives up. The test of what follows compiles
+// the kernel with few, and without the first try, which may take much longer.
+constexpr uint32_t kManyTries = 1u << 22;
+#ifdef CSA2_PAGED_ATTN_WAIT_TRIES
+constexpr uint32_t kWaitTries = CSA2_PAGED_ATTN_WAIT_TRIES;
+#else
+constexpr uint32_t kWaitTries = kManyTries;
+#endif
+
 // A part of a token that more than one CTA works on, for the joining kernel.
 struct PartList {
   int32_t token;       // -1: this CTA begins no such token
@@ -259,6 +268,7 @@ struct __align__(16) Shared {
   uint64_t o;                 // O^T complete
   uint64_t info_full[kRing];
   uint64_t info_used[kRing];  // 27 warps
+  uint64_t soft;              // the softmax's warps meet at a token's end: 8 warps
   uint64_t end[2];
 };
 // (no static shared memory: dynamic shared memory then starts 1,024-byte aligned)
@@ -297,6 +307,18 @@ __device__ __forceinline__ void load_q_one(uint32_t elected, uint32_t q_smem, co
         : "memory");
 }
 
+// Waits for what is in flight to a barrier, whatever became of the run; bounded all
+// the same. (One statement to the compiler: as C++ loops it moved the role loops'
+// code, 32 sequences of 65,536 entries 290 to 299 us against 287.)
+__device__ __forceinline__ void ended(uint64_t* bar, uint32_t par) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 n;\n\tmov.u32 n, %2;\n\t"
+      "LOOP:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.eq.u32 p, n, 0;\n\t@!p bra LOOP;\n\t"
+      "DONE:\n\t}" ::"r"(tc::smem_u32(bar)), "r"(par & 1u), "n"((int)kManyTries)
+      : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap q_map,
                       Args a) {
@@ -328,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&sh.s_read, kSoftWarps);
     tc::mbar_init(&sh.p, kSoftWarps);
     tc::mbar_init(&sh.o, 1);
+    tc::mbar_init(&sh.soft, kSoftWarps);
     for (int i = 0; i < 2; ++i) tc::mbar_init(sh.end + i, 1);
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(sh.info_full + i, 1);
@@ -416,18 +439,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // so that the compiler knows it as the warp's: the loops below cost 3 % more else
   const int32_t n_run = (int32_t)__reduce_max_sync(0xffffffffu, (uint32_t)(sh.tile1 - sh.tile0));
 
-  // A wait that runs out (2^22 tries, a tenth of a second at least) raises
+  // A wait that runs out (kWaitTries, a tenth of a second at least) raises
   // sh.abort, on which every later wait gives up at once and nothing more is
   // issued. The loops then run to their ends all the same, so that no warp is
-  // missing at a barrier, but write no more outputs (an Info that was not waited
-  // for names no token), and TIMEOUT is recorded.
+  // missing at a barrier.sync, but write no more outputs, and TIMEOUT is recorded. An
+  // Info that was not waited for names no token, and warps may read it differently:
+  // where its word decides, the softmax's warps meet at an mbarrier (meet()), not at
+  // a barrier.sync. What was issued is waited for by the warp that issued it, behind
+  // its loop and whatever became of the run (ended()).
   // (Counted, not timed, and kept short: the code of all roles together has to
   // stay in the instruction cache.)
   const auto wait = [&](uint64_t* bar, uint32_t par) {
-    if (!tc::mbar_try_wait(bar, par & 1u)) {
+    if (kWaitTries < kManyTries || !tc::mbar_try_wait(bar, par & 1u)) {
       uint32_t n = 0;
       while (!tc::mbar_try_wait_sleep(bar, par & 1u, 200u)) {
-        if (sh.abort || ++n >= (1u << 22)) {
+        if (sh.abort || ++n >= kWaitTries) {
           sh.abort = 1;
           break;
         }
@@ -587,20 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         info_done(j);
       }
-      // (the last copies are waited for by the warps that read them; those may not
-      // have when a wait ran out)
-      if (aborted())
-        for (uint32_t i = armed > 8 ? armed - 8 : 0; i < armed; ++i)
-          for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.raw + i % 8, (i / 8) & 1u); ++n) {
-          }
+      // (the warps that read the last copies wait for them too, but not when a wait ran out)
+      for (uint32_t i = armed > 8 ? armed - 8 : 0; i < armed; ++i) ended(sh.raw + i % 8, i / 8);
     }
-    if ((warp == kSWarp || warp == kOWarp) && n_run > 0 && sh.abort) {
-      // a wait ran out: products in flight end before tensor memory is freed
+    if ((warp == kSWarp || warp == kOWarp) && n_run > 0) {
+      // products in flight end before tensor memory is freed
       tc::mma_commit_one(elected, sh.end + (warp - kSWarp));
-      for (uint32_t n = 0; n < (1u << 22) && !tc::mbar_try_wait(sh.end + (warp - kSWarp), 0); ++n) {
-      }
-      for (uint32_t n = 0; n < (1u << 22) && tokens > 0 && !tc::mbar_try_wait(&sh.q_raw, (tokens - 1u) & 1u); ++n) {
-      }
+      ended(sh.end + (warp - kSWarp), 0);
+      if (tokens > 0) ended(&sh.q_raw, tokens - 1u);
       __syncwarp();
     }
   } else if (warp >= kFeedS) {
@@ -756,6 +776,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 32; ++i) l_acc[i] = 0.0f;
       if (tid < kHeads) sh.ref[tid] = 0.0f;
       uint32_t tokens = 0;  // of the run, with queries converted
+      // three times at a token's end, twice at the run's: phases 3 (tokens - 1) ..
+      const auto meet = [&](uint32_t phase) {
+        arrive(&sh.soft);
+        while (!tc::mbar_try_wait(&sh.soft, phase & 1u) && !sh.abort) {
+        }
+        __syncwarp();
+      };
       convert_q(tokens++);
       named_barrier(8, kSoftWarps * 32);  // mul, ref
       int slot = 2 * cta;               // where a part of the present token goes
@@ -877,10 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float lsum = warp_transpose_reduce16<false>(v, lane);
             if (lane < 16) sh.red[quad][h0 + u + lane] = lsum;
           }
-          named_barrier(8, kSoftWarps * 32);
-          const bool complete = whole && last_of_token, lost = sh.abort != 0;
+          meet(tokens - 1);
+          const bool complete = whole && last_of_token;
           const int64_t token = info.token;
-          if (tid < kHeads && !lost) {
+          if (tid < kHeads && !sh.abort) {
             const float l = sh.red[0][tid] + sh.red[1][tid] + sh.red[2][tid] + sh.red[3][tid];
             sh.up[tid] = !complete ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
             if (!complete) a.part_ml[(int64_t)slot * kHeads + tid] = make_float2(sh.ref[tid], l);
@@ -888,11 +915,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               a.lse[token * kHeads + tid] = l > 0.0f ? (sh.ref[tid] + log2f(l)) * 0.6931471805599453f : -INFINITY;
             sh.ref[tid] = 0.0f;
           }
-          named_barrier(8, kSoftWarps * 32);
+          meet(tokens);
           // the next token's queries have come meanwhile; its O^T only after them
           if (j + 1 < n_run) convert_q(tokens++);
           wait(&sh.o, (uint32_t)j);  // O^T of this tile is complete
           tc::tc_fence_after();
+          const bool lost = sh.abort != 0;
 #pragma unroll 2
           for (int x = 0; x < 8 && !lost; ++x) {  // channel block 2 half + x / 4, heads 16 (x % 4) ..
             const int mb = 2 * half + (x >> 2), hh = (x & 3) * 16;
@@ -931,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           open = true;
           whole = true;
           slot = 2 * cta + 1;
-          named_barrier(8, kSoftWarps * 32);  // mul, ref, up, red
+          if (j + 1 < n_run) meet(tokens);  // mul, ref, up, red
         }
         info_done(j);
       }
