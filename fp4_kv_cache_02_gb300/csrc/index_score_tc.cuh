@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       return g < 2 && j < (kTileRows >> run_shift) && (int64_t)t + g < end_of(t) && row_of(t) < nv;
     };
     const auto look_up = [&](int32_t t) { return wanted(t) ? places[row_of(t) >> p.pages.shift] : -1; };
-    int issued = 0;
+    int issued = 0, again = 0;  // copies; stages used again behind them
     bool ok = true;
     int32_t t0 = __shfl_sync(0xffffffffu, next(), 0);
     int32_t page0 = look_up(t0);
@@ -393,21 +393,23 @@ __global__ void __launch_bounds__(kThreads, 3)
       const int s = issued % kStages;
       ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&empty[s], ((uint32_t)(issued / kStages) & 1u) ^ 1u, s_abort,
                                                          &g_index_error));
-      if (ok && lane == 0) {
-        s_ring[issued % kRing] = -1;
-        tc::mbar_arrive(&full[s]);
+      if (ok) {
+        ++again;
+        if (lane == 0) {
+          s_ring[issued % kRing] = -1;
+          tc::mbar_arrive(&full[s]);
+        }
       }
     }
-    if (*s_abort) {
-      // let copies already in flight land before the CTA's memory goes away
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-        tc::mbar_wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1u, s_abort, &g_index_error, 100000000ull);
-    }
+    // copies land before the CTA's memory goes away (that of a stage used again since
+    // has been waited for)
+    for (int i = max(0, issued - kStages + again); i < issued; ++i)
+      tc::mbar_wait_issued(&full[i % kStages], (uint32_t)(i / kStages));
     __syncwarp();
   } else if (warp == kProducerWarp) {
     // ---- TMA producer ----
     if (lane == 0) {
-      int issued = 0;
+      int issued = 0, again = 0;  // copies; stages used again behind them
       const auto issue = [&](int i, int64_t tile) -> bool {
         const int s = i % kStages;
         const uint32_t ph = (uint32_t)(i / kStages) & 1u;
@@ -447,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           if (tc::mbar_wait_bounded(&empty[s], ((uint32_t)(issued / kStages) & 1u) ^ 1u, s_abort, &g_index_error)) {
             s_ring[issued % kRing] = -1;
             tc::mbar_arrive(&full[s]);
+            ++again;
           }
         }
       } else {
@@ -455,12 +458,9 @@ __global__ void __launch_bounds__(kThreads, 3)
           ++issued;
         }
       }
-      if (*s_abort) {
-        // let copies already in flight land before the CTA's memory goes away
-        for (int i = issued - kStages; i < issued; ++i)
-          if (i >= 0) tc::mbar_wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1u, s_abort,
-                                            &g_index_error, 100000000ull);
-      }
+      // copies land before the CTA's memory goes away, as over pages
+      for (int i = max(0, issued - kStages + again); i < issued; ++i)
+        tc::mbar_wait_issued(&full[i % kStages], (uint32_t)(i / kStages));
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -476,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       tc::tmem_cp_32x128_x4(tmem + kSfbCol, tc::smem_desc(tc::smem_u32(sSfb), 0, 128, tc::kSwizzleNone));
     __syncwarp();
     int last = -1;
+    bool passed = false;
     for (int i = 0; claimed || i < n_tiles; ++i) {
       const int s = i % kStages;
       const uint32_t ph = (uint32_t)(i / kStages) & 1u;
@@ -485,7 +486,8 @@ __global__ void __launch_bounds__(kThreads, 3)
                 tc::mbar_wait_bounded(&full[s], ph, s_abort, &g_index_error);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (claimed && s_ring[i % kRing] < 0) {
-        if (lane == 0) tc::mbar_arrive(&acc_full[a]);  // passes the end on to the epilogue
+        if (lane == 0) tc::mma_commit(&acc_full[a]);  // passes the end on to the epilogue
+        passed = true;
         break;
       }
       // scales of keys lane, lane+32, lane+64, lane+96 -> one 16-byte row
@@ -509,9 +511,11 @@ __global__ void __launch_bounds__(kThreads, 3)
       last = i;
       __syncwarp();
     }
-    if (*s_abort && last >= 0 && lane == 0)  // MMAs must finish before tensor memory is freed
-      tc::mbar_wait_bounded(&acc_full[last & 1], (uint32_t)(last >> 1) & 1u, s_abort, &g_index_error,
-                            100000000ull);
+    // MMAs (with none, the copy of q's scales) must finish before tensor memory is freed
+    if (lane == 0 && (claimed || n_tiles > 0)) {
+      if (last < 0 && !passed) tc::mma_commit(&acc_full[0]);
+      tc::mbar_wait_issued(&acc_full[last < 0 ? 0 : last & 1], (uint32_t)(last < 0 ? 0 : last >> 1));
+    }
     __syncwarp();
   } else {
     // ---- epilogue: warps 0..3, one key row per thread ----

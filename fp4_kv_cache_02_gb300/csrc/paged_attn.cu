@@ -109,13 +109,11 @@ constexpr float kTop = 11.0f, kSlack = 4.0f;
 
 constexpr int kPartFloats = kHeads * kHeadDim;
 
-// Tries of a wait (200 ns each) before it gives up. The test of what follows compiles
-// the kernel with few, and without the first try, which may take much longer.
-constexpr uint32_t kManyTries = 1u << 22;
-#ifdef CSA2_PAGED_ATTN_WAIT_TRIES
-constexpr uint32_t kWaitTries = CSA2_PAGED_ATTN_WAIT_TRIES;
+// Tries of a wait (200 ns each or more) before it gives up.
+#ifdef CSA2_WAIT_LIMIT
+constexpr uint32_t kWaitTries = CSA2_WAIT_LIMIT / 32;  // (a look takes about 32 clocks)
 #else
-constexpr uint32_t kWaitTries = kManyTries;
+constexpr uint32_t kWaitTries = 1u << 22;
 #endif
 
 // A part of a token that more than one CTA works on, for the joining kernel.
@@ -307,18 +305,6 @@ __device__ __forceinline__ void load_q_one(uint32_t elected, uint32_t q_smem, co
         : "memory");
 }
 
-// Waits for what is in flight to a barrier, whatever became of the run; bounded all
-// the same. (One statement to the compiler: as C++ loops it moved the role loops'
-// code, 32 sequences of 65,536 entries 290 to 299 us against 287.)
-__device__ __forceinline__ void ended(uint64_t* bar, uint32_t par) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 n;\n\tmov.u32 n, %2;\n\t"
-      "LOOP:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\tsetp.eq.u32 p, n, 0;\n\t@!p bra LOOP;\n\t"
-      "DONE:\n\t}" ::"r"(tc::smem_u32(bar)), "r"(par & 1u), "n"((int)kManyTries)
-      : "memory");
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap q_map,
                       Args a) {
@@ -446,13 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Info that was not waited for names no token, and warps may read it differently:
   // where its word decides, the softmax's warps meet at an mbarrier (meet()), not at
   // a barrier.sync. What was issued is waited for by the warp that issued it, behind
-  // its loop and whatever became of the run (ended()).
+  // its loop and whatever became of the run.
   // (Counted, not timed, and kept short: the code of all roles together has to
   // stay in the instruction cache.)
   const auto wait = [&](uint64_t* bar, uint32_t par) {
-    if (kWaitTries < kManyTries || !tc::mbar_try_wait(bar, par & 1u)) {
+    if (!tc::mbar_look(bar, par & 1u, 0)) {
       uint32_t n = 0;
-      while (!tc::mbar_try_wait_sleep(bar, par & 1u, 200u)) {
+      while (!tc::mbar_look(bar, par & 1u, 200u)) {
         if (sh.abort || ++n >= kWaitTries) {
           sh.abort = 1;
           break;
@@ -614,13 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         info_done(j);
       }
       // (the warps that read the last copies wait for them too, but not when a wait ran out)
-      for (uint32_t i = armed > 8 ? armed - 8 : 0; i < armed; ++i) ended(sh.raw + i % 8, i / 8);
+      for (uint32_t i = armed > 8 ? armed - 8 : 0; i < armed; ++i) tc::mbar_wait_issued(sh.raw + i % 8, i / 8);
     }
     if ((warp == kSWarp || warp == kOWarp) && n_run > 0) {
       // products in flight end before tensor memory is freed
       tc::mma_commit_one(elected, sh.end + (warp - kSWarp));
-      ended(sh.end + (warp - kSWarp), 0);
-      if (tokens > 0) ended(&sh.q_raw, tokens - 1u);
+      tc::mbar_wait_issued(sh.end + (warp - kSWarp), 0);
+      if (tokens > 0) tc::mbar_wait_issued(&sh.q_raw, tokens - 1u);
       __syncwarp();
     }
   } else if (warp >= kFeedS) {
