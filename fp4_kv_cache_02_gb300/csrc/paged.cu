@@ -109,7 +109,6 @@ __device__ __forceinline__ bool append_fits(int64_t nv, int32_t count, const Pag
 __device__ __forceinline__ void resolve_token(const AppendArgs& a, int32_t i, int64_t& row, int64_t& pos) {
   row = -1;
   pos = 0;
-  if (i >= a.n_tokens) return;
   const int32_t given = a.rope && a.positions ? a.positions[i] : 0;
   const int32_t b = a.cu ? sequence_of(a.cu, a.B, i) : i / a.per_seq;
   if (b >= a.B) return;  // behind the last sequence
@@ -152,19 +151,22 @@ __global__ void __launch_bounds__(kPagedWarps * 32) paged_append_kernel(AppendAr
     return;
   }
   const int64_t first = ((int64_t)blockIdx.x * kPagedWarps + (threadIdx.x >> 5)) * kPerWarp;
-  if (first >= a.n_tokens) return;
+  // rows of no sequence are not read: their owner may still be writing them
+  const int32_t row0 = a.cu ? max(a.cu[0], 0) : 0, row1 = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;
+  if (first + kPerWarp <= row0 || first >= row1) return;
   uint4 v[kPerWarp][2];
   uint2 kw[kPerWarp];
 #pragma unroll
   for (int j = 0; j < kPerWarp; ++j) {
-    const int64_t i = first + j < a.n_tokens ? first + j : first;
-    const uint4* src = reinterpret_cast<const uint4*>(a.kv + i * kHeadDim + lane * 16);
+    const int32_t i = min(max((int32_t)first + j, row0), row1 - 1);
+    const uint4* src = reinterpret_cast<const uint4*>(a.kv + (int64_t)i * kHeadDim + lane * 16);
     v[j][0] = __ldcs(src);  // (read once)
     v[j][1] = __ldcs(src + 1);
-    kw[j] = __ldcs(reinterpret_cast<const uint2*>(a.ik + i * kIdxDim) + lane);
+    kw[j] = __ldcs(reinterpret_cast<const uint2*>(a.ik + (int64_t)i * kIdxDim) + lane);
   }
   int64_t my_row = -1, my_pos = 0;
-  if (lane < kPerWarp) resolve_token(a, (int32_t)min((int64_t)0x7FFFFFFF, first + lane), my_row, my_pos);
+  if (lane < kPerWarp && first + lane >= row0 && first + lane < row1)
+    resolve_token(a, (int32_t)(first + lane), my_row, my_pos);
   float(&turned)[2][CSA2_MAX_ROPE_DIM] = s_turned[threadIdx.x >> 5];
 #pragma unroll
   for (int j = 0; j < kPerWarp; ++j) {

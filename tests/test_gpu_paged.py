@@ -383,6 +383,34 @@ def test_append_of_nothing(csa2):
     assert out.tolist() == [4, 9] and csa2.csa2_get_last_error() == 0
 
 
+@pytest.mark.parametrize("n", [23, 6000])  # one and several tokens to a warp
+@pytest.mark.parametrize("cu", [[0, 0, 0], [7, 7, 7], [23, 23, 23], [5, 6, 6], [6, 6, 9], [0, 1, 2], [21, 22, 23], [9, 4, 4],
+                                [-4, -2, 0], [24, 40, 7000], [5, 2, 8]])
+def test_append_of_few_rows_among_many(csa2, cu, n):
+    """Rows of no sequence, and runs that are not within the rows, at every place within a warp's tokens."""
+    kv, ik = normal(gen(98), n, 512), normal(gen(98), n, 128)
+    planes = [torch.zeros(2, 16, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
+    want = [p.clone() for p in planes]
+    packed = *csa2.pack_kv_fp4(kv), *csa2.quant_mxfp4(ik)
+    counts = []
+    for b in range(2):
+        lo, hi = cu[b], cu[b + 1]
+        ok = 0 <= lo <= hi <= n
+        run = hi - lo if ok and hi - lo <= 13 else 0
+        counts.append(3 + run)
+        if run and cu == sorted(cu):
+            for plane, new in zip(want, packed):
+                plane[b, 3:3 + run] = new.view(torch.uint8).view(n, -1)[lo:hi]
+    out = torch.empty(2, dtype=torch.int32, device="cuda")
+    csa2.csa2_paged_kv_append(kv, ik, *planes, ints([[0], [1]]), ints([3, 3]), out, cu_tokens=ints(cu))
+    refused = any(not 0 <= cu[b] <= cu[b + 1] <= n or cu[b + 1] - cu[b] > 13 for b in range(2))
+    assert csa2.csa2_get_last_error() == (DEVICE_ERROR if refused else 0)
+    assert out.tolist() == counts
+    if cu == sorted(cu):
+        for got, ref in zip(planes, want):
+            assert torch.equal(got, ref)
+
+
 def test_append_refuses_an_empty_angle_table(csa2):
     """A table without positions is not a missing one: nothing is written unrotated. Without tokens there is nothing to turn."""
     planes = [torch.zeros(2, 16, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
