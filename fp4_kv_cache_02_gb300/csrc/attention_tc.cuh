@@ -240,11 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
     // largest |q| has exponent e (bf16 exponent field e + 127); 2^(14 - e) puts
-    // it in [2^14, 2^15). Clamped so that 2^k and 2^-k stay normal fp32.
+    // it in [2^14, 2^15). Clamped so that 2^k and 2^-k stay normal fp32 (k is -113 at
+    // least for a finite q).
     int k = 0;
     if (amax != 0u) {
       const int e = (int)((amax >> 7) & 0xFFu) - 127;
-      k = min(max(14 - e, -100), 100);
+      k = min(14 - e, 126);
     }
     const float up = __int_as_float((127 + k) << 23);
 #pragma unroll

@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int o = 1; o < 8; o <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
           const uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
           int k2 = 0;
-          if (amax != 0u) k2 = min(max(14 - ((int)(amax >> 7) - 127), -100), 100);
+          if (amax != 0u) k2 = min(14 - ((int)(amax >> 7) - 127), 126);  // (-113 at least: both powers are normal)
           const float up = __int_as_float((127 + k2) << 23);
 #pragma unroll
           for (int b = 0; b < 8; ++b) {

@@ -810,6 +810,32 @@ def test_dense_queries_of_very_different_sizes(csa2):
     check_dense(csa2, c, q, [1], 0, True, 1.0, got)
 
 
+@pytest.mark.parametrize("e", [124, 110, -100])
+def test_attention_of_queries_at_the_ends_of_their_type(csa2, e):
+    """Queries times 2^e with sm_scale 2^-e are the same scores to the last bit, dense, selected and on flat planes."""
+    c = Cache(csa2, [400, 33], 16, 92)
+    q = normal(gen(93), 2, 64, 512, scale=512 ** -0.5)
+    q = torch.where(q.abs() < 2.0 ** -20, 0, q)  # (nothing becomes subnormal)
+    far = (q.double() * 2.0 ** e).bfloat16()
+    assert torch.equal(far.double() * 2.0 ** -e, q.double())
+    idx = ints([[0, 5, 17, 399], [3, 32, -1, -1]])
+    swa = csa2.pack_fp8(normal(gen(94), 2, 1, 16, 512))
+    flat = c.flat_planes()
+    res = []
+    for x, scale in ((q, 1.0), (far, 2.0 ** -e)):
+        dense = run_dense(csa2, c, x, scale=scale)
+        x = x[:, None].contiguous()
+        o1, o2, l1 = torch.empty_like(x), torch.empty_like(x), torch.empty(2, 1, 64, device="cuda")
+        csa2.csa2_paged_sparse_attn_decode(x, c.kv_data, c.kv_scale, c.table, c.n_visible, idx, swa, o1,
+                                           csa2.paged_sparse_attn_workspace(2, 1, 4, 16), lse=l1, sm_scale=scale)
+        csa2.csa2_sparse_attn_decode(x, flat[0], flat[1], c.n_visible, idx, swa, o2, csa2.attn_workspace(2, 4, 16),
+                                     sm_scale=scale)
+        res.append((*dense, o1, l1, o2))
+    assert csa2.csa2_get_last_error() == 0
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 def test_dense_missing_pages_and_bad_counts(csa2):
     c = Cache(csa2, [500, 300, 200, 100], 16, 65, most=40)
     g = gen(66)
