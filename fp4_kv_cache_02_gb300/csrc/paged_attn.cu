@@ -232,6 +232,7 @@ struct Info {
   int32_t at;       // its first entry
   int32_t token;    // row of q
   int32_t left;     // tiles of the token behind this one
+  int32_t some;     // the tile has a row whose page is there
 };
 
 // Shared memory behind the operands.
@@ -547,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             record_error(&g_paged_attn_error, CSA2_ERR_DEVICE);
           }
         }
+        const int some = __any_sync(0xffffffffu, page >= 0);
         if (j >= kRing) wait(sh.info_used + j % kRing, (uint32_t)(j / kRing) - 1u);
         Info& to = sh.info[j % kRing];
         if (lane < 8) to.page[lane] = page;
@@ -555,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           to.at = w.tile * kRows;
           to.token = w.seq.first + w.tok;
           to.left = w.tiles - 1 - w.tile;
+          to.some = some;
         }
         // (a later token's queries into L2, up to kRing tiles before they are needed)
         if (lane == 0 && j > 0 && w.tile == 0)
@@ -829,8 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.up[h] = up;
             sh.shrink[h] = open ? 1.0f : fast_exp2(-up);  // (before the first reference O^T and l are 0)
           }
-          // (a tile with a row sets every head's reference)
-          open = open && !(fmaxf(fmaxf(sh.red[0][h0], sh.red[1][h0]), fmaxf(sh.red[2][h0], sh.red[3][h0])) > -INFINITY);
+          // (a tile with a row sets every head's reference, of a head whose scores are all
+          // -inf or NaN as well: the next tile's maxima may not be taken for the first)
+          open = open && !info.some;
           named_barrier(1 + half, 128);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {

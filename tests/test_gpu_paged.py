@@ -836,6 +836,34 @@ def test_attention_of_queries_at_the_ends_of_their_type(csa2, e):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bad", [0, 31, 32, 63])
+def test_dense_heads_with_scores_past_32_bits(csa2, bad):
+    """A head whose scores all pass fp32's range downwards leaves the other heads of its token as they are, whichever it is:
+    the first tile sets their references although that head has no maximum."""
+    n = 40000  # (several tiles to an SM)
+    c = Cache(csa2, [n], 64, 99)
+    x = normal(gen(100), n, 512)
+    x[:, 0] = 6.0
+    x *= torch.linspace(0.5, 3.0, n, device="cuda").flip(0)[:, None].bfloat16()  # (the maxima change)
+    d, s = csa2.pack_kv_fp4(x)
+    c.kv_data.view(-1, 256)[c.rows[0]] = d
+    c.kv_scale.view(-1, 32)[c.rows[0]] = s.view(torch.uint8)
+    q = normal(gen(101), 2, 64, 512, scale=0.2)
+    want = run_dense(csa2, c, q)
+    q[:, bad] = 0
+    q[:, bad, 0] = -3e38
+    got = run_dense(csa2, c, q)
+    assert csa2.csa2_get_last_error() == 0
+    others = [h for h in range(64) if h != bad]
+    for a, b in zip(got, want):
+        assert torch.equal(a[:, others], b[:, others])
+    check = [t[:, others] for t in got]
+    rows = c.latents(csa2, 0)
+    for j in range(2):
+        o, l, a, err = dense_reference(q[j][others], rows[:n - 1 + j], 1.0)
+        assert torch.all((check[1][j].double() - o).abs() <= (2.0 ** -11 + 3 * err + 2.0 ** -18) * a + 1e-30)
+
+
 def test_dense_missing_pages_and_bad_counts(csa2):
     c = Cache(csa2, [500, 300, 200, 100], 16, 65, most=40)
     g = gen(66)
