@@ -377,7 +377,8 @@ extern "C" int csa2_paged_sparse_attn_decode(const void* q_bf16, int32_t B, int3
                                              const int32_t* idx, int32_t k, const uint8_t* swa, int32_t n_swa,
                                              float sm_scale, void* out_bf16, float* out_f32, float* lse,
                                              void* workspace, size_t workspace_bytes, csa2_stream_t stream) {
-  if (B != 0 && (!q_bf16 || !kv_data || !kv_scale || !n_visible || (!idx && k > 0) || !out_bf16))
+  if (B != 0 &&
+      (!q_bf16 || !paged_planes(n_pages, kv_data, kv_scale) || !n_visible || (!idx && k > 0) || !out_bf16))
     return CSA2_ERR_INVALID_ARG;
   PageTable pages;
   if (int rc = paged_check(page_table, n_pages, page_size, max_pages, B, pages)) return rc;

@@ -116,7 +116,8 @@ extern "C" int csa2_paged_index_score(const uint8_t* q_data, const uint8_t* q_e8
                                       const int32_t* n_visible, int64_t n_pos, float* scores, int32_t* tile_counters,
                                       csa2_stream_t stream) {
   if (n_pos < 0) return CSA2_ERR_INVALID_ARG;
-  if (n_pos > 0 && B != 0 && (!q_data || !q_e8m0 || !w || !ik_data || !ik_scale || !n_visible || !scores))
+  if (n_pos > 0 && B != 0 &&
+      (!q_data || !q_e8m0 || !w || !paged_planes(n_pages, ik_data, ik_scale) || !n_visible || !scores))
     return CSA2_ERR_INVALID_ARG;
   PageTable pages;
   if (int rc = paged_check(page_table, n_pages, page_size, max_pages, B, pages)) return rc;
@@ -131,12 +132,14 @@ extern "C" int csa2_paged_index_score(const uint8_t* q_data, const uint8_t* q_e8
   const int64_t pool = n_pages << pages.shift;
   const int run = page_size < scan_tc::kTileRows ? page_size : scan_tc::kTileRows;
   CUtensorMap map;
-  // (an empty pool has no page to follow: the map then only has to be valid)
+  // (an empty pool has no page to follow: the map then only has to be valid, over any
+  // memory)
+  void* plane = (void*)(pool > 0 ? ik_data : q_data);
   cuuint64_t dims[3] = {(cuuint64_t)kIkBytes, (cuuint64_t)(pool > 0 ? pool : 1), 1};
   cuuint64_t strides[2] = {(cuuint64_t)kIkBytes, (cuuint64_t)(pool > 0 ? pool : 1) * kIkBytes};
   cuuint32_t box[3] = {(cuuint32_t)kIkBytes, (cuuint32_t)run, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void*)ik_data, dims, strides, box, estr,
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, plane, dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return CSA2_ERR_CUDA;

@@ -398,7 +398,8 @@ extern "C" int csa2_paged_kv_append(const void* kv_bf16, const void* ik_bf16, in
                                     uint8_t* kv_data, uint8_t* kv_scale, uint8_t* ik_data, uint8_t* ik_scale,
                                     int64_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                                     const int32_t* n_visible, int32_t* n_visible_out, csa2_stream_t stream) {
-  if (B != 0 && (!kv_data || !kv_scale || !ik_data || !ik_scale || !n_visible)) return CSA2_ERR_INVALID_ARG;
+  if (B != 0 && (!paged_planes(n_pages, kv_data, kv_scale) || !paged_planes(n_pages, ik_data, ik_scale) || !n_visible))
+    return CSA2_ERR_INVALID_ARG;
   if (n_tokens > 0 && (!kv_bf16 || !ik_bf16)) return CSA2_ERR_INVALID_ARG;
   AppendArgs a{};
   if (int rc = paged_check(page_table, n_pages, page_size, max_pages, B, a.pages)) return rc;

@@ -1124,7 +1124,7 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
                                const int32_t* page_table, int32_t max_pages, const int32_t* n_visible, int32_t causal,
                                float sm_scale, void* out_bf16, float* out_f32, float* lse, void* workspace,
                                size_t workspace_bytes, csa2_stream_t stream) {
-  if (n_tokens > 0 && B != 0 && (!q_bf16 || !kv_data || !kv_scale || !n_visible || !out_bf16))
+  if (n_tokens > 0 && B != 0 && (!q_bf16 || !paged_planes(n_pages, kv_data, kv_scale) || !n_visible || !out_bf16))
     return CSA2_ERR_INVALID_ARG;
   pattn::Args a{};
   if (int rc = paged_check(page_table, n_pages, page_size, max_pages, B, a.pages)) return rc;
@@ -1160,14 +1160,14 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   auto encode = tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   // the pool's codes, in boxes of one group's 64 bytes of a run of rows (an empty
-  // pool has nothing to copy: the map then only has to be valid)
+  // pool has nothing to copy: the map then only has to be valid, over any memory)
   const int64_t pool = n_pages << a.pages.shift;
   CUtensorMap rows_map;
   cuuint64_t dims[2] = {(cuuint64_t)kKvBytes, (cuuint64_t)(pool > 0 ? pool : 1)};
   cuuint64_t strides[1] = {(cuuint64_t)kKvBytes};
   cuuint32_t box[2] = {64, (cuuint32_t)(page_size < pattn::kRows ? page_size : pattn::kRows)};
   cuuint32_t estr[2] = {1, 1};
-  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)kv_data, dims, strides, box, estr,
+  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)(pool > 0 ? (const void*)kv_data : q_bf16), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return CSA2_ERR_CUDA;

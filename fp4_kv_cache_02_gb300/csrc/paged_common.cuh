@@ -58,6 +58,11 @@ static inline int paged_check(const int32_t* page_table, int64_t n_pages, int32_
   return CSA2_OK;
 }
 
+// The planes of a pool; one without pages has none (an empty tensor's address is null).
+static inline bool paged_planes(int64_t n_pages, const void* data, const void* scale) {
+  return n_pages == 0 || (data && scale);
+}
+
 // Rows of each sequence when cu is NULL.
 static inline int paged_runs(const int32_t* cu, int32_t n_tokens, int32_t B, int32_t& per_seq) {
   per_seq = 0;

@@ -579,7 +579,8 @@ int csa2_sparse_attn_prefill_replay(const void* q_bf16, int32_t T,
  * an entry being laid out as in the planes of the conventions above. Entry e of
  * sequence b is row e % page_size of page page_table[b][e / page_size].
  *   - page_size is a power of two, at least CSA2_MIN_PAGE. A pool holds at most
- *     2^31 - 1 entries. Plane base pointers are 16-byte aligned.
+ *     2^31 - 1 entries. Plane base pointers are 16-byte aligned; a pool without
+ *     pages needs none.
  *   - page_table [B][max_pages] int32. Only the table's first
  *     ceil(n / page_size) places of a sequence with n entries are read; the
  *     others may hold anything. A page outside [0, n_pages) that is needed is

@@ -1040,6 +1040,43 @@ def test_dense_joins_the_window_by_merge(csa2):
         assert torch.all((mf[b].double() - ref).abs() <= (2.0 ** -11 + 5 * d + 2.0 ** -17) * a)
 
 
+def test_a_pool_without_pages(csa2):
+    """Sequences without entries over a pool that has none; and entries that are nowhere."""
+    planes = [torch.empty(0, 16, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    g = gen(102)
+    q = normal(g, 3, 64, 512, scale=512 ** -0.5)
+    qi, qs, w = queries(csa2, g, 2)
+    swa = csa2.pack_fp8(normal(g, 2, 1, 16, 512))
+    idx = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    sq = q[:2, None].contiguous()
+    alone = torch.empty_like(sq)
+    flat = torch.zeros(2, 128, 256, dtype=torch.uint8, device="cuda"), torch.zeros(2, 128, 32, dtype=torch.uint8, device="cuda")
+    csa2.csa2_sparse_attn_decode(sq, *flat, ints([0, 0]), idx, swa, alone, csa2.attn_workspace(2, 4, 16))
+    for lens, status in (([0, 0], 0), ([5, 40], DEVICE_ERROR)):
+        nv = ints(lens)
+        out, lse = torch.full_like(q, 7.0), torch.full((3, 64), 7.0, device="cuda")
+        csa2.csa2_paged_attn(q, planes[0], planes[1], table, nv, out, csa2.paged_attn_workspace(3, 2), cu_q=ints([0, 2, 3]), lse=lse)
+        assert csa2.csa2_get_last_error() == status
+        assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+        scores = torch.full((2, 48), 7.0, device="cuda")
+        csa2.csa2_paged_index_score(qi, qs, w, planes[2], planes[3], table, nv, scores)
+        assert csa2.csa2_get_last_error() == status
+        assert torch.all(scores == -float("inf"))
+        pick = torch.arange(4, dtype=torch.int32, device="cuda").repeat(2, 1) if status else idx
+        got = torch.full_like(sq, 7.0)
+        csa2.csa2_paged_sparse_attn_decode(sq, planes[0], planes[1], table, nv, pick, swa, got,
+                                           csa2.paged_sparse_attn_workspace(2, 1, 4, 16))
+        assert csa2.csa2_get_last_error() == status
+        assert torch.equal(got, alone)
+    kv, ik = normal(g, 2, 512), normal(g, 2, 128)
+    after = torch.empty(2, dtype=torch.int32, device="cuda")
+    csa2.csa2_paged_kv_append(kv[:0], ik[:0], *planes, table, ints([0, 0]), after)
+    assert csa2.csa2_get_last_error() == 0 and after.tolist() == [0, 0]
+    csa2.csa2_paged_kv_append(kv, ik, *planes, table, ints([0, 0]), after)
+    assert csa2.csa2_get_last_error() == DEVICE_ERROR and after.tolist() == [1, 1]
+
+
 # ---- a server's use of them ------------------------------------------------------------------
 
 

@@ -124,3 +124,19 @@ def test_workspace_sizes(lib):
     dense = lib.csa2_paged_attn_workspace_size
     assert dense(1, 1) == dense(1 << 20, 7) > 0  # two parts per SM, whatever the batch
     assert dense(0, 1) == dense(1, 0) == 0
+
+
+NO_POOL = dict(n_pages=0, kv_data=None, kv_scale=None)
+
+
+def test_a_pool_without_pages_needs_no_planes(lib):
+    keys = dict(ik_data=None, ik_scale=None)
+    assert call(lib.csa2_paged_kv_append, APPEND, APPEND_GOOD, **NO_POOL, **keys, B=0) == OK
+    # (beside a second thing that is wrong, so that nothing is enqueued)
+    assert call(lib.csa2_paged_kv_append, APPEND, APPEND_GOOD, **NO_POOL, **keys, kv=P + 8) == ALIGN
+    assert call(lib.csa2_paged_index_score, SCORE, SCORE_GOOD, n_pages=0, **keys, q=P + 8) == ALIGN
+    assert call(lib.csa2_paged_sparse_attn_decode, SPARSE, SPARSE_GOOD, **NO_POOL) == WORKSPACE
+    assert call(lib.csa2_paged_attn, DENSE, DENSE_GOOD, **NO_POOL) == WORKSPACE
+    # one that has pages does
+    for missing in ("kv_data", "kv_scale", "ik_data", "ik_scale"):
+        assert call(lib.csa2_paged_kv_append, APPEND, APPEND_GOOD, **{missing: None}, n_pages=1) == ARG
