@@ -128,9 +128,16 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object (0.4 us instead of 3), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream):
-    # (the handle without the Stream object: 0.4 us instead of 3)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 def _req(t, dtype, name, allow_none=False):

@@ -140,3 +140,19 @@ def test_a_pool_without_pages_needs_no_planes(lib):
     # one that has pages does
     for missing in ("kv_data", "kv_scale", "ik_data", "ik_scale"):
         assert call(lib.csa2_paged_kv_append, APPEND, APPEND_GOOD, **{missing: None}, n_pages=1) == ARG
+
+
+def test_streams_without_the_raw_handle(monkeypatch):
+    """The current stream's handle, whether or not torch gives it without a Stream object; a given stream's as it is."""
+    from fp4_kv_cache_02_gb300 import csa2
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    monkeypatch.setattr(csa2.torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(csa2.torch.cuda, "current_stream", lambda: Stream(77))
+    monkeypatch.setattr(csa2, "_raw_stream", lambda device: 70 + device)
+    assert csa2._s(None) == 73 and csa2._s(Stream(5)) == 5
+    monkeypatch.setattr(csa2, "_raw_stream", None)
+    assert csa2._s(None) == 77 and csa2._s(Stream(5)) == 5
