@@ -59,12 +59,13 @@ __device__ __forceinline__ void encode_mxfp4_block(const uint32_t (&w)[16], uint
 // x / d rounded to nearest, from r = 1 / d rounded to nearest: the product x r
 // is corrected once by its exact remainder (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990). The
-// remainder is taken as q d - x, which keeps the sign of a zero. It is exact
-// while x is finite, the quotient does not overflow and neither is near the
-// subnormals; further down the quotient is off by some last bits, far below
-// the lowest border of the codes made of it. Run over every finite fp32 x with
-// d = 6 and every E4M3 d that a block with x in it can have, the codes equal
-// those of __fdiv_rn.
+// remainder is taken as q d - x, which keeps the sign of a zero. While x is
+// finite, the quotient does not overflow and neither is near the subnormals, every
+// step scales with powers of two, and over all significands of x and of an E4M3 d
+// (6 has that of 1.5) the result is the rounded quotient: tests/test_quotient.py.
+// No quotient overflows: x is at most 6.4 d unless d is the largest scale. Further
+// down the quotient is off by some last bits, far below the lowest border of the
+// codes made of it.
 __device__ __forceinline__ float div_by(float x, float d, float r) {
   const float q = x * r;
   return __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);

@@ -289,6 +289,53 @@ def test_append_of_nans_and_infinities_equals_the_flat_append(csa2, tokens):
         assert torch.equal(b[:, 3:3 + tokens].reshape(B * tokens, -1), c.view(torch.uint8).view(B * tokens, -1))
 
 
+def test_append_codes_of_fp32_values_beside_every_border(csa2):
+    """Turned values are fp32: the encoder's codes for values within three steps of every border of every scale, and scales for
+    blocks whose largest is within three steps of every border between scales, against the rounded quotients. A table of
+    (c, 0) makes any fp32 value c of a row of ones."""
+    def beside(x):
+        bits = np.float32(x).view(np.int32)
+        return [(bits + i).astype(np.int32).view(np.float32) for i in range(-3, 4)]
+
+    scales = torch.arange(0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    borders = (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)
+    blocks = []
+    for s in scales[1:]:
+        near = [v for b in borders for v in beside(b * s)] + [s * 6] * 11
+        blocks += [[6 * s] + near[15 * i:15 * i + 15] for i in range(4)]
+    rng = np.random.default_rng(7)
+    for lo, hi in zip(scales, scales[1:]):
+        blocks += [[v] + list(v * rng.random(15, dtype=np.float32)) for v in beside(3 * (lo + hi))]
+    blocks += [[v] + list(v * rng.random(15, dtype=np.float32)) for v in beside(6 * 464.0) + beside(6 * 448.0) + beside(1e30)]
+    blocks += [[0.0] * 16] * (-len(blocks) % 4)
+    c = torch.from_numpy(np.array(blocks, dtype=np.float32)).view(-1, 64)
+    n = c.shape[0]
+    rope = torch.stack([c, torch.zeros_like(c)], -1).cuda().contiguous()
+    kv = torch.ones(n, 512, dtype=torch.bfloat16, device="cuda")
+    kv[:, 448:] = -1.0  # the second of each pair: -c
+    ik = torch.zeros(n, 128, dtype=torch.bfloat16, device="cuda")
+    pages = -(-n // 16)
+    planes = [torch.zeros(pages, 16, w, dtype=torch.uint8, device="cuda") for w in (256, 32, 64, 4)]
+    csa2.csa2_paged_kv_append(kv, ik, *planes, torch.arange(pages, dtype=torch.int32, device="cuda")[None], ints([0]), rope=rope)
+    assert csa2.csa2_get_last_error() == 0
+    v = c.view(n, 4, 16)
+    want = (v.abs().amax(-1) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    s = want.float()[..., None]
+    a = v / torch.where(s > 0, s, torch.ones_like(s))
+    code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int() + (a >= 3.5).int()
+            + (a > 5.0).int())
+    code = torch.where(s > 0, code, torch.zeros_like(code)).view(n, 64)
+    got = torch.stack([planes[0] & 15, planes[0] >> 4], -1).view(-1, 512)[:n].int().cpu()
+    scale = planes[1].view(-1, 32)[:n].cpu()
+    for half, sign in ((0, 0), (1, 8)):
+        assert torch.equal(scale[:, 24 + 4 * half:28 + 4 * half], want.view(torch.uint8))
+        part = got[:, 384 + 64 * half:448 + 64 * half]
+        negative = torch.where(s.expand(n, 4, 16).reshape(n, 64) > 0, sign, 0)
+        # (a zero of either sign: the code's sign is not looked at)
+        assert torch.equal(part & 7, code)
+        assert torch.equal((part & 8)[code > 0], negative[code > 0].int())
+
+
 def test_append_at_given_positions(csa2):
     g = gen(11)
     runs, past, page = [4, 9], [30, 2], 16
