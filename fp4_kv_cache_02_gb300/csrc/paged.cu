@@ -266,7 +266,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 constexpr int kRopeRows = 4;
 
 __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
-  pdl_begin();
+  // (no pdl_launch_dependents(): the selected attention behind loads its queries, which
+  // are written here, before it waits for this kernel)
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t row0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kRopeRows;
   const int64_t left = a.n_tokens * a.heads - row0;

@@ -489,7 +489,8 @@ int csa2_sparse_attn_kernel_launches(int32_t n_queries, int32_t k,
  *   before it on the stream (the indices and n_visible are read after): they
  *   must not be written by that kernel when it is one of this library's
  *   attention or merge kernels (which let their successor start early); the
- *   packers and anything launched without programmatic dependence are safe.
+ *   packers, csa2_rope and anything launched without programmatic dependence
+ *   are safe.
  *   Precision: rows and q enter the tensor cores as fp16 (exact: the row
  *   values have at most 6 significant bits, q is scaled by a power of two per
  *   head), P as fp16 (relative rounding 2^-11), fp32 accumulation.

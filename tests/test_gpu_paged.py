@@ -576,6 +576,42 @@ def test_append_of_infinities_and_of_what_overflows(csa2, interleaved):
         assert torch.all(scale.view(64, -1)[blocks] == largest)
 
 
+@pytest.mark.parametrize("between", [False, True])
+def test_attention_right_behind_the_rotation(csa2, between):
+    """The selected attention loads its queries before it waits for the kernel before it: a rotation that is still writing them
+    may not let it start, nor the attention call behind another one."""
+    g = gen(104)
+    n = 4096                                            # (the rotation takes 80 us, the queries are its last rows)
+    c = Cache(csa2, [300], 64, 105)
+    flat = c.flat_planes()
+    x = normal(g, n, 64, 512, scale=512 ** -0.5)
+    rope = angles(n, 64)
+    idx = torch.arange(128, dtype=torch.int32, device="cuda")[None]
+    swa = csa2.pack_fp8(normal(g, 1, 4, 16, 512))
+    other, o3 = x[:4].view(1, 4, 64, 512).contiguous(), torch.empty(1, 4, 64, 512, dtype=torch.bfloat16, device="cuda")
+    ws = [csa2.paged_sparse_attn_workspace(1, 4, 128, 16) for _ in range(3)]
+    want = None
+    for i in range(6):
+        for call in ("paged", "flat"):
+            turned = torch.zeros_like(x)
+            q = turned[-4:].view(1, 4, 64, 512)
+            got = torch.empty_like(q)
+            torch.cuda.synchronize()
+            csa2.csa2_rope(x, rope, None, turned, interleaved=True)
+            if want is None:
+                torch.cuda.synchronize()
+            elif between:
+                csa2.csa2_paged_sparse_attn_decode(other, c.kv_data, c.kv_scale, c.table, c.n_visible, idx, swa, o3, ws[0])
+            if call == "paged":
+                csa2.csa2_paged_sparse_attn_decode(q, c.kv_data, c.kv_scale, c.table, c.n_visible, idx, swa, got, ws[1])
+            else:
+                csa2.csa2_sparse_attn_decode(q, flat[0], flat[1], c.n_visible, idx, swa, got, ws[2])
+            if want is None:
+                want = got
+            assert torch.equal(got, want), (i, call)
+    assert csa2.csa2_get_last_error() == 0
+
+
 # ---- index scores ---------------------------------------------------------------------
 
 
