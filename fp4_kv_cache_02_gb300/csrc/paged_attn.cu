@@ -1135,8 +1135,8 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
     return CSA2_ERR_ALIGNMENT;
   if (n_tokens == 0 || B == 0) return CSA2_OK;
   const int G = paged_attn_ctas();
-  // a CTA counts its tiles, no more than its units, in 32 bits
-  if ((int64_t)n_tokens * ((a.pages.capacity() + pattn::kRows) / pattn::kRows + pattn::kTokenUnits) / G >= 0x7FFFFFFELL)
+  // a CTA counts its tiles' four groups in 32 bits (and has no more tiles than units)
+  if ((int64_t)n_tokens * ((a.pages.capacity() + pattn::kRows) / pattn::kRows + pattn::kTokenUnits) / G >= 0x3FFFFFFELL)
     return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (!workspace || !csa2_aligned(workspace, 256) ||
       workspace_bytes < csa2_paged_attn_workspace_size(n_tokens, B))

@@ -117,6 +117,14 @@ def test_dense(lib, change, status):
     assert call(lib.csa2_paged_attn, DENSE, DENSE_GOOD, **change) == status
 
 
+def test_dense_refuses_more_tiles_than_it_counts(lib):
+    """2^24 tiles a token: a CTA (of 152, the number without a device too) may have 2^30."""
+    many = dict(page=1 << 20, n_pages=1, max_pages=2048, cu=P)
+    for n in (9728, 12000, 1 << 20):
+        assert call(lib.csa2_paged_attn, DENSE, DENSE_GOOD, **many, n=n) == SHAPE
+    assert call(lib.csa2_paged_attn, DENSE, DENSE_GOOD, **many, n=9000) == WORKSPACE
+
+
 def test_workspace_sizes(lib):
     sparse = lib.csa2_paged_sparse_attn_workspace_size
     assert sparse(32, 1, 512, 128) > sparse(32, 1, 256, 128) > 0
