@@ -104,13 +104,14 @@ struct Params {
 // number. Where CTAs have several tiles each (p.spread > 0), each sequence has
 // one CTA and the grid's others go to the sequences in proportion to their
 // tiles, a tile that only has -inf written to it counting an eighth (512 bytes
-// against 9,200): 23.5 us over 32 sequences of 21,845 to 65,536 entries, 27.0
-// with equal shares. Every warp works it out for itself; false for the few CTAs
-// that the rounding leaves over. The CTAs of a sequence lie p.spread apart, so
-// that each has its part of the SMs with two CTAs and of those with three (30.0
+// against 9,200): 22.4 us over 32 sequences of 21,845 to 65,536 entries, 25.3
+// with equal shares (32 of 65,536 each lose by it: 30.4 us against 29.2). Every warp
+// works it out for itself; false for the few CTAs that the rounding leaves over. The
+// CTAs of a sequence lie p.spread apart, so
+// that each has its part of the SMs with two CTAs and of those with three (30.4
 // us over 32 equal sequences; 31.8 side by side). Where the sequences' longest
 // has a CTA a tile, or there are no CTAs to spare, the shares are equal (5
-// sequences of at most 9,001 entries: 6.5 us, and 8.6 with the work above).
+// sequences of at most 9,001 entries: 5.9 us, and 8.8 with the work above).
 __device__ __forceinline__ bool paged_share(const Params& p, int lane, int& b, int& chunk, int& n_chunks) {
   const int B = p.B;
   if (p.spread == 0) {
@@ -309,17 +310,17 @@ __global__ void __launch_bounds__(kThreads, 3)
     // 8g + j has run j of tile g of the pair. While a pair's copies are issued,
     // the next pair's pages are being looked up and the pair after that is being
     // claimed: in turn the three would take two round trips to L2 and the wait
-    // for a stage for each pair (50.5 us over 32 sequences of 65,536 entries, against
-    // 31.5 as here with the same ranges). Pages past the visible entries are not
+    // for a stage for each pair (20 us more over 32 sequences of 65,536 entries when
+    // it was measured, with the same ranges). Pages past the visible entries are not
     // looked up; what a missing page leaves in the stage is never scored (s_mask).
     const int run_shift = p.pages.shift < 7 ? p.pages.shift : 7;
     const int run = 1 << run_shift;
     const int g = lane >> 3, j = lane & 7;
     const int32_t* places = p.pages.table + (int64_t)b * p.pages.max_pages;
     // Seven eighths of the tiles are fixed ranges, the last eighth is claimed: that
-    // evens out the CTAs' different shares of the bandwidth (28.8 us over 32
-    // sequences of 65,536 entries; 29.4 with three quarters fixed, 31.4 with six
-    // tiles each, 30.5 with all fixed).
+    // evens out the CTAs' different shares of the bandwidth (30.4 us over 32
+    // sequences of 65,536 entries; 30.7 with three quarters fixed, 33.1 with six
+    // tiles each, 32.5 with all fixed).
     const int64_t part = (int64_t)t_vis * 7 / 8 / n_chunks;
     const int64_t own = !claimed || n_chunks == 1 ? per : part > 0 ? part : 1;
     const int64_t fixed0 = (int64_t)chunk * own;

@@ -129,10 +129,11 @@ __device__ __forceinline__ void resolve_token(const AppendArgs& a, int32_t i, in
 // kPerWarp consecutive tokens to a warp: their rows of the pool are looked up
 // by as many lanes at once (the chain boundary -> count -> page -> angles is
 // four dependent reads), while the rows of all of them are on their way.
-// Bound: 1,636 bytes an entry would take 19 us for 76,801 entries in pages of 16;
-// 39.5 us measured (3.2 TB/s), 31 without a rotation. About 300 instructions an
-// entry keep the schedulers 60 % busy, and a warp's entries wait for their angles
-// one after another (all four's at once took 43.6 us). A step of 32: 3.1 us.
+// Bound: 1,636 bytes an entry would take 19 us for 76,831 entries in pages of 16;
+// 39.5 us measured (3.2 TB/s), 29.0 without a rotation. 397 warp instructions an
+// entry keep the schedulers 62 % busy, with 22 warps on an SM (79 registers a
+// thread), and a warp's entries wait for their angles one after another (all four's
+// at once took longer). A step of 32: 3.2 us.
 template <int kPerWarp>
 __global__ void __launch_bounds__(kPagedWarps * 32) paged_append_kernel(AppendArgs a) {
   static_assert(kIdxDim == 32 * 4 && kHeadDim == 32 * 16, "a lane holds 16 latent and 4 key channels");
@@ -236,7 +237,7 @@ __global__ void advance_paged_kernel(int32_t* __restrict__ n_visible, const int3
 // worth, and no lane waits for another's rotation.
 // Bound by HBM: 4,096 x 64 rows of 512 in 82 us, 6.5 TB/s of 4 bytes an element
 // (two rows to a warp 94 us, eight 103; one thread to a 16-byte chunk, its row
-// found by division, 157). The queries of a step of 32 take 2.7 us.
+// found by division, 157). The queries of a step of 32 take 2.6 us.
 struct RopeArgs {
   const uint16_t* x;
   uint16_t* out;

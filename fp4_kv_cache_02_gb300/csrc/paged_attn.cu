@@ -21,10 +21,10 @@
 // memory 1,024 (32 a product, 48 from shared memory), O^T 1,536 (48: A and B
 // both from shared memory). Beside them a tile costs 2,880 wavefronts of shared
 // memory (the rows as fp16 written once, the codes read twice, P, the waits) and
-// 3,050 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
+// 3,060 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
 // Measured 4,600 to 4,900 cycles a tile: 32 sequences of 65,536 entries 288 us
 // (954 TFLOP/s, 49 % of the measured bf16 rate; 2.1 TB/s), 2,048 tokens of a
-// prompt behind 6,144 entries 1.94 ms (994 TFLOP/s), 24 sequences of 1 to 4
+// prompt behind 6,144 entries 1.92 ms (1,002 TFLOP/s), 24 sequences of 1 to 4
 // tokens over up to 16,385 entries 108 us, one token over 317 entries 17 us (2.5
 // the set-up, 2 the queries, 5 the tile's chain, 2 the output, 4 the joining
 // kernel). A token costs 9,000 cycles beside its tiles, while the pipeline runs
@@ -1167,8 +1167,8 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   cuuint64_t strides[1] = {(cuuint64_t)kKvBytes};
   cuuint32_t box[2] = {64, (cuuint32_t)(page_size < pattn::kRows ? page_size : pattn::kRows)};
   cuuint32_t estr[2] = {1, 1};
-  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)(pool > 0 ? (const void*)kv_data : q_bf16), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  void* plane = (void*)(pool > 0 ? (const void*)kv_data : q_bf16);
+  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, plane, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return CSA2_ERR_CUDA;
   // the queries, in boxes of a token's 64 heads by 64 channels

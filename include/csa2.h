@@ -695,8 +695,10 @@ int csa2_paged_sparse_attn_decode(const void* q_bf16, int32_t B, int32_t L,
                                   float* out_f32, float* lse, void* workspace,
                                   size_t workspace_bytes, csa2_stream_t stream);
 
-/** Bytes of workspace csa2_paged_attn needs on the current device (it depends
- *  on n_tokens only up to the device's number of SMs). */
+/** Bytes of workspace csa2_paged_attn needs on the current device: the same for
+ *  every n_tokens > 0 and B > 0, two parts of 128 KiB per SM and their lists
+ *  (38 MiB on 152 SMs), 0 otherwise. One buffer serves calls of any size, one
+ *  after another. */
 size_t csa2_paged_attn_workspace_size(int32_t n_tokens, int32_t B);
 
 /**
