@@ -33,7 +33,9 @@
 //      operand; the unnormalised O is staged in shared memory and sent to the
 //      workspace by one bulk copy, (m, l) by plain stores.
 // The SWA tiles depend on nothing the kernel before this one writes, so they
-// run before the programmatic-launch wait; only the selected tiles follow it.
+// run before the programmatic-launch wait; only the selected tiles follow it,
+// and the partials: the kernel before may be a call with the same workspace
+// whose merge still reads its own.
 // Merge: after one cluster barrier (release / acquire) CTA r bulk-copies the
 // slices of heads [64r/C, 64(r+1)/C) of every partial from the workspace
 // (L2), weighs them by 2^(m_j - M) / L in fixed partial order
@@ -431,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // `layer` in sQ, giving partial `part` of that layer's query. next_layer >= 0:
   // the layer of the CTA's next pass, whose Q is loaded into sQ as soon as
   // this pass's S^T is complete. more_rows: R is rewritten after this pass ----
+  bool waited = false;  // for the kernel before this one
   auto attend = [&](const int layer, const int part, const int next_layer, const bool more_rows) {
     const uint32_t par = passes_done & 1u;
     // ---- S^T = R Q^T ----
@@ -601,6 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // w % 4 in block w / 4 (cb = 4 (w / 4) + w % 4), all 64 heads; a partial is
     // laid out [cb][h][32] ----
     if (!kSeq) {
+      if (!waited) {
+        pdl_wait();
+        waited = true;
+      }
       const int cb = (warp >> 2) * 4 + rq;
       const uint32_t o_base = tmem + ((uint32_t)(rq * 32) << 16) + kColO + 64u * (uint32_t)(warp >> 2);
       float* dst = part_o_u + (((int64_t)layer * n_part + part) * 16 + cb) * (kHeads * 32);
@@ -648,7 +655,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // items j of the list [SWA tiles, selected tiles] belong to CTA j mod C; the
   // SWA tiles come first, before the wait for the indices
-  bool waited = false;
 #pragma unroll 1
   for (int j = rank; j < n_items; j += C) {
     const bool swa = j < L * n_swt;

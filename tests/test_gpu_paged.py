@@ -752,6 +752,56 @@ def test_sparse_attention_equals_the_flat_call(csa2, page, B, L, k, n_swa):
         assert torch.allclose(res[0][1], res[1][1], rtol=0, atol=2.0 ** -10)
 
 
+@pytest.mark.parametrize("form,B,L,k,n_swa", [("reuse", 3, 4, 512, 128)] + [
+    (form, *shape) for form in ("paged", "flat")
+    for shape in ((1, 1, 512, 128), (3, 4, 512, 128), (20, 1, 128, 128), (2, 1, 128, 512), (40, 1, 512, 16))])
+def test_selected_attention_calls_in_a_row_share_a_workspace(csa2, form, B, L, k, n_swa):
+    """Layer after layer with one workspace, eager and captured: a call may not write its partials while the call before it still
+    reads its own (it starts on its window before that call has ended)."""
+    g = gen(106)
+    lens = [700 - 10 * b for b in range(B)]
+    c = Cache(csa2, lens, 64, 107)
+    flat = c.flat_planes()
+    idx = torch.stack([torch.randperm(min(lens), generator=g, device="cuda")[:k].sort().values for _ in range(B)]).int()
+    if idx.shape[1] < k:
+        idx = torch.cat([idx, torch.full((B, k - idx.shape[1]), -1, dtype=torch.int32, device="cuda")], 1)
+    idx = idx.contiguous()
+    layers = [(normal(g, B, L, 64, 512, scale=512 ** -0.5), csa2.pack_fp8(normal(g, B, L, n_swa, 512, scale=i + 1.0))) for i in range(4)]
+    ws = csa2.paged_sparse_attn_workspace(B, L, k, n_swa)
+
+    def call(i, out):
+        q, swa = layers[i]
+        if form == "paged":
+            csa2.csa2_paged_sparse_attn_decode(q, c.kv_data, c.kv_scale, c.table, c.n_visible, idx, swa, out, ws)
+        elif form == "flat":
+            csa2.csa2_sparse_attn_decode(q, flat[0], flat[1], c.n_visible, idx, swa, out, ws)
+        else:
+            csa2.csa2_sparse_attn_reuse(q, flat[0], flat[1], c.n_visible, idx, swa, out, ws)
+
+    outs = [torch.empty_like(q) for q, _ in layers]
+    for i, o in enumerate(outs):
+        call(i, o)
+        torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, o in enumerate(outs):
+            call(i, o)
+    for n in range(40):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        if n % 2:
+            graph.replay()
+        else:
+            for i, o in enumerate(outs):
+                call(i, o)
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, want)):
+            assert torch.equal(a, b), (n, i)
+    assert csa2.csa2_get_last_error() == 0
+
+
 def test_sparse_attention_skips_what_is_not_there(csa2):
     """Entries at or past n_visible and entries of missing pages are left out and reported."""
     g = gen(33)
