@@ -107,11 +107,11 @@ struct Params {
 // against 9,200): 22.4 us over 32 sequences of 21,845 to 65,536 entries, 25.3
 // with equal shares (32 of 65,536 each lose by it: 30.4 us against 29.2). Every warp
 // works it out for itself; false for the few CTAs that the rounding leaves over. The
-// CTAs of a sequence lie p.spread apart, so
-// that each has its part of the SMs with two CTAs and of those with three (30.4
-// us over 32 equal sequences; 31.8 side by side). Where the sequences' longest
-// has a CTA a tile, or there are no CTAs to spare, the shares are equal (5
-// sequences of at most 9,001 entries: 5.9 us, and 8.8 with the work above).
+// CTAs of a sequence lie p.spread apart, so that each has its part of the SMs with
+// two CTAs and of those with three (30.4 us over 32 equal sequences; 31.8 side by
+// side). Where the sequences' longest has a CTA a tile, or there are no CTAs to
+// spare, the shares are equal (5 sequences of at most 9,001 entries: 5.9 us, and 8.8
+// with the work above).
 __device__ __forceinline__ bool paged_share(const Params& p, int lane, int& b, int& chunk, int& n_chunks) {
   const int B = p.B;
   if (p.spread == 0) {

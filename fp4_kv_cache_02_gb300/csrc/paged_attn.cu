@@ -1168,7 +1168,8 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   cuuint32_t box[2] = {64, (cuuint32_t)(page_size < pattn::kRows ? page_size : pattn::kRows)};
   cuuint32_t estr[2] = {1, 1};
   void* plane = (void*)(pool > 0 ? (const void*)kv_data : q_bf16);
-  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, plane, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  if (encode(&rows_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, plane, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return CSA2_ERR_CUDA;
   // the queries, in boxes of a token's 64 heads by 64 channels
