@@ -24,7 +24,7 @@
 // 3,060 issue slots per scheduler, most of them conversions: 65,536 codes, twice.
 // Measured 4,600 to 4,900 cycles a tile: 32 sequences of 65,536 entries 288 us
 // (954 TFLOP/s, 49 % of the measured bf16 rate; 2.1 TB/s), 2,048 tokens of a
-// prompt behind 6,144 entries 1.92 ms (1,002 TFLOP/s), 24 sequences of 1 to 4
+// prompt behind 6,144 entries 1.93 ms (1,000 TFLOP/s), 24 sequences of 1 to 4
 // tokens over up to 16,385 entries 108 us, one token over 317 entries 17 us (2.5
 // the set-up, 2 the queries, 5 the tile's chain, 2 the output, 4 the joining
 // kernel). A token costs 9,000 cycles beside its tiles, while the pipeline runs
@@ -765,11 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 32; ++i) l_acc[i] = 0.0f;
       if (tid < kHeads) sh.ref[tid] = 0.0f;
       uint32_t tokens = 0;  // of the run, with queries converted
-      // three times at a token's end, twice at the run's: phases 3 (tokens - 1) ..
+      // three times at a token's end, twice at the run's: phases 3 (tokens - 1) .. (not
+      // wait(): the shorter loop is 0.5 % of a prompt chunk)
       const auto meet = [&](uint32_t phase) {
         arrive(&sh.soft);
-        while (!tc::mbar_try_wait(&sh.soft, phase & 1u) && !sh.abort) {
-        }
+        for (uint32_t n = 0; !tc::mbar_try_wait(&sh.soft, phase & 1u) && !sh.abort;)
+          if (++n >= kWaitTries) sh.abort = 1;
         __syncwarp();
       };
       convert_q(tokens++);
