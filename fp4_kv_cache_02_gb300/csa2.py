@@ -32,6 +32,7 @@ CAP_ALIGN = 128
 MAX_TOPK = 4096
 MIN_PAGE = 16
 MAX_ROPE_DIM = 128
+FP4_FORMATS = {"e8m0": 0, "e4m3": 1}  # scales of packed weights: E8M0 per 32 inputs, E4M3 per 16
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "misaligned",
           -4: "CUDA error", -5: "device wait timed out", -6: "workspace", -7: "device rejected input",
@@ -105,6 +106,10 @@ def _load():
         "csa2_paged_attn_workspace_size": (sz, [i32, i32]),
         "csa2_paged_attn": (ctypes.c_int, [vp, i32, vp, i32, vp, vp, i64, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp,
                                            sz, vp]),
+        "csa2_fp4_weights_size": (sz, [i32, i32, i32]),
+        "csa2_fp4_weights": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp]),
+        "csa2_fp4_linear_workspace_size": (sz, [i32, i32, i32]),
+        "csa2_fp4_linear": (ctypes.c_int, [vp, i32, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -638,6 +643,52 @@ def csa2_paged_attn(q, kv_data, kv_scale, page_table, n_visible, out, workspace,
           ws_at, workspace.numel(), _s(stream))
 
 
+# ---- products with 4-bit weights ---------------------------------------------------
+
+def _format(name):
+    if name not in FP4_FORMATS:
+        raise ValueError(f"format must be one of {', '.join(FP4_FORMATS)}, got {name!r}")
+    return FP4_FORMATS[name]
+
+
+def csa2_fp4_weights_size(n_out, n_in, format) -> int:
+    """Bytes of the laid-out form of an n_out x n_in matrix."""
+    return int(_lib.csa2_fp4_weights_size(n_out, n_in, _format(format)))
+
+
+def csa2_fp4_weights(data, scale, weights, format, stream=None):
+    """data [n_out, n_in / 2] u8 and scale [n_out, n_in / 32 (e8m0) or / 16 (e4m3)]
+    u8, as the encoders pack them -> weights (u8, csa2_fp4_weights_size bytes)."""
+    dev = _device(data, "data")
+    if data.dim() != 2:
+        raise ValueError("data must be [n_out, n_in / 2]")
+    n_out, n_in = data.shape[0], 2 * data.shape[1]
+    scale_at = _shaped(scale, torch.uint8, (n_out, n_in // (16 if format == "e4m3" else 32)), "scale", dev)
+    if weights.numel() < csa2_fp4_weights_size(n_out, n_in, format):
+        raise ValueError("weights needs csa2_fp4_weights_size(n_out, n_in, format) bytes")
+    _call("csa2_fp4_weights", _take(data, torch.uint8, "data", dev), scale_at, n_out, n_in, _format(format),
+          _take(weights, torch.uint8, "weights", dev), _s(stream))
+
+
+def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None, stream=None):
+    """x [n_tokens, n_in] bf16, weights from csa2_fp4_weights -> out [n_tokens,
+    n_out] bf16 = scale * x W^T and / or out_f32, the same in fp32 (either may be
+    None, not both)."""
+    dev = _device(x, "x")
+    x_at, w_at = _take(x, torch.bfloat16, "x", dev), _take(weights, torch.uint8, "weights", dev)
+    ws_at = _take(workspace, torch.uint8, "workspace", dev)
+    to = out_f32 if out is None else out
+    if x.dim() != 2 or to is None or to.dim() != 2 or to.shape[0] != x.shape[0]:
+        raise ValueError("x must be [n_tokens, n_in], out or out_f32 [n_tokens, n_out]")
+    (n, n_in), n_out = x.shape, to.shape[1]
+    kind = _format(format)
+    if weights.numel() < _lib.csa2_fp4_weights_size(n_out, n_in, kind):
+        raise ValueError(f"weights holds fewer than {n_out} x {n_in} weights")
+    _call("csa2_fp4_linear", x_at, n, w_at, n_out, n_in, kind, float(scale),
+          _optional(out, torch.bfloat16, (n, n_out), "out", dev), _optional(out_f32, torch.float32, (n, n_out), "out_f32", dev),
+          ws_at, workspace.numel(), _s(stream))
+
+
 # ---- allocating helpers (torch memory plumbing + the entry points above) --------
 
 def _ws(nbytes, device):
@@ -691,3 +742,15 @@ def paged_attn_workspace(n_tokens, B, device="cuda"):
 
 def paged_sparse_attn_workspace(B, L, k, n_swa, device="cuda"):
     return _ws(_lib.csa2_paged_sparse_attn_workspace_size(B, L, k, n_swa), device)
+
+
+def fp4_weights(data, scale, format, stream=None):
+    """Packed weights laid out for csa2_fp4_linear."""
+    weights = torch.empty(csa2_fp4_weights_size(data.shape[0], 2 * data.shape[1], format), dtype=torch.uint8,
+                          device=data.device)
+    csa2_fp4_weights(data, scale, weights, format, stream)
+    return weights
+
+
+def fp4_linear_workspace(n_tokens, n_in, format, device="cuda"):
+    return _ws(_lib.csa2_fp4_linear_workspace_size(n_tokens, n_in, _format(format)), device)

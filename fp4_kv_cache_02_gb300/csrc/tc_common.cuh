@@ -216,6 +216,8 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32
          | ((M >> 4) & 31u) << 24 // M
          | (a_sf_id & 3u) << 29;  // scale factor A data id
 }
+// The same with UE4M3 scales, one per 16 (kind::mxf4nvf4).
+__host__ __device__ constexpr uint32_t idesc_nvf4(uint32_t M, uint32_t N) { return idesc_mxf4(M, N, 0, 0) & ~(1u << 23); }
 // kind::f16 with bf16 A/B, fp32 accumulate; a_mn / b_mn select MN-major operands.
 __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4)                // D format: f32
@@ -268,6 +270,32 @@ __device__ __forceinline__ void mma_f16_ta_one(uint32_t one, uint32_t d_tmem, ui
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
+// Block-scaled E2M1 x E2M1, K = 64: one UE8M0 scale per 32 or (kE4M3) one UE4M3 per 16.
+template <bool kE4M3>
+__device__ __forceinline__ void mma_fp4_one(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if constexpr (kE4M3)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %7, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem), "r"(one)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %7, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_cp_32x128_x4_one(uint32_t one, uint32_t taddr, uint64_t sdesc) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(sdesc), "r"(one)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit_one(uint32_t one, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
@@ -303,6 +331,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // 32 registers per thread into 32 lanes x 32 consecutive 32-bit columns.

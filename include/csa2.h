@@ -738,6 +738,62 @@ int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32_t* cu_q,
                     void* out_bf16, float* out_f32, float* lse, void* workspace,
                     size_t workspace_bytes, csa2_stream_t stream);
 
+/* ======================================================================== */
+/* Products with 4-bit weights                                               */
+/* ======================================================================== */
+
+/* A matrix W [n_out][n_in] of packed weights: E2M1 codes [n_out][n_in/2] and scales
+ *     CSA2_FP4_E8M0  one E8M0 per 32 inputs [n_out][n_in/32] (csa2_quant_mxfp4),
+ *     CSA2_FP4_E4M3  one E4M3 per 16 inputs [n_out][n_in/16], not negative, not NaN
+ *                    (csa2_pack_kv_fp4 over the matrix as rows of 512).
+ * n_in is a multiple of 32. */
+#define CSA2_FP4_E8M0 0
+#define CSA2_FP4_E4M3 1
+
+/** Bytes of the laid-out form of an n_out x n_in matrix (rows rounded up to 128,
+ *  inputs to 256); 0 for sizes or a format that are refused. */
+size_t csa2_fp4_weights_size(int32_t n_out, int32_t n_in, int32_t format);
+
+/**
+ * Lays packed weights out for csa2_fp4_linear, once for a matrix: blocks of 128
+ * rows x 256 inputs as the tensor cores read them, codes and scales unchanged.
+ *   data, weights 16-byte aligned; weights has csa2_fp4_weights_size bytes, all of
+ *   them written.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, CUDA.
+ */
+int csa2_fp4_weights(const uint8_t* data, const uint8_t* scale, int32_t n_out,
+                     int32_t n_in, int32_t format, uint8_t* weights,
+                     csa2_stream_t stream);
+
+/** Bytes of workspace csa2_fp4_linear needs: the same for every n_out. */
+size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in,
+                                      int32_t format);
+
+/**
+ * out[t][n] = scale * sum_k x[t][k] * W[n][k]: the projections around the cache
+ * (report section 2.3: latents, indexer keys and queries; notes section 4.4: FP4
+ * weights), from one token, a matrix-vector product, to a prompt.
+ *   x [n_tokens][n_in] bf16; weights from csa2_fp4_weights with the same n_out, n_in
+ *   and format; out_bf16 and out_f32 [n_tokens][n_out], at least one of them
+ *   (rounded from the same fp32 value).
+ *   Precision: a token's blocks of 32 (E8M0) or 16 (E4M3) channels enter as sums of
+ *   eight E2M1 vectors: exact for channels within 2^-14 of their block's largest,
+ *   off by at most 2^-22 of the largest otherwise (with E4M3 scales, or 2^-39 of the
+ *   token's largest; with either, or 2^-121). Products are exact, sums in fp32. A
+ *   token with an infinity or a NaN has NaN in all its outputs; other tokens do not
+ *   notice it. The same call gives the same bits; a token's result may differ in the
+ *   last fp32 bits with the number of tokens.
+ *   x, weights 16-byte aligned; the outputs must not overlap anything that is read.
+ *   workspace: csa2_fp4_linear_workspace_size bytes, 256-byte aligned, contents
+ *   need not be kept; calls that may run at the same time need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA.
+ */
+int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens,
+                    const uint8_t* weights, int32_t n_out, int32_t n_in,
+                    int32_t format, float scale, void* out_bf16, float* out_f32,
+                    void* workspace, size_t workspace_bytes,
+                    csa2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
