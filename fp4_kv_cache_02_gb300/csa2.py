@@ -32,6 +32,8 @@ CAP_ALIGN = 128
 MAX_TOPK = 4096
 MIN_PAGE = 16
 MAX_ROPE_DIM = 128
+MAX_BEAMS = 256
+MAX_BEAM_K = 64
 FP4_FORMATS = {"e8m0": 0, "e4m3": 1}  # scales of packed weights: E8M0 per 32 inputs, E4M3 per 16
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "misaligned",
@@ -110,6 +112,10 @@ def _load():
         "csa2_fp4_weights": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp]),
         "csa2_fp4_linear_workspace_size": (sz, [i32, i32, i32]),
         "csa2_fp4_linear": (ctypes.c_int, [vp, i32, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]),
+        "csa2_beam_select_workspace_size": (sz, [i32, i32, i32, i32]),
+        "csa2_beam_select": (ctypes.c_int, [vp, i32, i32, i32, i32, i64, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
+        "csa2_paged_reorder": (ctypes.c_int, [vp, vp, i32, vp, vp, vp, vp, i32, i64, i32, vp, i32, i32, vp, vp, vp, vp]),
+        "csa2_reorder_rows": (ctypes.c_int, [vp, i64, i64, vp, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -689,6 +695,84 @@ def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None,
           ws_at, workspace.numel(), _s(stream))
 
 
+# ---- beam search -------------------------------------------------------------------
+
+def csa2_beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, lse=None, stream=None):
+    """logits [B, W, V] bf16 or fp32 (rows any distance apart, elements adjacent),
+    scores [B, W] fp32 or None -> the k best (beam, token) pairs of each sequence:
+    out_scores fp32, out_parents (rows b * W + w) and out_tokens int32 [B, k]; lse
+    [B, W] fp32 is optional."""
+    dev = out_scores.get_device() if out_scores is not None else -1
+    if logits.dim() != 3 or logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [B, W, V] of bf16 or fp32")
+    if logits.get_device() != dev or dev != torch.cuda.current_device():
+        raise ValueError(f"logits and out_scores must be on the current device, cuda:{torch.cuda.current_device()}")
+    B, W, V = logits.shape
+    ld = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != W * ld):
+        raise ValueError("logits must have adjacent elements and equally distant rows")
+    if out_scores.dim() != 2 or out_scores.shape[0] != B:
+        raise ValueError("out_scores must be [B, k]")
+    k = out_scores.shape[1]
+    _call("csa2_beam_select", logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0, B, W, V, ld,
+          _optional(scores, torch.float32, (B, W), "scores", dev), k,
+          _take(out_scores, torch.float32, "out_scores", dev),
+          _shaped(out_parents, torch.int32, (B, k), "out_parents", dev),
+          _shaped(out_tokens, torch.int32, (B, k), "out_tokens", dev),
+          _optional(lse, torch.float32, (B, W), "lse", dev),
+          _take(workspace, torch.uint8, "workspace", dev), workspace.numel(), _s(stream))
+
+
+def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_out, n_visible_out, kv_data=None,
+                       kv_scale=None, ik_data=None, ik_scale=None, stream=None):
+    """Row r takes over the entries of row parents[r] [R] int32: full pages shared, a
+    partly filled last page copied into fresh_pages[r] for all rows but the first with
+    that parent. Planes [n_pages, page, width], or [layers, n_pages, page, width] for
+    caches that share the table; page_table [rows, max_pages] -> page_table_out [R,
+    max_pages], n_visible [rows] -> n_visible_out [R]."""
+    dev = _device(parents, "parents")
+    if parents.dim() != 1:
+        raise ValueError("parents must be [R]")
+    R = parents.shape[0]
+    at, pool = [], None
+    for t, width, name in ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"),
+                           (ik_scale, 4, "ik_scale")):
+        if t is None:
+            at.append(None)
+            continue
+        at.append(_take(t, torch.uint8, name, dev))
+        shape = t.shape if t.dim() == 4 else (1, *t.shape)
+        if len(shape) != 4 or (pool is not None and pool != shape[:3]) or shape[3] != width:
+            raise ValueError(f"{name} must be [layers, n_pages, page_size, {width}] like the other planes")
+        pool = tuple(shape[:3])
+    if pool is None or (kv_data is None) != (kv_scale is None) or (ik_data is None) != (ik_scale is None):
+        raise ValueError("codes and scales of the latents, of the keys, or of both are required")
+    table = _take(page_table, torch.int32, "page_table", dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, max_pages]")
+    rows, max_pages = page_table.shape
+    _call("csa2_paged_reorder", _shaped(parents, torch.int32, (R,), "parents", dev),
+          _shaped(fresh_pages, torch.int32, (R,), "fresh_pages", dev), R, *at, pool[0], pool[1], pool[2], table, rows,
+          max_pages, _shaped(n_visible, torch.int32, (rows,), "n_visible", dev),
+          _shaped(page_table_out, torch.int32, (R, max_pages), "page_table_out", dev),
+          _shaped(n_visible_out, torch.int32, (R,), "n_visible_out", dev), _s(stream))
+
+
+def csa2_reorder_rows(src, parents, dst, stream=None):
+    """dst[r] = src[parents[r]]: src [rows, ...], dst [R, ...] of any one type, rows of
+    a multiple of 16 bytes; parents [R] int32, -1 leaves a row as it was."""
+    dev = _device(src, "src")
+    src_at, dst_at = _take(src, src.dtype, "src", dev), _take(dst, src.dtype, "dst", dev)
+    if src.dim() < 1 or dst.dim() != src.dim() or dst.shape[1:] != src.shape[1:]:
+        raise ValueError("src must be [rows, ...] and dst [R, ...] with rows alike")
+    size = src.element_size()
+    for n in src.shape[1:]:
+        size *= n
+    R = dst.shape[0]
+    _call("csa2_reorder_rows", src_at, src.shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R, dst_at,
+          _s(stream))
+
+
 # ---- allocating helpers (torch memory plumbing + the entry points above) --------
 
 def _ws(nbytes, device):
@@ -754,3 +838,7 @@ def fp4_weights(data, scale, format, stream=None):
 
 def fp4_linear_workspace(n_tokens, n_in, format, device="cuda"):
     return _ws(_lib.csa2_fp4_linear_workspace_size(n_tokens, n_in, _format(format)), device)
+
+
+def beam_select_workspace(B, W, V, k, device="cuda"):
+    return _ws(_lib.csa2_beam_select_workspace_size(B, W, V, k), device)

@@ -235,3 +235,4 @@ int csa2_read_and_clear_attn_error(cudaStream_t s);
 int csa2_read_and_clear_paged_error(cudaStream_t s);
 int csa2_read_and_clear_paged_attn_error(cudaStream_t s);
 int csa2_read_and_clear_linear_error(cudaStream_t s);
+int csa2_read_and_clear_beam_error(cudaStream_t s);

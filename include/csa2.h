@@ -794,6 +794,86 @@ int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens,
                     void* workspace, size_t workspace_bytes,
                     csa2_stream_t stream);
 
+/* ======================================================================== */
+/* Beam search                                                               */
+/* ======================================================================== */
+
+#define CSA2_MAX_BEAMS 256
+#define CSA2_MAX_BEAM_K 64
+
+/** Bytes of workspace csa2_beam_select needs. */
+size_t csa2_beam_select_workspace_size(int32_t B, int32_t W, int32_t V,
+                                       int32_t k);
+
+/**
+ * Beam search's selection: for each of B sequences with W beams the k best of the
+ * W * V candidates (w, v) by
+ *     scores[b][w] + x[b][w][v] - log sum_u exp(x[b][w][u]),
+ * falling, ties to the lowest w * V + v (W = 1: the k likeliest tokens of each row).
+ *   logits: row b * W + w begins at element (b * W + w) * ld, ld >= V; bf16, or fp32
+ *   with logits_f32 = 1. A logit of -inf is no candidate. A row whose logits are all
+ *   -inf takes no part, nor does one whose score is not finite (a beam that is not in
+ *   use); a row that holds a NaN or +inf takes none either and is reported as DEVICE.
+ *   (A beam that has ended stands by itself with 0 for its end token and -inf for the
+ *   others.)
+ *   scores [B][W] fp32, NULL: 0. out_scores [B][k] fp32; out_parents [B][k] int32, the
+ *   row b * W + w (what csa2_paged_reorder takes); out_tokens [B][k] int32. Behind the
+ *   last candidate: -inf, -1, -1. lse (nullable) [B][W] fp32: the rows' log sums (NaN
+ *   for one that holds a NaN or +inf).
+ *   Sums are held in fp32, scores in 64 bits until they are written. The result is
+ *   deterministic.
+ *   1 <= k <= CSA2_MAX_BEAM_K, 1 <= W <= CSA2_MAX_BEAMS, B * W < 2^23.
+ *   workspace: csa2_beam_select_workspace_size bytes, 256-byte aligned; calls that may
+ *   run at the same time need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA.
+ */
+int csa2_beam_select(const void* logits, int32_t logits_f32, int32_t B,
+                     int32_t W, int32_t V, int64_t ld, const float* scores,
+                     int32_t k, float* out_scores, int32_t* out_parents,
+                     int32_t* out_tokens, float* lse, void* workspace,
+                     size_t workspace_bytes, csa2_stream_t stream);
+
+/**
+ * Reordering of paged sequences after a selection (or forking them): row r of the new
+ * batch takes over the entries of row parents[r] of the old one. Full pages are
+ * shared. The partly filled last page, which the next append writes, goes to the
+ * lowest r with that parent; every other row gets its entries copied into page
+ * fresh_pages[r].
+ *   parents [R] int32, 0 .. rows_in-1; -1: row r is empty (its count is 0).
+ *   fresh_pages [R] int32: looked at only where a copy is needed (page_table_out then
+ *   holds it); those pages must be in use by nothing else, each given to one row.
+ *   kv_data, kv_scale, ik_data, ik_scale: planes [layers][n_pages][page_size][..] of the
+ *   pool, the layers' caches sharing one table; either pair may be NULL.
+ *   page_table [rows_in][max_pages], n_visible [rows_in]; page_table_out [R][max_pages],
+ *   n_visible_out [R], which must not overlap them. Only the first
+ *   ceil(n / page_size) places of a row of page_table_out are written.
+ *   A parent that is neither -1 nor a row, or whose count is negative or above
+ *   max_pages * page_size, leaves row r's place and count as they were; a copy whose
+ *   page or source is outside the pool leaves -1 in the table. Both are reported as
+ *   DEVICE.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, CUDA.
+ */
+int csa2_paged_reorder(const int32_t* parents, const int32_t* fresh_pages,
+                       int32_t R, uint8_t* kv_data, uint8_t* kv_scale,
+                       uint8_t* ik_data, uint8_t* ik_scale, int32_t layers,
+                       int64_t n_pages, int32_t page_size,
+                       const int32_t* page_table, int32_t rows_in,
+                       int32_t max_pages, const int32_t* n_visible,
+                       int32_t* page_table_out, int32_t* n_visible_out,
+                       csa2_stream_t stream);
+
+/**
+ * dst[r] = src[parents[r]] for rows of row_bytes bytes: any other state of a sequence,
+ * such as its layers' sliding windows [L][n_swa][512].
+ *   src [rows_in][row_bytes], dst [R][row_bytes], 16-byte aligned, not overlapping;
+ *   row_bytes a multiple of 16. parents[r] = -1 leaves row r as it was; another value
+ *   that is no row too, and is reported as DEVICE.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, CUDA.
+ */
+int csa2_reorder_rows(const void* src, int64_t rows_in, int64_t row_bytes,
+                      const int32_t* parents, int32_t R, void* dst,
+                      csa2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
