@@ -32,7 +32,7 @@ CAP_ALIGN = 128
 MAX_TOPK = 4096
 MIN_PAGE = 16
 MAX_ROPE_DIM = 128
-MAX_BEAMS = 256
+MAX_BEAMS = 64
 MAX_BEAM_K = 64
 FP4_FORMATS = {"e8m0": 0, "e4m3": 1}  # scales of packed weights: E8M0 per 32 inputs, E4M3 per 16
 

@@ -6,6 +6,8 @@
 // Candidate (w, v) of a sequence scores  score[w] + x[w][v] - lse(x[w]),  lse the
 // log of the sum of exp over the vocabulary; the k largest are wanted, ties to the
 // lowest w * V + v.
+#include <float.h>
+
 #include "paged_common.cuh"
 
 namespace csa2 {
@@ -16,9 +18,10 @@ namespace beam {
 
 constexpr int kThreads = 256;
 constexpr int kMaxK = CSA2_MAX_BEAM_K;
-constexpr int kMaxLists = 512;              // lists of a sequence that the joining kernel takes: one a thread
-constexpr int kVectors = 4;                 // 16-byte loads of a thread in a tile
-constexpr int kKeep = 512;                  // candidates held before they are cut down to about k
+constexpr int kX = 16;                      // values of a thread in a tile
+constexpr int kRoom = 2560;                 // candidates that fit
+constexpr int kJoinThreads = 512;
+constexpr int kMaxEntries = 8192;           // entries of a sequence's lists in the joining kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Values by size, equal ones by place, the lower first: larger is better, all
@@ -32,40 +35,64 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 }
 __device__ __forceinline__ uint32_t key_place(uint64_t key) { return ~(uint32_t)key; }
 
-// The k-th largest of the block's keys, one a thread (0: none); 1 when there are
-// fewer than k. Each thread counts the keys above its own.
-__device__ __forceinline__ uint64_t kth_of_block(uint64_t key, int k, uint64_t* s_keys, uint64_t* s_kth) {
+// A bound from below on the k-th largest of the block's values: the k-th largest of
+// 64 (k <= 16) or 128 of them, each the largest of four or two threads' (0: none); 1
+// when there are fewer than k. Each counts the keys above its own: all 256 threads'
+// would take four times the instructions of 128 for a bound that 8 % fewer values reach.
+__device__ __forceinline__ int threads_to_rep(int k) { return k <= 16 ? 4 : 2; }
+__device__ __forceinline__ uint64_t bound_of_block(uint64_t key, int k, uint64_t* s_keys, uint64_t* s_bound) {
+  const int per = threads_to_rep(k), reps = kThreads / per;
+  key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+  if (per == 4) key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
   __syncthreads();
-  s_keys[threadIdx.x] = key;
-  if (threadIdx.x == 0) *s_kth = 1;
+  if (threadIdx.x % per == 0) s_keys[threadIdx.x / per] = key;
+  if (threadIdx.x == 0) *s_bound = 1;
   __syncthreads();
-  int above = 0;
+  if ((int)threadIdx.x < reps) {
+    key = s_keys[threadIdx.x];
+    int above = 0;
 #pragma unroll 8
-  for (int i = 0; i < kThreads; i += 2) {
-    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(s_keys + i);
-    above += (two.x > key) + (two.y > key);
+    for (int i = 0; i < reps; i += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(s_keys + i);
+      above += (two.x > key) + (two.y > key);
+    }
+    if (key != 0 && above == k - 1) *s_bound = key;
   }
-  if (key != 0 && above == k - 1) *s_kth = key;
   __syncthreads();
-  return *s_kth;
+  return *s_bound;
+}
+
+// Two fp32 operations at once (the values come in pairs of registers).
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void mul2(float& a, float& b, float x) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(a), "+f"(b) : "f"(x));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
 }
 
 template <typename T>
-struct Vec;
+struct Vec;  // 16 bytes of logits
 template <>
 struct Vec<float> {
   static constexpr int n = 4;
-  static __device__ __forceinline__ void load(const float* p, float* x) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  static constexpr uint32_t none = 0xFF800000u;  // -inf
+  static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
 };
 template <>
 struct Vec<uint16_t> {
   static constexpr int n = 8;
-  static __device__ __forceinline__ void load(const uint16_t* p, float* x) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+  static constexpr uint32_t none = 0xFF80FF80u;
+  static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -76,7 +103,7 @@ struct Vec<uint16_t> {
   static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
 };
 
-struct Part {     // of a row's softmax: sum of 2^(x log2e - ref)
+struct Part {  // of a row's softmax: its largest value, the sum of exp(x - ref)
   float ref, sum;
 };
 
@@ -90,25 +117,21 @@ struct RowArgs {
 };
 
 // One CTA reads a part of a row once: the softmax's running reference and sum, and
-// the part's k largest. A tile of the part is in registers at a time. The k-th
-// largest of the threads' own largest values bounds the k-th largest from below;
-// what reaches the bound goes to a list in shared memory, which is cut down by the
-// same rule when it is long. With random logits some 1.1 k values of the first tile
-// and fewer of each later one reach it. A list that would overflow (rising logits) is
-// taken back to the tile's start and the bound is raised by the tile's own values:
-// then at most k threads' values pass.
+// the part's k largest. A tile of 4,096 values is in registers while the next is loaded. What
+// reaches the bound goes to a list in shared memory; the bound is taken from the first tile,
+// and from the list whenever that is long, which cuts it down to about 1.2 k. A list
+// that would overflow (rising logits) is taken back to the tile's start and the bound
+// is raised by the tile's own values: then only few threads' values pass.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
-  constexpr int kN = Vec<T>::n, kX = kVectors * kN;
-  constexpr int kRoom = kX == 32 ? 3072 : 2048;
-  // what a cut leaves (k threads' entries), a tile's values over its own bound (k
-  // threads' values) and the row's ends fit together
-  static_assert(kMaxK * (kRoom / kThreads) + kMaxK * kX + 2 * kN <= kRoom && kRoom % kThreads == 0, "list too short");
-  static_assert(kKeep + kMaxK * kX + 2 * kN <= kRoom, "list too short");
-  __shared__ uint64_t s_list[kRoom];
-  __shared__ __align__(16) uint64_t s_keys[kThreads];
+__global__ void __launch_bounds__(kThreads, 4) rows_kernel(RowArgs<T> a) {
+  constexpr int kN = Vec<T>::n, kVectors = kX / kN;
+  // what is kept, a tile's values over its own bound (4 k threads' for k <= 16, 2 k
+  // threads' above) and the row's ends fit together
+  static_assert(kThreads + 2 * kMaxK * kX + 2 * kN <= kRoom && 4 * 16 <= 2 * kMaxK && kRoom % kThreads == 0, "list too short");
+  __shared__ __align__(16) uint64_t s_list[kRoom];
+  __shared__ __align__(16) uint64_t s_keys[kThreads / 2];
   __shared__ uint64_t s_kth;
-  __shared__ int s_n;
+  __shared__ int s_added[3], s_left;
   __shared__ Part s_part[kThreads / 32];
   pdl_begin();
   const int32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
@@ -120,15 +143,18 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
   const int32_t per = (vectors + a.parts - 1) / a.parts;
   const int32_t v_begin = min(vectors, part * per), v_end = min(vectors, v_begin + per);
   const int k = a.k;
+  const int keep = k <= 32 ? kThreads / 2 : kThreads;  // a longer list is cut
 
   float ref = -INFINITY, sum = 0.0f;
   uint64_t bound = 1;
-  float bound_value = -INFINITY;
+  float bound_value = -FLT_MAX;  // (-inf is no candidate)
   int n = 0;  // entries of the list, as every thread knows it
-  if (threadIdx.x == 0) s_n = 0;
+  if (threadIdx.x < 3) s_added[threadIdx.x] = 0;
   __syncthreads();
 
-  const auto cut = [&]() {  // the list down to what reaches its own bound
+  // The list down to what reaches its own bound: the entries of 4 k or 2 k threads, so
+  // from n to n / 2 + keep / 2 at most.
+  const auto cut = [&]() {
     uint64_t mine[kRoom / kThreads];
     uint64_t best = 0;
 #pragma unroll
@@ -137,32 +163,40 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
       mine[i] = at < n ? s_list[at] : 0;
       best = max(best, mine[i]);
     }
-    bound = max(bound, kth_of_block(best, k, s_keys, &s_kth));
-    if (threadIdx.x == 0) s_n = 0;
+    bound = max(bound, bound_of_block(best, k, s_keys, &s_kth));
+    if (threadIdx.x == 0) s_left = 0;
     __syncthreads();
+    int stay = 0;
 #pragma unroll
-    for (int i = 0; i < kRoom / kThreads; ++i)
-      if (mine[i] >= bound) s_list[atomicAdd(&s_n, 1)] = mine[i];
+    for (int i = 0; i < kRoom / kThreads; ++i) stay += mine[i] >= bound;
+    if (stay) {
+      int at = atomicAdd(&s_left, stay);
+#pragma unroll
+      for (int i = 0; i < kRoom / kThreads; ++i)
+        if (mine[i] >= bound) s_list[at++] = mine[i];
+    }
     __syncthreads();
-    n = s_n;
-    bound_value = bound > 1 ? key_value(bound) : -INFINITY;
+    n = s_left;
+    bound_value = bound > 1 ? key_value(bound) : -FLT_MAX;
   };
 
-  // Tiles of the vectors; the first also holds the row's ends, as a last vector of
-  // thread 0 (before) and 1 (behind).
-  bool first = true;
-  for (int32_t v0 = v_begin; first || v0 < v_end; v0 += kThreads * kVectors) {
-    float x[kX];
+  uint4 raw[kVectors];
+  const auto fetch = [&](int32_t v0) {
 #pragma unroll
     for (int j = 0; j < kVectors; ++j) {
       const int32_t v = v0 + j * kThreads + (int32_t)threadIdx.x;
-      if (v < v_end) {
-        Vec<T>::load(x0 + lead + (int64_t)v * kN, x + j * kN);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[j * kN + i] = -INFINITY;
-      }
+      raw[j] = v < v_end ? __ldcs(reinterpret_cast<const uint4*>(x0 + lead) + v)
+                         : make_uint4(Vec<T>::none, Vec<T>::none, Vec<T>::none, Vec<T>::none);
     }
+  };
+  fetch(v_begin);
+  bool first = true;
+  int turn = 0;  // the tile's counter of three
+  for (int32_t v0 = v_begin; v0 < v_end; v0 += kThreads * kVectors) {
+    float x[kX];
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j) Vec<T>::unpack(raw[j], x + j * kN);
+    fetch(v0 + kThreads * kVectors);
     const auto place_of = [&](int i) {
       return (uint32_t)(lead + (v0 + (i / kN) * kThreads + (int32_t)threadIdx.x) * kN + i % kN);
     };
@@ -175,13 +209,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
     }
     // (x - ref first: exact where it counts, and 0 for a row of the type's lowest
     // value, whose product with log2 e is infinite; with ref +inf the sum is NaN)
-    const float from = ref > -INFINITY ? ref : 0.0f;
+    const float from = ref > -INFINITY ? -ref : 0.0f;
     float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kX; ++i) {
-      float e;
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((x[i] - from) * kLog2e));
-      add[i % 4] += e;
+    for (int i = 0; i < kX; i += 2) {
+      float u = x[i], v = x[i + 1];
+      add2(u, v, from, from);
+      mul2(u, v, kLog2e);
+      add2(add[i % 4], add[i % 4 + 1], ex2(u), ex2(v));
     }
     sum += (add[0] + add[1]) + (add[2] + add[3]);
 
@@ -189,10 +224,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
       if (!(top >= bound_value)) return;
 #pragma unroll
       for (int i = 0; i < kX; ++i) {
-        if (x[i] >= bound_value && x[i] > -INFINITY) {
+        if (x[i] >= bound_value) {
           const uint64_t key = make_key(x[i], place_of(i));
           if (key >= bound) {
-            const int at = atomicAdd(&s_n, 1);
+            const int at = n + atomicAdd(&s_added[turn], 1);
             if (at < kRoom) s_list[at] = key;
           }
         }
@@ -200,23 +235,29 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
     };
     if (!first) push();
     __syncthreads();
-    const int reached = s_n;
-    if (first || reached > kRoom) {
-      uint64_t best = 0;
+    int added = s_added[turn];
+    // the tile's before this one: everyone has read it, and it is added to again behind
+    // the next barrier. So a tile has one barrier, and the list is not read before it.
+    if (threadIdx.x == 0) s_added[turn == 0 ? 2 : turn - 1] = 0;
+    if (first || n + added > kRoom) {
+      int at = 0;
 #pragma unroll
-      for (int i = kX - 1; i >= 0; --i)
-        if (x[i] > -INFINITY) best = max(best, make_key(x[i], place_of(i)));
-      bound = max(bound, kth_of_block(best, k, s_keys, &s_kth));
-      bound_value = bound > 1 ? key_value(bound) : -INFINITY;
-      if (threadIdx.x == 0) s_n = n;
+      for (int i = kX - 1; i > 0; --i)
+        if (x[i] == top) at = i;
+      if (x[0] == top) at = 0;
+      const uint64_t best = top > -INFINITY ? make_key(top, place_of(at)) : 0;
+      bound = max(bound, bound_of_block(best, k, s_keys, &s_kth));
+      bound_value = bound > 1 ? key_value(bound) : -FLT_MAX;
+      if (threadIdx.x == 0) s_added[turn] = 0;
       __syncthreads();
       push();
       __syncthreads();
+      added = s_added[turn];
     }
-    n = s_n;
-    if (n > kKeep) cut();
-    __syncthreads();  // everyone knows the count before the next tile adds to it
+    n += added;
+    while (n > keep) cut();
     first = false;
+    turn = turn == 2 ? 0 : turn + 1;
   }
 
   // the row's ends: fewer than 2 kN values, one to a thread
@@ -234,19 +275,25 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
       }
       sum += exp2f((v - (ref > -INFINITY ? ref : 0.0f)) * kLog2e);
       const uint64_t key = make_key(v, (uint32_t)at);
-      if (key >= bound) s_list[atomicAdd(&s_n, 1)] = key;
+      if (key >= bound) s_list[n + atomicAdd(&s_added[turn], 1)] = key;
     }
     __syncthreads();
-    n = s_n;
+    n += s_added[turn];
   }
-  if (n > kThreads) cut();
+  while (n > keep) cut();
+  if (threadIdx.x == 0) s_list[n] = 0;  // (read in pairs; n <= keep)
+  __syncthreads();
 
   // the k largest, each to its rank
   uint64_t* list = a.lists + (int64_t)blockIdx.x * k;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t key = s_list[i];
     int above = 0;
-    for (int j = 0; j < n; ++j) above += s_list[j] > key;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(s_list + j);
+      above += (two.x > key) + (two.y > key);
+    }
     if (above < k) list[above] = key;
   }
   for (int i = n + threadIdx.x; i < k; i += kThreads) list[i] = 0;
@@ -273,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs<T> a) {
 // ---- joining ---------------------------------------------------------------------
 
 struct JoinArgs {
-  int32_t W, V, k, parts;
+  int32_t W, k, parts, k_shift, row_shift;
   const Part* part;
   const uint64_t* lists;
   const float* scores;
@@ -283,9 +330,10 @@ struct JoinArgs {
 };
 
 struct Best {
-  uint64_t score;  // order-preserving bits of the double
-  uint64_t place;  // ~(w * V + v)
+  uint64_t score;  // order-preserving bits of the double; 0: none
+  uint64_t place;  // ~(w << 32 | token)
 };
+__device__ __forceinline__ bool above(uint64_t a, uint64_t b) { return a > b; }
 __device__ __forceinline__ bool above(const Best& a, const Best& b) {
   return a.score > b.score || (a.score == b.score && a.place > b.place);
 }
@@ -297,89 +345,138 @@ __device__ __forceinline__ double order_value(uint64_t b) {
   return __longlong_as_double((long long)(b >> 63 ? b & 0x7FFFFFFFFFFFFFFFull : ~b));
 }
 
-// One CTA to a sequence, a thread to a list. The rows' sums give lse; scores are
-// held in 64 bits, so that their order is that of the formula to about 2^-23 (what the
-// sums carry): in 32 bits x - lse would be rounded to 2^-20 for logits about 16. The
-// k-th largest head of the lists bounds the k-th largest from below; what reaches it
-// (at most k lists' entries) is ranked.
-__global__ void __launch_bounds__(kMaxLists) join_kernel(JoinArgs a) {
-  pdl_wait();
-  extern __shared__ Best s_best[];  // [k * k] behind the heads
-  __shared__ Best s_head[kMaxLists];
-  __shared__ double s_lse[CSA2_MAX_BEAMS];  // NaN: the row takes no part
-  __shared__ Best s_kth;
-  __shared__ int s_n;
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int lists = a.W * a.parts;
-  const int64_t row0 = (int64_t)b * a.W;
-  if (tid == 0) {
-    s_kth = {0, 0};
-    s_n = 0;
+// Joins `lists` lists (each of 2^shift falling entries, one after another, all entries
+// different) in fours or pairs until `left` are left. An entry's rank is its place in its
+// own list and, by bisection, those of the others: one thread an entry, the bisections
+// side by side. x holds the lists and y half as many; returns where the last ones are.
+template <int kWays, typename E>
+__device__ __forceinline__ void join_round(const E* x, E* y, int lists, int shift) {
+  const int size = 1 << shift;
+  for (int i = threadIdx.x; i < lists << shift; i += kJoinThreads) {
+    const E e = x[i];
+    const int l = i >> shift, l0 = l & ~(kWays - 1);
+    int pos[kWays - 1] = {};
+    const E* other[kWays - 1];
+#pragma unroll
+    for (int o = 0; o < kWays - 1; ++o) other[o] = x + ((l0 + ((l + 1 + o) & (kWays - 1))) << shift);
+    for (int s = size / 2; s; s /= 2) {
+#pragma unroll
+      for (int o = 0; o < kWays - 1; ++o)
+        if (above(other[o][pos[o] + s - 1], e)) pos[o] += s;
+    }
+    int rank = i & (size - 1);
+#pragma unroll
+    for (int o = 0; o < kWays - 1; ++o) rank += pos[o] + (above(other[o][pos[o]], e) ? 1 : 0);
+    if (rank < size) y[((l / kWays) << shift) + rank] = e;
   }
-  for (int w = tid; w < a.W; w += blockDim.x) {
+  __syncthreads();
+}
+template <typename E>
+__device__ __forceinline__ const E* join_lists(E* x, E* y, int lists, int left, int shift) {
+  while (lists > left) {
+    const bool four = lists >= 4 * left;
+    if (four)
+      join_round<4>(x, y, lists, shift);
+    else
+      join_round<2>(x, y, lists, shift);
+    lists /= four ? 4 : 2;
+    E* t = x;
+    x = y;
+    y = t;
+  }
+  return x;
+}
+
+// Powers of two: a list's entries, a sequence's rows.
+__host__ __device__ constexpr int power_shift(int n) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return s;
+}
+__host__ __device__ constexpr int join_bytes(int W, int parts, int k) {
+  const int k2 = 1 << power_shift(k), rows2 = 1 << power_shift(W);
+  return 3 * W * parts * k2 / 2 * (int)sizeof(uint64_t) + 3 * rows2 * k2 / 2 * (int)sizeof(Best) + 64;
+}
+// (the parts' entries are at most kMaxEntries, or the rows' where each has one part)
+constexpr int kMaxJoinBytes = 3 * kMaxEntries / 2 * (int)sizeof(uint64_t) + 3 * CSA2_MAX_BEAMS * kMaxK / 2 * (int)sizeof(Best) + 64;
+static_assert(CSA2_MAX_BEAMS * kMaxK <= kMaxEntries && kMaxJoinBytes <= 226 * 1024, "lists too long");
+
+// One CTA to a sequence: each row's lists are joined by value, the rows' lists by
+// score. Scores are held in 64 bits, so that their order is that of the formula to
+// what the sums carry (about 2^-22): in 32 bits x - lse would be rounded to 2^-20 for
+// logits about 16. The time does not depend on the values.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a) {
+  pdl_wait();
+  extern __shared__ Best s_best[];  // the rows' lists and half as many, then the parts'
+  __shared__ double s_lse[CSA2_MAX_BEAMS];  // NaN: the row takes no part
+  __shared__ double s_score[CSA2_MAX_BEAMS];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int k = a.k;
+  const int64_t row0 = (int64_t)b * a.W;
+  const int shift = a.k_shift, mask = (1 << shift) - 1;
+  const int rows2 = 1 << a.row_shift;
+  Best* x = s_best;
+  Best* y = x + (rows2 << shift);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(y + (rows2 << shift) / 2 + 1);
+  const int entries = a.W * a.parts << shift;
+  const uint64_t* from = a.lists + row0 * a.parts * k;
+  for (int i = tid; i < entries; i += kJoinThreads) {
+    // (what is no candidate is below all that are, and different from the rest)
+    const uint64_t key = (i & mask) < k ? from[(i >> shift) * k + (i & mask)] : 0;
+    keys[i] = key ? key : (uint32_t)~i;
+  }
+  for (int w = tid >> 5; w < a.W; w += kJoinThreads / 32) {  // a warp to a row
     const Part* p = a.part + (row0 + w) * a.parts;
     float ref = -INFINITY;
-    for (int c = 0; c < a.parts; ++c) ref = fmaxf(ref, p[c].ref);
+    for (int c = lane; c < a.parts; c += 32) ref = fmaxf(ref, p[c].ref);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     float sum = 0.0f;
-    for (int c = 0; c < a.parts; ++c)
-      sum += p[c].ref == -INFINITY ? p[c].sum : p[c].sum * exp2f((p[c].ref - ref) * kLog2e);
-    double lse = -INFINITY;
-    if (!(sum <= 3.0e38f) || !(ref < INFINITY)) {
-      record_error(&g_beam_error, CSA2_ERR_DEVICE);  // a NaN or +inf among the logits
-      lse = NAN;
-    } else if (sum > 0.0f) {
-      lse = (double)ref + log((double)sum);
+    for (int c = lane; c < a.parts; c += 32) {
+      const Part v = p[c];
+      sum += v.ref == -INFINITY ? v.sum : v.sum * exp2f((v.ref - ref) * kLog2e);
     }
-    if (a.lse) a.lse[row0 + w] = (float)lse;
-    const float s = a.scores ? a.scores[row0 + w] : 0.0f;
-    s_lse[w] = fabsf(s) < INFINITY && sum > 0.0f ? lse : (double)NAN;
-  }
-  __syncthreads();
-  const uint64_t* list = a.lists + (row0 * a.parts + tid) * a.k;
-  const int w = tid < lists ? tid / a.parts : 0;
-  const double lse = s_lse[w], score = a.scores ? (double)a.scores[row0 + w] : 0.0;
-  const auto best_of = [&](uint64_t key) -> Best {
-    if (key == 0 || isnan(lse)) return {0, 0};
-    // (in this order: the lowest value of fp32 less itself leaves the score)
-    return {order(score + ((double)key_value(key) - lse)), ~((uint64_t)w * (uint64_t)a.V + key_place(key))};
-  };
-  Best head{0, 0};
-  if (tid < lists) head = best_of(list[0]);
-  s_head[tid] = head;
-  __syncthreads();
-  if (head.place) {
-    int n = 0;
-    for (int i = 0; i < lists; ++i) n += above(s_head[i], head);
-    if (n == a.k - 1) s_kth = head;
-  }
-  __syncthreads();
-  const Best kth = s_kth;
-  if (head.place && !above(kth, head)) {
-    for (int i = 0; i < a.k; ++i) {
-      const Best c = i == 0 ? head : best_of(list[i]);
-      if (!c.place || above(kth, c)) break;
-      s_best[atomicAdd(&s_n, 1)] = c;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      double lse = -INFINITY;
+      if (!(sum <= 3.0e38f) || !(ref < INFINITY)) {
+        record_error(&g_beam_error, CSA2_ERR_DEVICE);  // a NaN or +inf among the logits
+        lse = NAN;
+      } else if (sum > 0.0f) {
+        // the sum's exponent apart: the logarithm of a value in [1, 2) is off by 2^-24,
+        // and 64-bit operations are slow here
+        const uint32_t bits = __float_as_uint(sum);
+        const float m = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+        lse = (double)ref + ((double)((int)(bits >> 23) - 127) * 0.69314718055994531 + (double)logf(m));
+      }
+      if (a.lse) a.lse[row0 + w] = (float)lse;
+      const float s = a.scores ? a.scores[row0 + w] : 0.0f;
+      s_lse[w] = fabsf(s) < INFINITY && sum > 0.0f ? lse : (double)NAN;
+      s_score[w] = s;
     }
   }
   __syncthreads();
-  const int n = s_n;
-  for (int i = tid; i < n; i += blockDim.x) {
-    const Best c = s_best[i];
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += above(s_best[j], c);
-    if (r < a.k) {
-      const uint64_t at = ~c.place;
-      const int64_t o = (int64_t)b * a.k + r;
-      a.out_scores[o] = (float)order_value(c.score);
-      a.out_parents[o] = (int32_t)(row0 + (int64_t)(at / (uint64_t)a.V));
-      a.out_tokens[o] = (int32_t)(at % (uint64_t)a.V);
-    }
+  // (the number of parts is a power of two: a row's lists are joined with one another)
+  const uint64_t* rows = join_lists(keys, keys + entries, a.W * a.parts, a.W, shift);
+  for (int i = tid; i < rows2 << shift; i += kJoinThreads) {
+    const int w = i >> shift;
+    const uint64_t key = w < a.W ? rows[i] : 0;
+    Best c{0, (uint64_t)~i};
+    // (x - lse first: the lowest value of fp32 less itself leaves the score)
+    if (key >> 32 && !isnan(s_lse[w]))
+      c = {order(s_score[w] + ((double)key_value(key) - s_lse[w])), ~((uint64_t)w << 32 | key_place(key))};
+    x[i] = c;
   }
-  for (int i = n + tid; i < a.k; i += blockDim.x) {
-    const int64_t o = (int64_t)b * a.k + i;
-    a.out_scores[o] = -INFINITY;
-    a.out_parents[o] = -1;
-    a.out_tokens[o] = -1;
+  __syncthreads();
+  const Best* best = join_lists(x, y, rows2, 1, shift);
+  for (int i = tid; i < k; i += kJoinThreads) {
+    const Best c = best[i];
+    const int64_t o = (int64_t)b * k + i;
+    const uint64_t at = ~c.place;
+    a.out_scores[o] = c.score ? (float)order_value(c.score) : -INFINITY;
+    a.out_parents[o] = c.score ? (int32_t)(row0 + (int64_t)(at >> 32)) : -1;
+    a.out_tokens[o] = c.score ? (int32_t)at : -1;
   }
 }
 
@@ -512,20 +609,20 @@ static int check_beam(int32_t B, int32_t W, int32_t V, int32_t k) {
   return CSA2_OK;
 }
 
-// Parts of a row: about 4 CTAs an SM in all (152 SMs: the size of a workspace does
-// not depend on the device), parts of 2,048 values at least.
-static int beam_parts(int32_t B, int32_t W, int32_t V) {
+// Parts of a row, a power of two: at most 608 CTAs in all (four to each of 152 SMs: the
+// size of a workspace does not depend on the device) unless there are more rows, parts
+// of 2,048 values at least.
+static int beam_parts(int32_t B, int32_t W, int32_t V, int32_t k) {
   const int64_t rows = (int64_t)B * W;
-  int64_t parts = (608 + rows - 1) / rows;
-  const int64_t most = V / 2048;
-  if (parts > most) parts = most;
-  if (parts > beam::kMaxLists / W) parts = beam::kMaxLists / W;
-  return parts < 1 ? 1 : (int)parts;
+  const int64_t entries = (int64_t)W << beam::power_shift(k);
+  int64_t parts = 1;
+  while (2 * parts * rows <= 304 && 2 * parts * 2048 <= V && 2 * parts * entries <= beam::kMaxEntries) parts *= 2;
+  return (int)parts;
 }
 
 extern "C" size_t csa2_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t k) {
   if (check_beam(B, W, V, k) != CSA2_OK || B == 0 || W == 0) return 0;
-  const size_t lists = (size_t)B * W * beam_parts(B, W, V);
+  const size_t lists = (size_t)B * W * beam_parts(B, W, V, k);
   return al256(lists * sizeof(beam::Part)) + al256(lists * k * sizeof(uint64_t));
 }
 
@@ -552,7 +649,7 @@ extern "C" int csa2_beam_select(const void* logits, int32_t logits_f32, int32_t 
     return CSA2_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < csa2_beam_select_workspace_size(B, W, V, k) || !csa2_aligned(workspace, 256))
     return CSA2_ERR_WORKSPACE;
-  const int parts = beam_parts(B, W, V);
+  const int parts = beam_parts(B, W, V, k);
   const int64_t rows = (int64_t)B * W;
   beam::Part* part = (beam::Part*)workspace;
   uint64_t* lists = (uint64_t*)((char*)workspace + al256((size_t)rows * parts * sizeof(beam::Part)));
@@ -561,10 +658,10 @@ extern "C" int csa2_beam_select(const void* logits, int32_t logits_f32, int32_t 
                   : launch_rows<uint16_t>(logits, ld, V, k, rows, parts, part, lists, s);
   if (rc) return rc;
   static Csa2PerDeviceOnce once;
-  if (csa2_smem_optin((const void*)beam::join_kernel, beam::kMaxK * beam::kMaxK * (int)sizeof(beam::Best), once) != CSA2_OK)
-    return CSA2_ERR_CUDA;
-  beam::JoinArgs j{W, V, k, parts, part, lists, scores, out_scores, out_parents, out_tokens, lse};
-  CSA2_LAUNCH_PDL(beam::join_kernel, dim3((unsigned)B), dim3(beam::kMaxLists), (size_t)k * k * sizeof(beam::Best), s, j);
+  if (csa2_smem_optin((const void*)beam::join_kernel, beam::kMaxJoinBytes, once) != CSA2_OK) return CSA2_ERR_CUDA;
+  beam::JoinArgs j{W, k, parts, beam::power_shift(k), beam::power_shift(W), part, lists, scores, out_scores, out_parents, out_tokens, lse};
+  CSA2_LAUNCH_PDL(beam::join_kernel, dim3((unsigned)B), dim3(beam::kJoinThreads),
+                  (size_t)beam::join_bytes(W, parts, k), s, j);
   return CSA2_OK;
 }
 

@@ -798,7 +798,7 @@ int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens,
 /* Beam search                                                               */
 /* ======================================================================== */
 
-#define CSA2_MAX_BEAMS 256
+#define CSA2_MAX_BEAMS 64
 #define CSA2_MAX_BEAM_K 64
 
 /** Bytes of workspace csa2_beam_select needs. */

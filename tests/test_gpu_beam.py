@@ -124,7 +124,7 @@ def make(kind, g, B, W, V, dtype):
 
 KINDS = ["normal", "equal", "few", "rising", "falling", "masked", "lowest", "peaked", "wide"]
 SIZES = [(1, 1, 1, 1), (2, 3, 2, 4), (1, 4, 7, 8), (3, 2, 33, 5), (2, 8, 1000, 16), (1, 4, 5003, 64), (40, 16, 2051, 32),
-         (1, 1, 40009, 64), (2, 256, 515, 64), (1, 2, 131075, 7)]
+         (1, 1, 40009, 64), (2, 64, 515, 64), (1, 2, 131075, 7)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

@@ -84,7 +84,7 @@ BEAM_GOOD = dict(logits=P, f32=1, B=2, W=3, V=100, ld=100, scores=P, k=4, out=P,
     (dict(ws=P + 64, ws_bytes=1 << 40), WORKSPACE), (dict(B=0), OK), (dict(B=0, logits=None, out=None), OK),
     (dict(B=-1), ARG), (dict(W=-1), ARG), (dict(W=0), ARG), (dict(V=-1), ARG), (dict(V=0), ARG), (dict(ld=99), ARG), (dict(k=-1), ARG),
     (dict(f32=2), ARG), (dict(logits=None), ARG), (dict(out=None), ARG), (dict(parents=None), ARG), (dict(tokens=None), ARG),
-    (dict(k=0), SHAPE), (dict(k=65), SHAPE), (dict(W=257), SHAPE), (dict(B=1 << 22, W=2), SHAPE),
+    (dict(k=0), SHAPE), (dict(k=65), SHAPE), (dict(W=65), SHAPE), (dict(B=1 << 22, W=2), SHAPE),
     (dict(logits=P + 2), ALIGN), (dict(logits=P + 2, f32=0), WORKSPACE), (dict(logits=P + 1, f32=0), ALIGN), (dict(scores=P + 2), ALIGN),
     (dict(out=P + 2), ALIGN), (dict(parents=P + 2), ALIGN), (dict(tokens=P + 2), ALIGN), (dict(lse=P + 2), ALIGN)])
 def test_beam(lib, change, status):
