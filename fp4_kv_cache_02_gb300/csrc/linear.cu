@@ -18,6 +18,8 @@
 // of a token are eight columns of the second operand, so the products cost tensor
 // time that a product bound by its weights' bytes has to spare, and no instruction
 // of the CUDA cores per weight.
+#include <stdlib.h>
+
 #include "tc_common.cuh"
 
 namespace csa2 {
@@ -31,6 +33,9 @@ constexpr int kChunk = 256;                 // inputs to a block of weights: 128
 constexpr int kRows = 128;                  // outputs to a block
 constexpr int kDataBytes = kRows * kChunk / 2;
 constexpr int kTileTokens = 32;             // tokens to a tile: 256 columns
+constexpr int kFewTokens = 4;               // tokens whose terms the product's own warps make
+constexpr int kMaxSplit = 8;                // CTAs that split the inputs of such a product
+constexpr int kStreamCtas = 152;            // of a product of more tokens: one to an SM
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 192;
 constexpr int kProducerWarp = 4;
@@ -100,76 +105,49 @@ __device__ __forceinline__ float2 e2m1x2_to_f32x2(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-struct TermArgs {
-  const uint16_t* x;
-  int32_t T, n_in, chunks, n, slices;
-  uint8_t* terms;
-  float* factor;
-};
+// The largest magnitude's bf16 bits of eight channels.
+__device__ __forceinline__ uint32_t top_bits(uint4 v) {
+  const uint32_t m2 = max_halves(max_halves(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                 max_halves(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return max(m2 & 0xFFFFu, m2 >> 16);
+}
 
-// One CTA takes 2,048 channels of a token, eight to a thread. With E4M3 scales the
-// terms' scales are powers of two relative to the row's own (2^-9 .. 2^8 relative to
-// 2^-8 of the row's largest block scale; a block below that takes the smallest), and
-// term j counts 2^(1-3j) of term 0: both are put back behind the product, the first as
-// the token's factor. With E8M0 scales they stand in the scale bytes themselves. A
-// row with an infinity or a NaN has the factor NaN.
+// A token's factor: with E4M3 scales the power of two that its terms' scales are relative
+// to, 2^-8 of the largest block scale; NaN for a row that holds an infinity or a NaN.
 template <bool kE4M3>
-__global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
-  pdl_begin();
-  __shared__ uint32_t s_max[kTermThreads / 32];
-  const int32_t t = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
-  const uint16_t* row = a.x + (int64_t)t * a.n_in;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t k = ((int64_t)slice * kTermThreads + threadIdx.x) * 8;
+__device__ __forceinline__ int base_exp(uint32_t top) { return kE4M3 ? scale_exp(top) - 8 : 0; }
+template <bool kE4M3>
+__device__ __forceinline__ float factor_of(uint32_t top) {
+  return top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                        : __uint_as_float((uint32_t)(base_exp<kE4M3>(top) + 127) << 23);
+}
 
-  uint32_t top2 = 0;
-  for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kTermThreads * 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + i);
-    top2 = max_halves(top2, max_halves(max_halves(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       max_halves(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-  }
-  uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_max[warp] = top;
-  __syncthreads();
-  top = s_max[0];
-#pragma unroll
-  for (int i = 1; i < kTermThreads / 32; ++i) top = max(top, s_max[i]);
-  const int row_exp = scale_exp(top) - 8;
-  if (slice == 0 && threadIdx.x == 0)
-    a.factor[t] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                  : kE4M3 ? __uint_as_float((uint32_t)(row_exp + 127) << 23) : 1.0f;
-
-  const int32_t c = (int32_t)(k / kChunk);
-  if (c >= a.chunks) return;  // (whole warps: a warp has one chunk)
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (k < a.n_in) v = *reinterpret_cast<const uint4*>(row + k);
-  uint32_t m2 = max_halves(max_halves(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                           max_halves(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-  uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+// One warp: the eight terms of a token's chunk of 256 channels, eight channels v to a
+// lane, into rows 8 tl .. 8 tl + 7 of the second operand's block. With E4M3 scales the
+// terms' scales are powers of two, 2^-9 .. 2^8 relative to `base` (a block below that
+// takes the smallest), and term j counts 2^(1-3j) of term 0: both are put back behind the
+// product. With E8M0 scales they stand in the scale bytes.
+template <bool kE4M3>
+__device__ __forceinline__ void put_terms(uint4 v, int base, int tl, uint8_t* data, uint8_t* scales, int nh, int lane) {
+  uint32_t m = top_bits(v);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   if (!kE4M3) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   int e = scale_exp(m);
-  if (kE4M3) e = max(e, row_exp - 9);
-  // (a row that is not finite: any terms do)
-  e = min(e, 126);
+  if (kE4M3) e = max(e, base - 9);
+  e = min(e, 126);  // (of a row that is not finite any terms do)
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
   float r[8];
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    r[2 * i] = bf16_bits_to_f32((uint16_t)(w[i] & 0xFFFFu)) * inv;
-    r[2 * i + 1] = bf16_bits_to_f32((uint16_t)(w[i] >> 16)) * inv;
+    r[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    r[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
   }
-  const int tl = t % kTileTokens;
-  uint8_t* block = a.terms + ((int64_t)(t / kTileTokens) * a.chunks + c) * terms_bytes(kE4M3, a.n);
-  uint8_t* scales = block + a.n * (kChunk / 2);
-  const int at = lane;  // 8 channels = 4 bytes of the row's 128
   constexpr int kLanesPer = kE4M3 ? 2 : 4;
   const int s_at = lane / kLanesPer;  // scale of the row: group s_at / 4, byte s_at % 4
-  uint32_t s_code;
+  uint32_t s_code = 0;
   if (kE4M3) {
-    const int rel = e - row_exp;  // -9 .. 8
+    const int rel = e - base;  // -9 .. 8
     s_code = rel >= -6 ? (uint32_t)(rel + 7) << 3 : 1u << (rel + 9);
   }
 #pragma unroll
@@ -183,24 +161,66 @@ __global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
       r[2 * i + 1] = (r[2 * i + 1] - q.y) * up;
     }
     const int n = tl * kTerms + j;
-    *reinterpret_cast<uint32_t*>(block + tc::sw128_offset(n, at / 4) + (at % 4) * 4) = codes;
+    *reinterpret_cast<uint32_t*>(data + tc::sw128_offset(n, lane / 4) + (lane % 4) * 4) = codes;
     if (!kE4M3) s_code = (uint32_t)(e + 127 - (j == 0 ? 0 : 3 * j - 1));
     if (lane % kLanesPer == 0)
-      scales[((s_at / 4) * column_groups(a.n) + n / 128) * group_bytes() + scale_place(n % 128) + s_at % 4] =
-          (uint8_t)s_code;
+      scales[((s_at / 4) * nh + n / 128) * group_bytes() + scale_place(n % 128) + s_at % 4] = (uint8_t)s_code;
   }
+}
+
+struct TermArgs {
+  const uint16_t* x;
+  int32_t T, n_in, chunks, n, slices;
+  uint8_t* terms;
+  float* factor;
+  int32_t* joined;
+};
+
+// The terms of all tokens, ahead of the product: one CTA takes 2,048 channels of a
+// token, eight to a thread.
+template <bool kE4M3>
+__global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
+  pdl_begin();
+  __shared__ uint32_t s_max[kTermThreads / 32];
+  if (blockIdx.x == 0 && threadIdx.x < kStreamCtas) a.joined[threadIdx.x] = 0;
+  const int32_t t = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
+  const uint16_t* row = a.x + (int64_t)t * a.n_in;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t top = 0;
+  for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kTermThreads * 8)
+    top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_max[warp] = top;
+  __syncthreads();
+  top = s_max[0];
+#pragma unroll
+  for (int i = 1; i < kTermThreads / 32; ++i) top = max(top, s_max[i]);
+  if (slice == 0 && threadIdx.x == 0) a.factor[t] = factor_of<kE4M3>(top);
+
+  const int64_t k = ((int64_t)slice * kTermThreads + threadIdx.x) * 8;
+  const int32_t c = (int32_t)(k / kChunk);
+  if (c >= a.chunks) return;  // (whole warps: a warp has one chunk)
+  const uint4 v = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0, 0, 0, 0);
+  uint8_t* block = a.terms + ((int64_t)(t / kTileTokens) * a.chunks + c) * terms_bytes(kE4M3, a.n);
+  put_terms<kE4M3>(v, base_exp<kE4M3>(top), t % kTileTokens, block, block + a.n * (kChunk / 2), column_groups(a.n), lane);
 }
 
 // ---- the product -----------------------------------------------------------------
 
+// Block (row tile, chunk) of the weights, (token tile, chunk) of the terms: number
+// tile * chunks + chunk.
 struct Params {
   const uint8_t* weights;
-  const uint8_t* terms;
+  const uint16_t* x;      // few_kernel
+  const uint8_t* terms;   // stream_kernel, as all of the following but the last line
   const float* factor;
+  int32_t* joined;        // parts that are there of the tile that CTA g is the first to have a part of
+  float* parts;           // [CTA][2][tokens of a tile][128]
   __nv_bfloat16* out_bf16;
   float* out_f32;
   float scale;
-  int32_t T, n_out, chunks, token_tiles, n, stages, cluster;
+  int32_t T, n_out, n_in, chunks, token_tiles, n, stages, split;
+  int64_t units;          // tiles x chunks
   uint32_t tmem_cols;
 };
 
@@ -218,40 +238,93 @@ __device__ __forceinline__ float ld_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void sync_four_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-constexpr int kHeadBytes = 256;  // barriers and words ahead of the ring's 1,024-byte boundary
+constexpr int kHeadBytes = 512;  // barriers and words ahead of the ring's 1,024-byte boundary
 
-// One CTA: 128 outputs x a tile of tokens x a range of chunks. A cluster's CTAs
-// share the chunks of one tile; each sums its range, and their sums are added in
-// rank order out of one another's shared memory.
-//   warp 4     producer: one bulk copy of a block of weights and one of the terms
-//              per stage; the first stages' weights before the terms are ready;
-//   warp 5     scales to tensor memory, four products of K = 64 a stage;
-//   warps 0-3  the tokens' eight columns summed, stored.
-template <bool kE4M3, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas) linear_kernel(Params p) {
+__device__ __forceinline__ uint8_t* ring_of(uint8_t* smem) {
+  const uint32_t raw = tc::smem_u32(smem);
+  return smem + (((raw + kHeadBytes + 1023u) & ~1023u) - raw);
+}
+
+// A stage's scales to its own columns of tensor memory (written again only when the
+// stage's barrier says that the products that read them are done), and its four products.
+// By a converged warp.
+template <bool kE4M3>
+__device__ __forceinline__ void stage_products(uint32_t one, uint32_t a_at, uint32_t b_at, int n, uint32_t acc, uint32_t sfa,
+                                               uint32_t idesc, bool add) {
+  constexpr int kG = groups(kE4M3);
+  const int nh = column_groups(n);
+  const uint32_t sfb = sfa + kG * 4;
+  for (int g = 0; g < kG; ++g)
+    tc::tmem_cp_32x128_x4_one(one, sfa + 4 * g,
+                              tc::smem_desc(a_at + kDataBytes + g * group_bytes(), 0, 128, tc::kSwizzleNone));
+  for (int g = 0; g < kG * nh; ++g)
+    tc::tmem_cp_32x128_x4_one(one, sfb + 4 * g,
+                              tc::smem_desc(b_at + n * (kChunk / 2) + g * group_bytes(), 0, 128, tc::kSwizzleNone));
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int g = kE4M3 ? m : m / 2;
+    const uint32_t id = kE4M3 ? 0u : (uint32_t)(m % 2) * 2;  // two products share a group's four bytes
+    tc::mma_fp4_one<kE4M3>(one, acc, tc::smem_desc(a_at + 32 * m, 0, 1024, tc::kSwizzle128B),
+                           tc::smem_desc(b_at + 32 * m, 0, 1024, tc::kSwizzle128B), idesc | id << 4 | id << 29, sfa + 4 * g,
+                           sfb + 4 * g * nh, add || m);
+  }
+}
+template <bool kE4M3>
+__device__ __forceinline__ uint32_t idesc_of(int n) {
+  return kE4M3 ? tc::idesc_nvf4(128, n) : tc::idesc_mxf4(128, n, 0, 0);
+}
+// Scale columns of a stage.
+__host__ __device__ constexpr int scale_cols(bool e4m3, int n) { return groups(e4m3) * 4 * (1 + column_groups(n)); }
+
+// A token's eight columns.
+template <bool kE4M3>
+__device__ __forceinline__ float sum_terms(const uint32_t* v) {
+  float y = __uint_as_float(v[7]);
+#pragma unroll
+  for (int j = 6; j >= 0; --j)
+    y = kE4M3 ? fmaf(y, j == 0 ? 0.25f : 0.125f, __uint_as_float(v[j])) : y + __uint_as_float(v[j]);
+  return y;
+}
+
+__device__ __forceinline__ void put_out(const Params& p, int64_t t, int64_t row, float y) {
+  if (row >= p.n_out) return;
+  y *= p.scale;
+  if (p.out_bf16) p.out_bf16[t * p.n_out + row] = __float2bfloat16_rn(y);
+  if (p.out_f32) p.out_f32[t * p.n_out + row] = y;
+}
+
+// ---- few tokens ------------------------------------------------------------------
+// One to four tokens in one launch: a CTA takes 128 outputs x a range of chunks and makes
+// its own terms (ahead of the product they would cost a launch and a trip through L2, 4 us
+// of 15 for 32,768 x 4,096 weights). The CTAs of a cluster split a row tile's chunks, and
+// their sums are added in rank order out of one another's shared memory.
+//   warp 4     producer: a bulk copy of a block of weights per stage, the first ones
+//              before x is waited for;
+//   warp 5     scales to tensor memory, products;
+//   warps 0-3  the terms, a (chunk, token) to a warp; then the columns summed, stored.
+template <bool kE4M3>
+__global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = tc::smem_u32(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  uint8_t* ring = smem_raw + (((raw + kHeadBytes + 1023u) & ~1023u) - raw);
+  uint32_t* s_top = s_tmem + 2;  // [warp][token]: the largest channel that the warp has seen
+  uint8_t* ring = ring_of(smem_raw);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)(blockIdx.x % (uint32_t)p.cluster);
-  const int64_t tile = blockIdx.x / (uint32_t)p.cluster;
-  const int32_t token_tile = (int32_t)(tile % p.token_tiles);
-  const int64_t row_tile = tile / p.token_tiles;
-  const int32_t c0 = (int32_t)((int64_t)p.chunks * rank / p.cluster);
-  const int32_t n_chunks = (int32_t)((int64_t)p.chunks * (rank + 1) / p.cluster) - c0;
-  const int blk_b = terms_bytes(kE4M3, p.n);
-  const int stage_bytes = block_bytes(kE4M3) + blk_b;
+  const int part = (int)(blockIdx.x % (uint32_t)p.split);
+  const int64_t row_tile = blockIdx.x / (uint32_t)p.split;
+  const int32_t c0 = (int32_t)((int64_t)p.chunks * part / p.split);
+  const int32_t n_chunks = (int32_t)((int64_t)p.chunks * (part + 1) / p.split) - c0;
+  const int stage_bytes = block_bytes(kE4M3) + terms_bytes(kE4M3, p.n);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&full[s], 1 + p.T);
       tc::mbar_init(&empty[s], 1);
     }
     tc::mbar_init(acc_full, 1);
@@ -266,24 +339,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) linear_kernel(Params p) {
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
-      const uint8_t* wsrc = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
-      const uint8_t* tsrc = p.terms + ((int64_t)token_tile * p.chunks + c0) * blk_b;
-      const int ahead = n_chunks < p.stages ? n_chunks : p.stages;
-      for (int i = 0; i < ahead; ++i) {
-        tc::mbar_arrive_expect_tx(&full[i], (uint32_t)stage_bytes);
-        tc::bulk_load(ring + i * stage_bytes, wsrc + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full[i]);
-      }
-      pdl_wait();
-      for (int i = 0; i < ahead; ++i)
-        tc::bulk_load(ring + i * stage_bytes + block_bytes(kE4M3), tsrc + (int64_t)i * blk_b, (uint32_t)blk_b, &full[i]);
-      int issued = ahead;
+      const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
+      int issued = 0;
       for (; issued < n_chunks; ++issued) {
         const int s = issued % p.stages;
         if (!tc::mbar_wait_bounded(&empty[s], ((uint32_t)(issued / p.stages) & 1u) ^ 1u, s_abort, &g_linear_error)) break;
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
-        tc::bulk_load(ring + s * stage_bytes, wsrc + (int64_t)issued * block_bytes(kE4M3), block_bytes(kE4M3), &full[s]);
-        tc::bulk_load(ring + s * stage_bytes + block_bytes(kE4M3), tsrc + (int64_t)issued * blk_b, (uint32_t)blk_b,
-                      &full[s]);
+        tc::mbar_arrive_expect_tx(&full[s], block_bytes(kE4M3));
+        tc::bulk_load(ring + s * stage_bytes, from + (int64_t)issued * block_bytes(kE4M3), block_bytes(kE4M3), &full[s]);
       }
       // copies land before the CTA's memory goes away
       for (int i = max(0, issued - p.stages); i < issued; ++i)
@@ -292,109 +354,321 @@ __global__ void __launch_bounds__(kThreads, kCtas) linear_kernel(Params p) {
     __syncwarp();
   } else if (warp == kMmaWarp) {
     const uint32_t one = tc::elect_one();
-    const uint32_t ring_at = tc::smem_u32(ring);
-    const int nh = column_groups(p.n);
-    constexpr int kG = groups(kE4M3);
-    const uint32_t sf_cols = (uint32_t)(kG * 4 * (1 + nh));  // scale columns of a stage
-    const uint32_t idesc = kE4M3 ? tc::idesc_nvf4(128, p.n) : tc::idesc_mxf4(128, p.n, 0, 0);
-    int done = 0;
-    for (; done < n_chunks; ++done) {
+    const uint32_t ring_at = tc::smem_u32(ring), idesc = idesc_of<kE4M3>(p.n);
+    for (int done = 0; done < n_chunks; ++done) {
       const int s = done % p.stages;
       const bool ok = tc::mbar_wait_bounded(&full[s], (uint32_t)(done / p.stages) & 1u, s_abort, &g_linear_error);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::tc_fence_after();
       const uint32_t a_at = ring_at + (uint32_t)(s * stage_bytes);
-      const uint32_t b_at = a_at + block_bytes(kE4M3);
-      // The stage's own scale columns: they are written again only when its barrier
-      // says that the products that read them are done.
-      const uint32_t sfa = tmem + (uint32_t)p.n + (uint32_t)s * sf_cols, sfb = sfa + kG * 4;
-      for (int g = 0; g < kG; ++g)
-        tc::tmem_cp_32x128_x4_one(one, sfa + 4 * g,
-                                  tc::smem_desc(a_at + kDataBytes + g * group_bytes(), 0, 128, tc::kSwizzleNone));
-      for (int g = 0; g < kG * nh; ++g)
-        tc::tmem_cp_32x128_x4_one(one, sfb + 4 * g,
-                                  tc::smem_desc(b_at + p.n * (kChunk / 2) + g * group_bytes(), 0, 128, tc::kSwizzleNone));
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int g = kE4M3 ? m : m / 2;
-        const uint32_t id = kE4M3 ? 0u : (uint32_t)(m % 2) * 2;  // two products share a group's four bytes
-        tc::mma_fp4_one<kE4M3>(one, tmem, tc::smem_desc(a_at + 32 * m, 0, 1024, tc::kSwizzle128B),
-                               tc::smem_desc(b_at + 32 * m, 0, 1024, tc::kSwizzle128B), idesc | id << 4 | id << 29,
-                               sfa + 4 * g, sfb + 4 * g * nh, (done | m) != 0);
-      }
+      stage_products<kE4M3>(one, a_at, a_at + block_bytes(kE4M3), p.n, tmem,
+                            tmem + (uint32_t)(p.n + s * scale_cols(kE4M3, p.n)), idesc, done != 0);
       tc::mma_commit_one(one, &empty[s]);
     }
     // whatever was issued ends before tensor memory is freed
     tc::mma_commit_one(one, acc_full);
     tc::mbar_wait_issued(acc_full, 0);
     __syncwarp();
+  } else {
+    pdl_wait();  // x; and the outputs may have readers before this call
+    const auto channels = [&](int c, int t) {
+      const int32_t k = (c0 + c) * kChunk + lane * 8;
+      return k < p.n_in ? *reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.n_in + k) : make_uint4(0, 0, 0, 0);
+    };
+    uint32_t top[kFewTokens] = {};
+    const auto share_tops = [&]() {
+#pragma unroll
+      for (int t = 0; t < kFewTokens; ++t) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, top[t]);
+        if (lane == 0) s_top[warp * kFewTokens + t] = m;
+      }
+      sync_four_warps();
+    };
+    if (kE4M3) {  // the scales' base: the largest of this CTA's channels
+      for (int c = warp; c < n_chunks; c += 4)
+#pragma unroll
+        for (int t = 0; t < kFewTokens; ++t)
+          if (t < p.T) top[t] = max(top[t], top_bits(channels(c, t)));
+      share_tops();
+    }
+    const int n_tasks = n_chunks * p.T;
+    for (int i = warp; i < n_tasks; i += 4) {
+      const int c = i / p.T, t = i % p.T, s = c % p.stages;
+      const uint4 v = channels(c, t);
+      const bool ok = tc::mbar_wait_bounded(&empty[s], ((uint32_t)(c / p.stages) & 1u) ^ 1u, s_abort, &g_linear_error);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      int base = 0;
+      if (kE4M3) {
+        base = base_exp<kE4M3>(max(max(s_top[t], s_top[kFewTokens + t]), max(s_top[2 * kFewTokens + t], s_top[3 * kFewTokens + t])));
+      } else {
+        const uint32_t m = top_bits(v);
+#pragma unroll
+        for (int j = 0; j < kFewTokens; ++j)
+          if (j == t) top[j] = max(top[j], m);
+      }
+      uint8_t* data = ring + s * stage_bytes + block_bytes(kE4M3);
+      put_terms<kE4M3>(v, base, t, data, data + p.n * (kChunk / 2), 1, lane);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&full[s]);
+    }
+    if (!kE4M3) share_tops();
   }
 
-  // ---- epilogue ----
-  const int32_t t0 = token_tile * kTileTokens;
-  const int nt = p.T - t0 < kTileTokens ? p.T - t0 : kTileTokens;
-  float* part = reinterpret_cast<float*>(ring);  // [nt][128], once the ring is done with
+  float* sums = reinterpret_cast<float*>(ring);  // [T][128], once the ring is done with
   if (warp < 4) {
     bool ok = tc::mbar_wait_bounded(acc_full, 0, s_abort, &g_linear_error);
     ok = __all_sync(0xffffffffu, ok) && !*s_abort;
     ok = __all_sync(0xffffffffu, ok);
-    pdl_wait();  // the factors; and the outputs may have readers before this call
     if (ok) {
       tc::tc_fence_after();
       const int row = warp * 32 + lane;
-      const int64_t out_row = row_tile * kRows + row;
-      for (int t = 0; t < nt; t += 2) {
-        uint32_t r[16];
-        tc::tmem_ld_32x32b_x16(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(t * kTerms), r);
-        tc::tmem_ld_wait();
+      uint32_t v[32];
+      // (columns past the accumulator hold scales: read, not used)
+      tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16), v);
+      tc::tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (t + h >= nt) break;
-          float y = __uint_as_float(r[8 * h + 7]);
-          if (kE4M3) {
-#pragma unroll
-            for (int j = 6; j >= 0; --j) y = fmaf(y, j == 0 ? 0.25f : 0.125f, __uint_as_float(r[8 * h + j]));
-          } else {
-#pragma unroll
-            for (int j = 6; j >= 0; --j) y += __uint_as_float(r[8 * h + j]);
-          }
-          y *= p.factor[t0 + t + h];
-          if (p.cluster > 1) {
-            part[(t + h) * kRows + row] = y;
-          } else if (out_row < p.n_out) {
-            y *= p.scale;
-            const int64_t at = (int64_t)(t0 + t + h) * p.n_out + out_row;
-            if (p.out_bf16) p.out_bf16[at] = __float2bfloat16_rn(y);
-            if (p.out_f32) p.out_f32[at] = y;
-          }
-        }
+      for (int t = 0; t < kFewTokens; ++t) {
+        if (t >= p.T) break;
+        const float y =
+            sum_terms<kE4M3>(v + 8 * t) *
+            factor_of<kE4M3>(max(max(s_top[t], s_top[kFewTokens + t]), max(s_top[2 * kFewTokens + t], s_top[3 * kFewTokens + t])));
+        if (p.split > 1)
+          sums[t * kRows + row] = y;
+        else
+          put_out(p, t, row_tile * kRows + row, y);
       }
       tc::tc_fence_before();
+    } else if (p.split > 1) {
+      for (int t = 0; t < p.T; ++t) sums[t * kRows + threadIdx.x] = __uint_as_float(0x7FC00000u);
     }
   }
   __syncthreads();
-  if (p.cluster > 1) {
+  if (p.split > 1) {
     cluster_sync();
-    bool ok = true;
-    for (int c = 0; c < p.cluster; ++c) ok = ok && __float_as_int(ld_peer(peer(tc::smem_u32((const void*)s_abort), c))) == 0;
-    const int per = nt * kRows / p.cluster;
-    for (int i = threadIdx.x; ok && i < per; i += kThreads) {
-      const int at = rank * per + i;
-      const int t = at / kRows, row = at % kRows;
-      const uint32_t here = tc::smem_u32(part + at);
-      float y = 0.0f;
-      for (int c = 0; c < p.cluster; ++c) y += ld_peer(peer(here, c));
-      const int64_t out_row = row_tile * kRows + row;
-      if (out_row < p.n_out) {
-        y *= p.scale;
-        const int64_t o = (int64_t)(t0 + t) * p.n_out + out_row;
-        if (p.out_bf16) p.out_bf16[o] = __float2bfloat16_rn(y);
-        if (p.out_f32) p.out_f32[o] = y;
-      }
+    const int per = p.T * kRows / p.split;  // (split is a power of two)
+    for (int i = threadIdx.x; i < per; i += kThreads) {
+      const int at = part * per + i;
+      const uint32_t here = tc::smem_u32(sums + at);
+      float v[kMaxSplit];
+#pragma unroll
+      for (int c = 0; c < kMaxSplit; ++c) v[c] = c < p.split ? ld_peer(peer(here, c)) : 0.0f;
+      float y = v[0];
+#pragma unroll
+      for (int c = 1; c < kMaxSplit; ++c) y += v[c];
+      put_out(p, at / kRows, row_tile * kRows + at % kRows, y);
     }
     cluster_sync();  // the peers have read this CTA's sums
   }
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, p.tmem_cols);
+}
+
+// ---- more tokens -----------------------------------------------------------------
+// Tiles of 128 outputs x up to 32 tokens. All tiles' chunks form one list (a row tile's
+// token tiles one after another, so that its weights are in L2 for them), cut into one
+// equal run to an SM. A run begins and ends inside tiles: their parts go through the
+// workspace, and the CTA that brings a tile's last part adds them, in the list's order
+// whoever that is. Nobody waits for another CTA.
+//   warp 8     producer: bulk copies of a block of weights and one of terms per stage,
+//              ahead across tiles;
+//   warp 9     scales to tensor memory, products; two accumulators up to 16 tokens;
+//   warps 0-7  the columns summed (a quarter of the rows, half of the tokens each), the
+//              accumulator given back, then stored or joined.
+constexpr int kSumWarps = 8;
+constexpr int kStreamThreads = 32 * (kSumWarps + 2);
+
+__device__ __forceinline__ void sync_sum_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <bool kE4M3>
+__global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
+  uint8_t* ring = ring_of(smem_raw);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t G = gridDim.x, g = blockIdx.x;
+  const int64_t u0 = p.units * g / G, u1 = p.units * (g + 1) / G;
+  const int64_t tile0 = u0 / p.chunks;
+  const int32_t chunk0 = (int32_t)(u0 - tile0 * p.chunks);
+  const int blk_b = terms_bytes(kE4M3, p.n);
+  const int stage_bytes = block_bytes(kE4M3) + blk_b;
+  const int accs = p.n <= 128 ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(&acc_full[a], 1);
+      tc::mbar_init(&acc_empty[a], kSumWarps);
+    }
+    *s_abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == kSumWarps + 1) tc::tmem_alloc(s_tmem, p.tmem_cols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == kSumWarps) {
+    if (lane == 0) {
+      struct Place {
+        int64_t row_tile;
+        int32_t token_tile, chunk;
+      };
+      const Place start{tile0 / p.token_tiles, (int32_t)(tile0 % p.token_tiles), chunk0};
+      const auto advance = [&](Place& at) {
+        if (++at.chunk < p.chunks) return;
+        at.chunk = 0;
+        if (++at.token_tile < p.token_tiles) return;
+        at.token_tile = 0;
+        ++at.row_tile;
+      };
+      const auto load_weights = [&](const Place& at, int s) {
+        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
+        tc::bulk_load(ring + s * stage_bytes, p.weights + (at.row_tile * p.chunks + at.chunk) * block_bytes(kE4M3),
+                      block_bytes(kE4M3), &full[s]);
+      };
+      const auto load_terms = [&](const Place& at, int s) {
+        tc::bulk_load(ring + s * stage_bytes + block_bytes(kE4M3), p.terms + ((int64_t)at.token_tile * p.chunks + at.chunk) * blk_b,
+                      (uint32_t)blk_b, &full[s]);
+      };
+      const int64_t n = u1 - u0;
+      const int ahead = n < p.stages ? (int)n : p.stages;
+      Place at = start;
+      for (int i = 0; i < ahead; ++i, advance(at)) load_weights(at, i);
+      pdl_wait();
+      at = start;
+      for (int i = 0; i < ahead; ++i, advance(at)) load_terms(at, i);
+      int64_t issued = ahead;
+      int s = ahead % p.stages;
+      uint32_t turn = (uint32_t)(ahead / p.stages);  // times that the ring has gone round
+      for (; issued < n; ++issued, advance(at)) {
+        if (!tc::mbar_wait_bounded(&empty[s], (turn & 1u) ^ 1u, s_abort, &g_linear_error)) break;
+        load_weights(at, s);
+        load_terms(at, s);
+        if (++s == p.stages) s = 0, ++turn;
+      }
+      // copies land before the CTA's memory goes away
+      for (int64_t i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+        tc::mbar_wait_issued(&full[i % p.stages], (uint32_t)(i / p.stages));
+    }
+    __syncwarp();
+  } else if (warp == kSumWarps + 1) {
+    const uint32_t one = tc::elect_one();
+    const uint32_t ring_at = tc::smem_u32(ring), idesc = idesc_of<kE4M3>(p.n);
+    int32_t chunk = chunk0;
+    int s = 0, a = 0;
+    uint32_t turn = 0, acc_turn = 0;
+    bool ok = true;
+    for (int64_t u = u0; ok && u < u1;) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&acc_empty[a], (acc_turn & 1u) ^ 1u, s_abort, &g_linear_error));
+      bool add = false;
+      const uint32_t acc = tmem + (uint32_t)(a * p.n);
+      for (; ok && u < u1 && chunk < p.chunks; ++u, ++chunk) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&full[s], turn & 1u, s_abort, &g_linear_error));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t a_at = ring_at + (uint32_t)(s * stage_bytes);
+        stage_products<kE4M3>(one, a_at, a_at + block_bytes(kE4M3), p.n, acc,
+                              tmem + (uint32_t)(accs * p.n + s * scale_cols(kE4M3, p.n)), idesc, add);
+        add = true;
+        tc::mma_commit_one(one, &empty[s]);
+        if (++s == p.stages) s = 0, ++turn;
+      }
+      chunk = 0;
+      // (whatever was issued ends before tensor memory is freed, an aborted run's too)
+      tc::mma_commit_one(one, &acc_full[a]);
+      if (u >= u1 || !ok) tc::mbar_wait_issued(&acc_full[a], acc_turn);
+      if (++a == accs) a = 0, ++acc_turn;
+    }
+    __syncwarp();
+  } else {
+    pdl_wait();  // the factors and the counts; and the outputs may have readers before this call
+    const int row = (warp & 3) * 32 + lane;
+    const int half = (p.n / kTerms / 2 + 3) / 4 * 4;  // tokens of a warp, at most 16
+    const int first = (warp >> 2) * half;
+    const int64_t per_part = (int64_t)(p.n / kTerms) * kRows;
+    int64_t tile = tile0;
+    int32_t chunk = chunk0;
+    int a = 0;
+    uint32_t acc_turn = 0;
+    for (int64_t u = u0; u < u1; ++tile) {
+      const int64_t token_tile = tile % p.token_tiles;
+      const int64_t t0 = token_tile * kTileTokens, out_row = tile / p.token_tiles * kRows + row;
+      const int nt = (int)(p.T - t0 < kTileTokens ? p.T - t0 : kTileTokens);
+      const bool begins = chunk == 0, ends = p.chunks - chunk <= u1 - u;
+      u += ends ? p.chunks - chunk : u1 - u;
+      chunk = 0;
+      // lane t holds token t's factor
+      const float factor = lane < nt ? p.factor[t0 + lane] : 0.0f;
+      // (after a wait that ran out the warps still meet at the same barriers: the waits of
+      // an aborted run end at once, and nothing is read or stored)
+      const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&acc_full[a], acc_turn & 1u, s_abort, &g_linear_error));
+      float y[16];
+      if (ok) {
+        tc::tc_fence_after();
+        const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(a * p.n + first * kTerms);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          if (i >= half || first + i >= nt) break;
+          uint32_t v[32];
+          // (columns past the accumulator hold scales or the other one: read, not used)
+          tc::tmem_ld_32x32b_x32(acc + (uint32_t)(i * kTerms), v);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            y[i + h] = sum_terms<kE4M3>(v + 8 * h) * __shfl_sync(0xffffffffu, factor, (first + i + h) & 31);
+        }
+        tc::tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&acc_empty[a]);
+      if (++a == accs) a = 0, ++acc_turn;
+
+      const int mine = ok ? min(half, nt - first) : 0;  // (none or fewer at the last tokens)
+      bool write = true;
+      if (!begins || !ends) {
+        float* to = p.parts + (g * 2 + (begins ? 1 : 0)) * per_part + (int64_t)first * kRows + row;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < mine) __stcg(to + i * kRows, y[i]);
+        // the CTAs that the tile's first and last chunk belong to
+        const int64_t g0 = ((tile * p.chunks + 1) * G - 1) / p.units, g1 = (((tile + 1) * p.chunks) * G - 1) / p.units;
+        __threadfence();
+        sync_sum_warps();
+        if (threadIdx.x == 0) *s_last = ok && atomicAdd(&p.joined[g0], 1) == (int)(g1 - g0);
+        sync_sum_warps();
+        write = *s_last != 0;
+        if (write) {
+          __threadfence();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+          for (int64_t c = g0; c <= g1; ++c) {
+            const float* from = p.parts + (c * 2 + (c == g0 ? 1 : 0)) * per_part + (int64_t)first * kRows + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i < mine) y[i] += __ldcg(from + i * kRows);
+          }
+        }
+      }
+      if (write) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < mine) put_out(p, t0 + first + i, out_row, y[i]);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == kSumWarps + 1) tc::tmem_dealloc(tmem, p.tmem_cols);
 }
 
 }  // namespace linear
@@ -456,52 +730,81 @@ static int64_t token_tiles_of(int32_t n_tokens) {
   return ((int64_t)n_tokens + linear::kTileTokens - 1) / linear::kTileTokens;
 }
 
+// Workspace of a product of more than kFewTokens: the tokens' factors, the counts and
+// parts of the tiles that CTAs share, the terms.
+struct LinearSpace {
+  size_t joined, parts, terms, bytes;
+};
+static LinearSpace space_of(int32_t T, int32_t n_in, bool e4m3) {
+  const int n = tile_columns(T);
+  LinearSpace s;
+  s.joined = al256((size_t)T * sizeof(float));
+  s.parts = s.joined + al256(linear::kStreamCtas * sizeof(int32_t));
+  s.terms = s.parts + (size_t)linear::kStreamCtas * 2 * (n / linear::kTerms) * linear::kRows * sizeof(float);
+  s.bytes = s.terms + (size_t)token_tiles_of(T) * (size_t)chunks_of(n_in) * linear::terms_bytes(e4m3, n);
+  return s;
+}
+
 extern "C" size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in, int32_t format) {
   if (n_tokens <= 0 || check_sizes(1, n_in, format) != CSA2_OK) return 0;
-  const size_t terms = (size_t)token_tiles_of(n_tokens) * (size_t)chunks_of(n_in) *
-                       linear::terms_bytes(format == CSA2_FP4_E4M3, tile_columns(n_tokens));
-  return al256((size_t)n_tokens * sizeof(float)) + al256(terms);
+  if (n_tokens <= linear::kFewTokens) return 256;  // (nothing is kept there)
+  return space_of(n_tokens, n_in, format == CSA2_FP4_E4M3).bytes;
+}
+
+// Stages that fit beside `acc` accumulator columns.
+static int stages_for(bool e4m3, int n, int acc, int cols, int smem) {
+  const int by_smem = (smem - linear::kHeadBytes - 1024) / (linear::block_bytes(e4m3) + linear::terms_bytes(e4m3, n));
+  const int by_cols = (cols - acc) / linear::scale_cols(e4m3, n);
+  const int most = by_smem < by_cols ? by_smem : by_cols;
+  return most < linear::kMaxStages ? most : linear::kMaxStages;
 }
 
 template <bool kE4M3>
-static int launch_linear(const void* x, int32_t T, const uint8_t* weights, int32_t n_out, int32_t n_in, float scale,
-                         void* out_bf16, float* out_f32, void* workspace, cudaStream_t stream) {
+static int launch_few(linear::Params p, cudaStream_t stream) {
   using namespace linear;
-  float* factor = (float*)workspace;
-  uint8_t* terms = (uint8_t*)workspace + al256((size_t)T * sizeof(float));
-  const int n = tile_columns(T);
-  const int64_t chunks = chunks_of(n_in), token_tiles = token_tiles_of(T), tiles = row_tiles_of(n_out) * token_tiles;
-  const int64_t slices = ((int64_t)n_in + kTermThreads * 8 - 1) / (kTermThreads * 8);
-  TermArgs ta{(const uint16_t*)x, T, n_in, (int32_t)chunks, n, (int32_t)slices, terms, factor};
-  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
-
-  const bool two = n <= 64;  // two CTAs to an SM
-  const int stage = block_bytes(kE4M3) + terms_bytes(kE4M3, n);
-  const int room = (two ? 113 : 226) * 1024 - kHeadBytes - 1024;
-  const int sf_cols = groups(kE4M3) * 4 * (1 + column_groups(n));
-  const int cols = two ? 256 : 512;
-  int stages = room / stage;
-  if (stages > (cols - n) / sf_cols) stages = (cols - n) / sf_cols;
-  if (stages > kMaxStages) stages = kMaxStages;
-  int cluster = 1;
-  while (cluster < 8 && tiles * cluster * 2 <= 304 && cluster * 2 <= chunks) cluster *= 2;
-  Params p{weights, terms, factor, (__nv_bfloat16*)out_bf16, out_f32, scale, T, n_out, (int32_t)chunks,
-           (int32_t)token_tiles, n, stages, cluster, (uint32_t)cols};
-  const int smem = kHeadBytes + 1024 + stages * stage;
-  static Csa2PerDeviceOnce once1, once2;
-  if (two) {
-    if (csa2_smem_optin((const void*)linear_kernel<kE4M3, 2>, 113 * 1024, once2) != CSA2_OK) return CSA2_ERR_CUDA;
-    if (csa2_launch_pdl_cluster(linear_kernel<kE4M3, 2>, dim3((unsigned)(tiles * cluster)), dim3(kThreads), (size_t)smem,
-                                stream, (unsigned)cluster, p) == cudaSuccess)
-      return CSA2_OK;
-  } else {
-    if (csa2_smem_optin((const void*)linear_kernel<kE4M3, 1>, 226 * 1024, once1) != CSA2_OK) return CSA2_ERR_CUDA;
-    if (csa2_launch_pdl_cluster(linear_kernel<kE4M3, 1>, dim3((unsigned)(tiles * cluster)), dim3(kThreads), (size_t)smem,
-                                stream, (unsigned)cluster, p) == cudaSuccess)
-      return CSA2_OK;
+  static Csa2PerDeviceOnce once;
+  constexpr int kSmem = 113 * 1024;  // two CTAs to an SM
+  if (csa2_smem_optin((const void*)few_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
+  const int64_t tiles = row_tiles_of(p.n_out);
+  p.tmem_cols = 256;
+  p.stages = stages_for(kE4M3, p.n, p.n, 256, kSmem);
+  p.split = 1;
+  while (p.split < kMaxSplit && tiles * p.split * 2 <= 304 && p.split * 2 <= p.chunks) p.split *= 2;
+  const int smem = kHeadBytes + 1024 + p.stages * (block_bytes(kE4M3) + terms_bytes(kE4M3, p.n));
+  if (csa2_launch_pdl_cluster(few_kernel<kE4M3>, dim3((unsigned)(tiles * p.split)), dim3(kThreads), (size_t)smem, stream,
+                              (unsigned)p.split, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return CSA2_ERR_CUDA;
   }
-  (void)cudaGetLastError();
-  return CSA2_ERR_CUDA;
+  return CSA2_OK;
+}
+
+template <bool kE4M3>
+static int launch_stream(linear::Params p, uint8_t* workspace, cudaStream_t stream) {
+  using namespace linear;
+  const LinearSpace space = space_of(p.T, p.n_in, kE4M3);
+  p.factor = (const float*)workspace;
+  p.joined = (int32_t*)(workspace + space.joined);
+  p.parts = (float*)(workspace + space.parts);
+  p.terms = workspace + space.terms;
+  const int64_t slices = ((int64_t)p.n_in + kTermThreads * 8 - 1) / (kTermThreads * 8);
+  TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
+  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
+
+  static Csa2PerDeviceOnce once;
+  constexpr int kSmem = 226 * 1024;
+  if (csa2_smem_optin((const void*)stream_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
+  const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
+  p.tmem_cols = 512;
+  p.stages = stages_for(kE4M3, p.n, p.n <= 128 ? 2 * p.n : p.n, 512, kSmem);
+  p.units = tiles * p.chunks;
+  static int UN = getenv("UN") ? atoi(getenv("UN")) : 2;
+  int64_t ctas = p.units / UN;
+  if (ctas < tiles) ctas = tiles;
+  if (ctas > kStreamCtas) ctas = kStreamCtas;
+  const int smem = kHeadBytes + 1024 + p.stages * (block_bytes(kE4M3) + terms_bytes(kE4M3, p.n));
+  CSA2_LAUNCH_PDL(stream_kernel<kE4M3>, dim3((unsigned)ctas), dim3(kStreamThreads), (size_t)smem, stream, p);
+  return CSA2_OK;
 }
 
 extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8_t* weights, int32_t n_out, int32_t n_in,
@@ -520,8 +823,20 @@ extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8
     return CSA2_ERR_UNSUPPORTED_SHAPE;
   const size_t need = csa2_fp4_linear_workspace_size(n_tokens, n_in, format);
   if (!workspace || workspace_bytes < need || !csa2_aligned(workspace, 256)) return CSA2_ERR_WORKSPACE;
-  return format == CSA2_FP4_E4M3 ? launch_linear<true>(x_bf16, n_tokens, weights, n_out, n_in, scale, out_bf16, out_f32,
-                                                       workspace, (cudaStream_t)stream)
-                                 : launch_linear<false>(x_bf16, n_tokens, weights, n_out, n_in, scale, out_bf16, out_f32,
-                                                        workspace, (cudaStream_t)stream);
+  linear::Params p{};
+  p.weights = weights;
+  p.x = (const uint16_t*)x_bf16;
+  p.out_bf16 = (__nv_bfloat16*)out_bf16;
+  p.out_f32 = out_f32;
+  p.scale = scale;
+  p.T = n_tokens;
+  p.n_out = n_out;
+  p.n_in = n_in;
+  p.chunks = (int32_t)chunks_of(n_in);
+  p.token_tiles = (int32_t)token_tiles_of(n_tokens);
+  p.n = tile_columns(n_tokens);
+  const bool e4m3 = format == CSA2_FP4_E4M3;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (n_tokens <= linear::kFewTokens) return e4m3 ? launch_few<true>(p, s) : launch_few<false>(p, s);
+  return e4m3 ? launch_stream<true>(p, (uint8_t*)workspace, s) : launch_stream<false>(p, (uint8_t*)workspace, s);
 }
