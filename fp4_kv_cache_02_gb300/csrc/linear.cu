@@ -9,17 +9,15 @@
 //
 // The weights go to the tensor cores as they lie in memory: block-scaled FP4
 // products with both operands E2M1. A bf16 row enters as a sum of kTerms = 8 E2M1
-// vectors. With s = 2^e the block's scale such that its largest |x| / s is in
-// [3.5, 7), the first term is x / s rounded to E2M1; what is left is at most s and
-// is rounded on the grid of s / 4, what is left then (at most s / 8) on that of
-// s / 32, and so on by 8: the remainder after eight terms is at most 2^-21 s, 2^-22 of
-// the block's largest, and zero for every channel within 2^-14 of it (its last bit is
-// a multiple of the eighth scale). All remainders are exact in fp32 on the way. The terms
+// vectors, the digits of its channels in base 8. With 2^E the leading power of two of
+// a block's largest channel, each channel is rounded to a multiple of 2^(E-21): off by
+// at most 2^-22 of the largest, and by nothing within 2^-14 of it, where all eight
+// bits of a bf16 lie on that grid. The multiple, below 2^22, has eight digits of
+// -4 .. 3, and those times 1/2 are E2M1 values, whose code is the digit's sign and
+// magnitude; the scales of the eight vectors are 2^(E+1), 2^(E-2) .. 2^(E-20). The terms
 // of a token are eight columns of the second operand, so the products cost tensor
 // time that a product bound by its weights' bytes has to spare, and no instruction
 // of the CUDA cores per weight.
-#include <stdlib.h>
-
 #include "tc_common.cuh"
 
 namespace csa2 {
@@ -37,11 +35,12 @@ constexpr int kFewTokens = 4;               // tokens whose terms the product's 
 constexpr int kMaxSplit = 8;                // CTAs that split the inputs of such a product
 constexpr int kStreamCtas = 152;            // of a product of more tokens: one to an SM
 constexpr int kMaxStages = 8;
-constexpr int kThreads = 192;
-constexpr int kProducerWarp = 4;
-constexpr int kMmaWarp = 5;
+constexpr int kSumWarps = 8;                // warps that make terms and sum columns
+constexpr int kProducerWarp = kSumWarps;
+constexpr int kMmaWarp = kSumWarps + 1;
+constexpr int kThreads = 32 * (kSumWarps + 2);
 constexpr int kTermThreads = 256;
-constexpr int kMinExp = -100;               // of a block's scale: all the terms' scales are E8M0 then
+constexpr int kMinExp = -100;               // of a block's largest: all the terms' scales are E8M0 then
 
 // Groups of scales in a block of 256 inputs: a group is what one tcgen05.cp moves,
 // four bytes (128 inputs at one scale per 32, 64 at one per 16) of 128 rows.
@@ -93,16 +92,10 @@ __global__ void weights_kernel(const uint8_t* __restrict__ data, const uint8_t* 
 
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// The exponent e of the scale of a block whose largest magnitude has these bf16 bits.
-__device__ __forceinline__ int scale_exp(uint32_t bits) {
-  const int e = (int)(bits >> 7) - 127 - 2 + ((bits & 0x60u) == 0x60u ? 1 : 0);
+// The exponent E of a block whose largest magnitude has these bf16 bits.
+__device__ __forceinline__ int block_exp(uint32_t bits) {
+  const int e = (int)(bits >> 7) - 127;
   return e < kMinExp ? kMinExp : e;
-}
-
-__device__ __forceinline__ float2 e2m1x2_to_f32x2(uint32_t byte) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(byte));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // The largest magnitude's bf16 bits of eight channels.
@@ -112,59 +105,87 @@ __device__ __forceinline__ uint32_t top_bits(uint4 v) {
   return max(m2 & 0xFFFFu, m2 >> 16);
 }
 
-// A token's factor: with E4M3 scales the power of two that its terms' scales are relative
-// to, 2^-8 of the largest block scale; NaN for a row that holds an infinity or a NaN.
+// The terms' scales are held relative to a power of two, 2^base, put back behind the
+// product as the token's factor. With E8M0 scales base is 1: the first scale of a block
+// with E = 127 is 2^128. With E4M3 scales it is such that the largest block's first one
+// is 2^8, the largest power of two that E4M3 holds, and the terms' common ratios are left
+// to sum_terms. A row that holds an infinity or a NaN has the factor NaN.
 template <bool kE4M3>
-__device__ __forceinline__ int base_exp(uint32_t top) { return kE4M3 ? scale_exp(top) - 8 : 0; }
+__device__ __forceinline__ int base_exp(uint32_t top) { return kE4M3 ? block_exp(top) - 7 : 1; }
 template <bool kE4M3>
 __device__ __forceinline__ float factor_of(uint32_t top) {
   return top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                         : __uint_as_float((uint32_t)(base_exp<kE4M3>(top) + 127) << 23);
 }
 
+// Base-8 digits (24 bits) one to a nibble; each nibble's highest bit is not defined.
+__device__ __forceinline__ uint32_t spread_digits(uint32_t v) {
+  v = (v & 0x00000FFFu) | ((v << 4) & ~0x00000FFFu);
+  v = (v & 0x00FF00FFu) | ((v << 2) & ~0x00FF00FFu);
+  return (v & 0x0F0F0F0Fu) | ((v << 1) & ~0x0F0F0F0Fu);
+}
+// Eight digits + 4 (0 .. 7, one to a nibble) to E2M1 codes of the digits times 1/2: the
+// digit itself from 4 on, else the sign and 4 - digit.
+__device__ __forceinline__ uint32_t digit_codes(uint32_t w) {
+  w &= 0x77777777u;
+  const uint32_t positive = ((w >> 2) & 0x11111111u) * 15u;
+  return (positive & w & 0x33333333u) | (~positive & (0xCCCCCCCCu - w));
+}
+
 // One warp: the eight terms of a token's chunk of 256 channels, eight channels v to a
-// lane, into rows 8 tl .. 8 tl + 7 of the second operand's block. With E4M3 scales the
-// terms' scales are powers of two, 2^-9 .. 2^8 relative to `base` (a block below that
-// takes the smallest), and term j counts 2^(1-3j) of term 0: both are put back behind the
-// product. With E8M0 scales they stand in the scale bytes.
+// lane, into rows 8 tl .. 8 tl + 7 of the second operand's block. (With a conversion to
+// E2M1, one back and a remainder for each term the terms of 1,021 x 4,096 channels took
+// 12 us; conversions are a quarter of the rate of other instructions.)
 template <bool kE4M3>
 __device__ __forceinline__ void put_terms(uint4 v, int base, int tl, uint8_t* data, uint8_t* scales, int nh, int lane) {
   uint32_t m = top_bits(v);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   if (!kE4M3) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  int e = scale_exp(m);
-  if (kE4M3) e = max(e, base - 9);
-  e = min(e, 126);  // (of a row that is not finite any terms do)
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-  float r[8];
+  int e = block_exp(m);
+  if (kE4M3) e = max(e, base + 7 - 17);  // (the smallest power of two that E4M3 holds is 2^-9)
+  e = min(e, 127);                       // (of a row that is not finite any terms do)
+  // x 2^(21-e), |x| < 2^(e+1), to the nearest integer: in the low bits of a sum with
+  // 1.5 x 2^23; then eight digits + 4
+  const float up = __uint_as_float((uint32_t)(127 + 21 - e) << 23);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t z[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    r[2 * i] = __uint_as_float(w[i] << 16) * inv;
-    r[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+    z[2 * i] = __float_as_uint(fmaf(__uint_as_float(w[i] << 16), up, 12582912.0f));
+    z[2 * i + 1] = __float_as_uint(fmaf(__uint_as_float(w[i] & 0xFFFF0000u), up, 12582912.0f));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = spread_digits((z[i] - 0x4B400000u + 044444444u) & 0xFFFFFFu);
+  // channel i's digits 0 .. 7 -> digit d of the eight channels: halves, bytes, nibbles
+  uint32_t h[8], b[8], d[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = __byte_perm(z[i], z[i + 4], 0x5410);      // digits 0 .. 3
+    h[i + 4] = __byte_perm(z[i], z[i + 4], 0x7632);  // digits 4 .. 7
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 4)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      b[i + j] = __byte_perm(h[i + j], h[i + j + 2], 0x6240);      // digits i, i + 1 of channels j, j + 2, ..
+      b[i + j + 2] = __byte_perm(h[i + j], h[i + j + 2], 0x7351);  // digits i + 2, i + 3
+    }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    d[i] = (b[i] & 0x0F0F0F0Fu) | ((b[i + 1] << 4) & 0xF0F0F0F0u);
+    d[i + 1] = ((b[i] >> 4) & 0x0F0F0F0Fu) | (b[i + 1] & 0xF0F0F0F0u);
   }
   constexpr int kLanesPer = kE4M3 ? 2 : 4;
   const int s_at = lane / kLanesPer;  // scale of the row: group s_at / 4, byte s_at % 4
-  uint32_t s_code = 0;
-  if (kE4M3) {
-    const int rel = e - base;  // -9 .. 8
-    s_code = rel >= -6 ? (uint32_t)(rel + 7) << 3 : 1u << (rel + 9);
-  }
+  const int n0 = tl * kTerms;         // (eight rows lie in one group of 32)
+  uint8_t* s_to = scales + ((s_at / 4) * nh + n0 / 128) * group_bytes() + scale_place(n0 % 128) + s_at % 4;
+  const int rel = e + 1 - base;  // of the first term's scale; E4M3: -9 .. 8
+  const uint32_t e4m3 = rel >= -6 ? (uint32_t)(rel + 7) << 3 : 1u << ((rel + 9) & 31);
+  uint8_t* to = data + n0 * (kChunk / 2) + (lane % 4) * 4;
 #pragma unroll
   for (int j = 0; j < kTerms; ++j) {
-    const uint32_t codes = cvt_e2m1x8(r);
-    const float up = j == 0 ? 4.0f : 8.0f;  // the next grid
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 q = e2m1x2_to_f32x2((codes >> (8 * i)) & 0xFFu);
-      r[2 * i] = (r[2 * i] - q.x) * up;
-      r[2 * i + 1] = (r[2 * i + 1] - q.y) * up;
-    }
-    const int n = tl * kTerms + j;
-    *reinterpret_cast<uint32_t*>(data + tc::sw128_offset(n, lane / 4) + (lane % 4) * 4) = codes;
-    if (!kE4M3) s_code = (uint32_t)(e + 127 - (j == 0 ? 0 : 3 * j - 1));
-    if (lane % kLanesPer == 0)
-      scales[((s_at / 4) * nh + n / 128) * group_bytes() + scale_place(n % 128) + s_at % 4] = (uint8_t)s_code;
+    *reinterpret_cast<uint32_t*>(to + tc::sw128_offset(j, lane / 4)) = digit_codes(d[7 - j]);
+    if (lane % kLanesPer == 0) s_to[16 * j] = (uint8_t)(kE4M3 ? e4m3 : (uint32_t)(rel + 127 - 3 * j));
   }
 }
 
@@ -176,8 +197,10 @@ struct TermArgs {
   int32_t* joined;
 };
 
-// The terms of all tokens, ahead of the product: one CTA takes 2,048 channels of a
-// token, eight to a thread.
+// The terms of all tokens, ahead of the product: one CTA takes 4,096 channels of a
+// token, twice eight to a thread. A token's factor is the sum of factor[t][0 .. factors - 1]:
+// with E4M3 scales one (every CTA looks at the whole row for its base), with E8M0 one to
+// a CTA (of 32,768 channels a look at the whole row took 3 us longer).
 template <bool kE4M3>
 __global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
   pdl_begin();
@@ -186,23 +209,34 @@ __global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
   const int32_t t = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
   const uint16_t* row = a.x + (int64_t)t * a.n_in;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t top = 0;
-  for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kTermThreads * 8)
-    top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
+  const int64_t k = ((int64_t)slice * 2 * kTermThreads + threadIdx.x) * 8;
+  constexpr int kStep = kTermThreads * 8;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const uint4 v0 = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : none;
+  const uint4 v1 = k + kStep < a.n_in ? *reinterpret_cast<const uint4*>(row + k + kStep) : none;
+  uint32_t top = max(top_bits(v0), top_bits(v1));
+  if (kE4M3 && a.slices > 1)
+#pragma unroll 4
+    for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kStep)
+      top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) s_max[warp] = top;
   __syncthreads();
   top = s_max[0];
 #pragma unroll
   for (int i = 1; i < kTermThreads / 32; ++i) top = max(top, s_max[i]);
-  if (slice == 0 && threadIdx.x == 0) a.factor[t] = factor_of<kE4M3>(top);
-
-  const int64_t k = ((int64_t)slice * kTermThreads + threadIdx.x) * 8;
+  if (threadIdx.x == 0 && (!kE4M3 || slice == 0)) {
+    const float factor = factor_of<kE4M3>(top);
+    a.factor[kE4M3 ? t : (int64_t)t * a.slices + slice] = slice == 0 || isnan(factor) ? factor : 0.0f;
+  }
+  const int base = base_exp<kE4M3>(top);
+  const auto put = [&](uint4 v, int32_t c) {  // (a warp has one chunk)
+    uint8_t* block = a.terms + ((int64_t)(t / kTileTokens) * a.chunks + c) * terms_bytes(kE4M3, a.n);
+    put_terms<kE4M3>(v, base, t % kTileTokens, block, block + a.n * (kChunk / 2), column_groups(a.n), lane);
+  };
   const int32_t c = (int32_t)(k / kChunk);
-  if (c >= a.chunks) return;  // (whole warps: a warp has one chunk)
-  const uint4 v = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0, 0, 0, 0);
-  uint8_t* block = a.terms + ((int64_t)(t / kTileTokens) * a.chunks + c) * terms_bytes(kE4M3, a.n);
-  put_terms<kE4M3>(v, base_exp<kE4M3>(top), t % kTileTokens, block, block + a.n * (kChunk / 2), column_groups(a.n), lane);
+  if (c < a.chunks) put(v0, c);
+  if (c + kStep / kChunk < a.chunks) put(v1, c + kStep / kChunk);
 }
 
 // ---- the product -----------------------------------------------------------------
@@ -211,15 +245,15 @@ __global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
 // tile * chunks + chunk.
 struct Params {
   const uint8_t* weights;
-  const uint16_t* x;      // few_kernel
-  const uint8_t* terms;   // stream_kernel, as all of the following but the last line
+  const uint16_t* x;
+  const uint8_t* terms;
   const float* factor;
-  int32_t* joined;        // parts that are there of the tile that CTA g is the first to have a part of
-  float* parts;           // [CTA][2][tokens of a tile][128]
+  int32_t* joined;  // stream_kernel: parts that are there of the tile that CTA g is the first to have a part of
+  float* parts;     // stream_kernel: [CTA][2][tokens of a tile][128]
   __nv_bfloat16* out_bf16;
   float* out_f32;
   float scale;
-  int32_t T, n_out, n_in, chunks, token_tiles, n, stages, split;
+  int32_t T, n_out, n_in, chunks, token_tiles, n, stages, split, factors;
   int64_t units;          // tiles x chunks
   uint32_t tmem_cols;
 };
@@ -238,7 +272,7 @@ __device__ __forceinline__ float ld_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void sync_four_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void sync_sum_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 constexpr int kHeadBytes = 512;  // barriers and words ahead of the ring's 1,024-byte boundary
 
@@ -278,14 +312,25 @@ __device__ __forceinline__ uint32_t idesc_of(int n) {
 // Scale columns of a stage.
 __host__ __device__ constexpr int scale_cols(bool e4m3, int n) { return groups(e4m3) * 4 * (1 + column_groups(n)); }
 
+// Tokens of a sum warp: half of a tile's, in fours, at most 16.
+__device__ __forceinline__ int tokens_of_warp(int n) { return (n / kTerms / 2 + 3) / 4 * 4; }
+
 // A token's eight columns.
 template <bool kE4M3>
 __device__ __forceinline__ float sum_terms(const uint32_t* v) {
   float y = __uint_as_float(v[7]);
 #pragma unroll
   for (int j = 6; j >= 0; --j)
-    y = kE4M3 ? fmaf(y, j == 0 ? 0.25f : 0.125f, __uint_as_float(v[j])) : y + __uint_as_float(v[j]);
+    y = kE4M3 ? fmaf(y, 0.125f, __uint_as_float(v[j])) : y + __uint_as_float(v[j]);
   return y;
+}
+
+// A token's factor, of which terms_kernel's CTAs wrote a part each.
+__device__ __forceinline__ float token_factor(const Params& p, int64_t t) {
+  float factor = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < p.factors; ++i) factor += __ldcg(p.factor + t * p.factors + i);
+  return factor;
 }
 
 __device__ __forceinline__ void put_out(const Params& p, int64_t t, int64_t row, float y) {
@@ -295,17 +340,19 @@ __device__ __forceinline__ void put_out(const Params& p, int64_t t, int64_t row,
   if (p.out_f32) p.out_f32[t * p.n_out + row] = y;
 }
 
-// ---- few tokens ------------------------------------------------------------------
-// One to four tokens in one launch: a CTA takes 128 outputs x a range of chunks and makes
-// its own terms (ahead of the product they would cost a launch and a trip through L2, 4 us
-// of 15 for 32,768 x 4,096 weights). The CTAs of a cluster split a row tile's chunks, and
-// their sums are added in rank order out of one another's shared memory.
-//   warp 4     producer: a bulk copy of a block of weights per stage, the first ones
-//              before x is waited for;
-//   warp 5     scales to tensor memory, products;
-//   warps 0-3  the terms, a (chunk, token) to a warp; then the columns summed, stored.
-template <bool kE4M3>
-__global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
+// ---- few tiles -------------------------------------------------------------------
+// Products of too few tiles (128 outputs x up to 32 tokens) to fill the SMs, and those
+// of few tokens. The CTAs of a cluster split a tile's chunks, and their sums are added in
+// rank order out of one another's shared memory. kOwnTerms: up to eight tokens, whose terms
+// each CTA makes itself: ahead of the product they would cost a launch and a trip through
+// L2 (4 us of 15 for a token by 32,768 x 4,096 weights).
+//   warp 8     producer: a bulk copy of a block of weights per stage (and one of the
+//              terms), the first weights before the call's inputs are waited for;
+//   warp 9     scales to tensor memory, products;
+//   warps 0-7  kOwnTerms: the terms, a (chunk, token) to a warp; then the columns summed
+//              (a quarter of the rows, half of the tokens each), stored.
+template <bool kE4M3, bool kOwnTerms, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);
   uint64_t* empty = full + kMaxStages;
@@ -317,14 +364,19 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = (int)(blockIdx.x % (uint32_t)p.split);
-  const int64_t row_tile = blockIdx.x / (uint32_t)p.split;
+  const int64_t tile = blockIdx.x / (uint32_t)p.split;
+  const int32_t token_tile = (int32_t)(tile % p.token_tiles);
+  const int64_t row_tile = tile / p.token_tiles;
+  const int32_t t0 = token_tile * kTileTokens;
+  const int nt = min(p.T - t0, kTileTokens);
   const int32_t c0 = (int32_t)((int64_t)p.chunks * part / p.split);
   const int32_t n_chunks = (int32_t)((int64_t)p.chunks * (part + 1) / p.split) - c0;
-  const int stage_bytes = block_bytes(kE4M3) + terms_bytes(kE4M3, p.n);
+  const int blk_b = terms_bytes(kE4M3, p.n);
+  const int stage_bytes = block_bytes(kE4M3) + blk_b;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      tc::mbar_init(&full[s], 1 + p.T);
+      tc::mbar_init(&full[s], kOwnTerms ? 1 + p.T : 1);
       tc::mbar_init(&empty[s], 1);
     }
     tc::mbar_init(acc_full, 1);
@@ -340,12 +392,25 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
   if (warp == kProducerWarp) {
     if (lane == 0) {
       const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
-      int issued = 0;
+      const uint8_t* terms = kOwnTerms ? nullptr : p.terms + ((int64_t)token_tile * p.chunks + c0) * blk_b;
+      const auto load_weights = [&](int i, int s) {
+        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(kOwnTerms ? block_bytes(kE4M3) : stage_bytes));
+        tc::bulk_load(ring + s * stage_bytes, from + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full[s]);
+      };
+      const auto load_terms = [&](int i, int s) {
+        if constexpr (!kOwnTerms)
+          tc::bulk_load(ring + s * stage_bytes + block_bytes(kE4M3), terms + (int64_t)i * blk_b, (uint32_t)blk_b, &full[s]);
+      };
+      const int ahead = n_chunks < p.stages ? n_chunks : p.stages;
+      for (int i = 0; i < ahead; ++i) load_weights(i, i);
+      if constexpr (!kOwnTerms) pdl_wait();
+      for (int i = 0; i < ahead; ++i) load_terms(i, i);
+      int issued = ahead;
       for (; issued < n_chunks; ++issued) {
         const int s = issued % p.stages;
         if (!tc::mbar_wait_bounded(&empty[s], ((uint32_t)(issued / p.stages) & 1u) ^ 1u, s_abort, &g_linear_error)) break;
-        tc::mbar_arrive_expect_tx(&full[s], block_bytes(kE4M3));
-        tc::bulk_load(ring + s * stage_bytes, from + (int64_t)issued * block_bytes(kE4M3), block_bytes(kE4M3), &full[s]);
+        load_weights(issued, s);
+        load_terms(issued, s);
       }
       // copies land before the CTA's memory goes away
       for (int i = max(0, issued - p.stages); i < issued; ++i)
@@ -370,36 +435,47 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
     tc::mbar_wait_issued(acc_full, 0);
     __syncwarp();
   } else {
-    pdl_wait();  // x; and the outputs may have readers before this call
+    pdl_wait();  // x or the factors; and the outputs may have readers before this call
+  }
+  if (kOwnTerms && warp < kSumWarps) {
     const auto channels = [&](int c, int t) {
       const int32_t k = (c0 + c) * kChunk + lane * 8;
       return k < p.n_in ? *reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.n_in + k) : make_uint4(0, 0, 0, 0);
     };
     uint32_t top[kFewTokens] = {};
+    const auto top_of = [&](int t) {
+      uint32_t m = s_top[t];
+#pragma unroll
+      for (int i = 1; i < kSumWarps; ++i) m = max(m, s_top[i * kFewTokens + t]);
+      return m;
+    };
     const auto share_tops = [&]() {
 #pragma unroll
       for (int t = 0; t < kFewTokens; ++t) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, top[t]);
         if (lane == 0) s_top[warp * kFewTokens + t] = m;
       }
-      sync_four_warps();
+      sync_sum_warps();
     };
     if (kE4M3) {  // the scales' base: the largest of this CTA's channels
-      for (int c = warp; c < n_chunks; c += 4)
+      for (int c = warp; c < n_chunks; c += kSumWarps)
 #pragma unroll
         for (int t = 0; t < kFewTokens; ++t)
           if (t < p.T) top[t] = max(top[t], top_bits(channels(c, t)));
       share_tops();
     }
-    const int n_tasks = n_chunks * p.T;
-    for (int i = warp; i < n_tasks; i += 4) {
+    // No more warps than there are (stage, token) places: a warp's last task is then at
+    // most a round of the ring behind its next, so that the stage it waits for is in the
+    // phase before the awaited one or later (a barrier tells two phases apart, not three).
+    const int n_tasks = n_chunks * p.T, workers = min(kSumWarps, p.stages * p.T);
+    for (int i = warp < workers ? warp : n_tasks; i < n_tasks; i += workers) {
       const int c = i / p.T, t = i % p.T, s = c % p.stages;
       const uint4 v = channels(c, t);
       const bool ok = tc::mbar_wait_bounded(&empty[s], ((uint32_t)(c / p.stages) & 1u) ^ 1u, s_abort, &g_linear_error);
       if (!__all_sync(0xffffffffu, ok)) break;
-      int base = 0;
+      uint32_t whole = 0;  // (E8M0 scales need no base of the token's own)
       if (kE4M3) {
-        base = base_exp<kE4M3>(max(max(s_top[t], s_top[kFewTokens + t]), max(s_top[2 * kFewTokens + t], s_top[3 * kFewTokens + t])));
+        whole = top_of(t);
       } else {
         const uint32_t m = top_bits(v);
 #pragma unroll
@@ -407,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
           if (j == t) top[j] = max(top[j], m);
       }
       uint8_t* data = ring + s * stage_bytes + block_bytes(kE4M3);
-      put_terms<kE4M3>(v, base, t, data, data + p.n * (kChunk / 2), 1, lane);
+      put_terms<kE4M3>(v, base_exp<kE4M3>(whole), t, data, data + p.n * (kChunk / 2), 1, lane);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&full[s]);
@@ -415,38 +491,47 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
     if (!kE4M3) share_tops();
   }
 
-  float* sums = reinterpret_cast<float*>(ring);  // [T][128], once the ring is done with
-  if (warp < 4) {
-    bool ok = tc::mbar_wait_bounded(acc_full, 0, s_abort, &g_linear_error);
-    ok = __all_sync(0xffffffffu, ok) && !*s_abort;
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc::tc_fence_after();
-      const int row = warp * 32 + lane;
-      uint32_t v[32];
-      // (columns past the accumulator hold scales: read, not used)
-      tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16), v);
-      tc::tmem_ld_wait();
+  float* sums = reinterpret_cast<float*>(ring);  // [nt][128], once the ring is done with
+  if (warp < kSumWarps) {
+    // lane t holds token t's factor (asked for one by one they cost a trip to L2 each)
+    float factor = 0.0f;
+    if (lane < nt) {
+      if constexpr (kOwnTerms) {
+        uint32_t m = s_top[lane];
 #pragma unroll
-      for (int t = 0; t < kFewTokens; ++t) {
-        if (t >= p.T) break;
-        const float y =
-            sum_terms<kE4M3>(v + 8 * t) *
-            factor_of<kE4M3>(max(max(s_top[t], s_top[kFewTokens + t]), max(s_top[2 * kFewTokens + t], s_top[3 * kFewTokens + t])));
-        if (p.split > 1)
-          sums[t * kRows + row] = y;
-        else
-          put_out(p, t, row_tile * kRows + row, y);
+        for (int i = 1; i < kSumWarps; ++i) m = max(m, s_top[i * kFewTokens + lane]);
+        factor = factor_of<kE4M3>(m);
+      } else {
+        factor = token_factor(p, t0 + lane);
       }
-      tc::tc_fence_before();
-    } else if (p.split > 1) {
-      for (int t = 0; t < p.T; ++t) sums[t * kRows + threadIdx.x] = __uint_as_float(0x7FC00000u);
     }
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(acc_full, 0, s_abort, &g_linear_error));
+    if (ok) tc::tc_fence_after();
+    const int row = (warp & 3) * 32 + lane;
+    const int half = tokens_of_warp(p.n), first = (warp >> 2) * half;
+    for (int t = first; t < min(first + half, nt); t += 4) {
+      uint32_t v[32];
+      if (ok) {
+        // (columns past the accumulator hold scales: read, not used)
+        tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(t * kTerms), v);
+        tc::tmem_ld_wait();
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float y = sum_terms<kE4M3>(v + 8 * h) * __shfl_sync(0xffffffffu, factor, (t + h) & 31);
+        if (t + h >= min(first + half, nt) || !ok) continue;
+        if (p.split > 1)
+          sums[(t + h) * kRows + row] = y;
+        else
+          put_out(p, t0 + t + h, row_tile * kRows + row, y);
+      }
+    }
+    if (ok) tc::tc_fence_before();
   }
   __syncthreads();
   if (p.split > 1) {
     cluster_sync();
-    const int per = p.T * kRows / p.split;  // (split is a power of two)
+    const int per = nt * kRows / p.split;  // (split is a power of two)
     for (int i = threadIdx.x; i < per; i += kThreads) {
       const int at = part * per + i;
       const uint32_t here = tc::smem_u32(sums + at);
@@ -456,14 +541,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
       float y = v[0];
 #pragma unroll
       for (int c = 1; c < kMaxSplit; ++c) y += v[c];
-      put_out(p, at / kRows, row_tile * kRows + at % kRows, y);
+      put_out(p, t0 + at / kRows, row_tile * kRows + at % kRows, y);
     }
     cluster_sync();  // the peers have read this CTA's sums
   }
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// ---- more tokens -----------------------------------------------------------------
+// ---- many tiles ------------------------------------------------------------------
 // Tiles of 128 outputs x up to 32 tokens. All tiles' chunks form one list (a row tile's
 // token tiles one after another, so that its weights are in L2 for them), cut into one
 // equal run to an SM. A run begins and ends inside tiles: their parts go through the
@@ -474,13 +559,13 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(Params p) {
 //   warp 9     scales to tensor memory, products; two accumulators up to 16 tokens;
 //   warps 0-7  the columns summed (a quarter of the rows, half of the tokens each), the
 //              accumulator given back, then stored or joined.
-constexpr int kSumWarps = 8;
-constexpr int kStreamThreads = 32 * (kSumWarps + 2);
-
-__device__ __forceinline__ void sync_sum_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
+__device__ __forceinline__ int load_acquire(const int* at) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+  return v;
+}
 template <bool kE4M3>
-__global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);
   uint64_t* empty = full + kMaxStages;
@@ -489,6 +574,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Params p) {
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
+  volatile int* s_complete = reinterpret_cast<volatile int*>(s_tmem + 3);  // [2]: of the first and the last tile
   uint8_t* ring = ring_of(smem_raw);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -594,22 +680,43 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Params p) {
   } else {
     pdl_wait();  // the factors and the counts; and the outputs may have readers before this call
     const int row = (warp & 3) * 32 + lane;
-    const int half = (p.n / kTerms / 2 + 3) / 4 * 4;  // tokens of a warp, at most 16
-    const int first = (warp >> 2) * half;
-    const int64_t per_part = (int64_t)(p.n / kTerms) * kRows;
+    const int half = tokens_of_warp(p.n), first = (warp >> 2) * half;
+    // where CTA c's part of its first tile, or of the tile that it begins, goes
+    const auto part_of = [&](int64_t c, bool begun) { return p.parts + (c * 2 + begun) * (p.n / kTerms) * kRows; };
     int64_t tile = tile0;
     int32_t chunk = chunk0;
     int a = 0;
     uint32_t acc_turn = 0;
     for (int64_t u = u0; u < u1; ++tile) {
       const int64_t token_tile = tile % p.token_tiles;
-      const int64_t t0 = token_tile * kTileTokens, out_row = tile / p.token_tiles * kRows + row;
+      const int64_t t0 = token_tile * kTileTokens, out_row = tile / p.token_tiles * kRows;
       const int nt = (int)(p.T - t0 < kTileTokens ? p.T - t0 : kTileTokens);
       const bool begins = chunk == 0, ends = p.chunks - chunk <= u1 - u;
       u += ends ? p.chunks - chunk : u1 - u;
       chunk = 0;
       // lane t holds token t's factor
-      const float factor = lane < nt ? p.factor[t0 + lane] : 0.0f;
+      float factor = 0.0f;
+      if (lane < nt) factor = token_factor(p, t0 + lane);
+      // A tile in parts: the CTAs that its first and last chunk belong to. Where there are
+      // two and the other's part is there (that of a run's last tile mostly is: the next
+      // CTA began with it), it is added to this one's, which need not be written.
+      const bool shared = !begins || !ends;
+      int64_t g0 = g, g1 = g;
+      bool complete = false;
+      float other[16];
+      if (shared) {
+        g0 = ((tile * p.chunks + 1) * G - 1) / p.units;
+        g1 = (((tile + 1) * p.chunks) * G - 1) / p.units;
+        if (g1 - g0 == 1) {
+          if (threadIdx.x == 0) s_complete[begins] = load_acquire(&p.joined[g0]);
+          sync_sum_warps();
+          complete = s_complete[begins] != 0;
+          const float* from = part_of(g == g0 ? g1 : g0, g != g0) + (int64_t)first * kRows + row;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (complete && i < half && first + i < nt) other[i] = __ldcg(from + i * kRows);
+        }
+      }
       // (after a wait that ran out the warps still meet at the same barriers: the waits of
       // an aborted run end at once, and nothing is read or stored)
       const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&acc_full[a], acc_turn & 1u, s_abort, &g_linear_error));
@@ -635,35 +742,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Params p) {
       if (++a == accs) a = 0, ++acc_turn;
 
       const int mine = ok ? min(half, nt - first) : 0;  // (none or fewer at the last tokens)
-      bool write = true;
-      if (!begins || !ends) {
-        float* to = p.parts + (g * 2 + (begins ? 1 : 0)) * per_part + (int64_t)first * kRows + row;
+      if (complete) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < mine) __stcg(to + i * kRows, y[i]);
-        // the CTAs that the tile's first and last chunk belong to
-        const int64_t g0 = ((tile * p.chunks + 1) * G - 1) / p.units, g1 = (((tile + 1) * p.chunks) * G - 1) / p.units;
-        __threadfence();
-        sync_sum_warps();
-        if (threadIdx.x == 0) *s_last = ok && atomicAdd(&p.joined[g0], 1) == (int)(g1 - g0);
-        sync_sum_warps();
-        write = *s_last != 0;
-        if (write) {
-          __threadfence();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = 0.0f;
-          for (int64_t c = g0; c <= g1; ++c) {
-            const float* from = p.parts + (c * 2 + (c == g0 ? 1 : 0)) * per_part + (int64_t)first * kRows + row;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i < mine) y[i] += __ldcg(from + i * kRows);
-          }
-        }
+        for (int i = 0; i < 16; ++i) y[i] += other[i];  // (in either order the same)
       }
-      if (write) {
+      if (!shared || complete) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (i < mine) put_out(p, t0 + first + i, out_row, y[i]);
+          if (i < mine) put_out(p, t0 + first + i, out_row + row, y[i]);
+        continue;
+      }
+      float* to = part_of(g, begins) + (int64_t)first * kRows + row;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < mine) __stcg(to + i * kRows, y[i]);
+      __threadfence();
+      sync_sum_warps();
+      if (threadIdx.x == 0) *s_last = ok && atomicAdd(&p.joined[g0], 1) == (int)(g1 - g0);
+      sync_sum_warps();
+      if (*s_last == 0) continue;
+      __threadfence();
+      for (int i = threadIdx.x; i < nt * kRows; i += 32 * kSumWarps) {
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int64_t c = g0; c <= g1; ++c) sum += __ldcg(part_of(c, c == g0) + i);
+        put_out(p, t0 + i / kRows, out_row + i % kRows, sum);
       }
     }
   }
@@ -730,6 +833,9 @@ static int64_t token_tiles_of(int32_t n_tokens) {
   return ((int64_t)n_tokens + linear::kTileTokens - 1) / linear::kTileTokens;
 }
 
+// CTAs to a token's terms.
+static int64_t slices_of(int32_t n_in) { return ((int64_t)n_in + linear::kTermThreads * 16 - 1) / (linear::kTermThreads * 16); }
+
 // Workspace of a product of more than kFewTokens: the tokens' factors, the counts and
 // parts of the tiles that CTAs share, the terms.
 struct LinearSpace {
@@ -738,7 +844,7 @@ struct LinearSpace {
 static LinearSpace space_of(int32_t T, int32_t n_in, bool e4m3) {
   const int n = tile_columns(T);
   LinearSpace s;
-  s.joined = al256((size_t)T * sizeof(float));
+  s.joined = al256((size_t)T * (e4m3 ? 1 : slices_of(n_in)) * sizeof(float));
   s.parts = s.joined + al256(linear::kStreamCtas * sizeof(int32_t));
   s.terms = s.parts + (size_t)linear::kStreamCtas * 2 * (n / linear::kTerms) * linear::kRows * sizeof(float);
   s.bytes = s.terms + (size_t)token_tiles_of(T) * (size_t)chunks_of(n_in) * linear::terms_bytes(e4m3, n);
@@ -747,7 +853,6 @@ static LinearSpace space_of(int32_t T, int32_t n_in, bool e4m3) {
 
 extern "C" size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in, int32_t format) {
   if (n_tokens <= 0 || check_sizes(1, n_in, format) != CSA2_OK) return 0;
-  if (n_tokens <= linear::kFewTokens) return 256;  // (nothing is kept there)
   return space_of(n_tokens, n_in, format == CSA2_FP4_E4M3).bytes;
 }
 
@@ -759,20 +864,23 @@ static int stages_for(bool e4m3, int n, int acc, int cols, int smem) {
   return most < linear::kMaxStages ? most : linear::kMaxStages;
 }
 
-template <bool kE4M3>
-static int launch_few(linear::Params p, cudaStream_t stream) {
+template <bool kE4M3, bool kOwnTerms, int kCtas>
+static int launch_split(linear::Params p, cudaStream_t stream) {
   using namespace linear;
   static Csa2PerDeviceOnce once;
-  constexpr int kSmem = 113 * 1024;  // two CTAs to an SM
-  if (csa2_smem_optin((const void*)few_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
-  const int64_t tiles = row_tiles_of(p.n_out);
-  p.tmem_cols = 256;
-  p.stages = stages_for(kE4M3, p.n, p.n, 256, kSmem);
+  constexpr int kSmem = 226 / kCtas * 1024, kCols = 512 / kCtas;
+  if (csa2_smem_optin((const void*)split_kernel<kE4M3, kOwnTerms, kCtas>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
+  const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
+  p.tmem_cols = kCols;
+  p.stages = stages_for(kE4M3, p.n, p.n, kCols, kSmem);
   p.split = 1;
-  while (p.split < kMaxSplit && tiles * p.split * 2 <= 304 && p.split * 2 <= p.chunks) p.split *= 2;
-  const int smem = kHeadBytes + 1024 + p.stages * (block_bytes(kE4M3) + terms_bytes(kE4M3, p.n));
-  if (csa2_launch_pdl_cluster(few_kernel<kE4M3>, dim3((unsigned)(tiles * p.split)), dim3(kThreads), (size_t)smem, stream,
-                              (unsigned)p.split, p) != cudaSuccess) {
+  // CTAs for all SMs; two to an SM where each has four chunks and more to itself (a token
+  // by 4,096 x 32,768: 14.8 us with 256 CTAs, 16.0 with 128; by 4,096 x 4,096: 6.2 and 5.7).
+  while (p.split < kMaxSplit && p.split * 2 <= p.chunks &&
+         (tiles * p.split * 2 <= kStreamCtas || (tiles * p.split * 2 <= kCtas * kStreamCtas && p.chunks >= 8 * p.split)))
+    p.split *= 2;
+  if (csa2_launch_pdl_cluster(split_kernel<kE4M3, kOwnTerms, kCtas>, dim3((unsigned)(tiles * p.split)), dim3(kThreads),
+                              (size_t)kSmem, stream, (unsigned)p.split, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return CSA2_ERR_CUDA;
   }
@@ -780,17 +888,8 @@ static int launch_few(linear::Params p, cudaStream_t stream) {
 }
 
 template <bool kE4M3>
-static int launch_stream(linear::Params p, uint8_t* workspace, cudaStream_t stream) {
+static int launch_stream(linear::Params p, cudaStream_t stream) {
   using namespace linear;
-  const LinearSpace space = space_of(p.T, p.n_in, kE4M3);
-  p.factor = (const float*)workspace;
-  p.joined = (int32_t*)(workspace + space.joined);
-  p.parts = (float*)(workspace + space.parts);
-  p.terms = workspace + space.terms;
-  const int64_t slices = ((int64_t)p.n_in + kTermThreads * 8 - 1) / (kTermThreads * 8);
-  TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
-  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
-
   static Csa2PerDeviceOnce once;
   constexpr int kSmem = 226 * 1024;
   if (csa2_smem_optin((const void*)stream_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
@@ -798,13 +897,38 @@ static int launch_stream(linear::Params p, uint8_t* workspace, cudaStream_t stre
   p.tmem_cols = 512;
   p.stages = stages_for(kE4M3, p.n, p.n <= 128 ? 2 * p.n : p.n, 512, kSmem);
   p.units = tiles * p.chunks;
-  static int UN = getenv("UN") ? atoi(getenv("UN")) : 2;
-  int64_t ctas = p.units / UN;
-  if (ctas < tiles) ctas = tiles;
-  if (ctas > kStreamCtas) ctas = kStreamCtas;
-  const int smem = kHeadBytes + 1024 + p.stages * (block_bytes(kE4M3) + terms_bytes(kE4M3, p.n));
-  CSA2_LAUNCH_PDL(stream_kernel<kE4M3>, dim3((unsigned)ctas), dim3(kStreamThreads), (size_t)smem, stream, p);
+  const int64_t ctas = p.units < kStreamCtas ? p.units : kStreamCtas;
+  CSA2_LAUNCH_PDL(stream_kernel<kE4M3>, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, p);
   return CSA2_OK;
+}
+
+template <bool kE4M3>
+static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stream) {
+  using namespace linear;
+  // Up to four tokens (three with E4M3 scales, whose base is a second look at x), and row
+  // tiles for one wave: in one launch (a token by 32,768 x 4,096: 13.9 us, 16.6 with the
+  // terms ahead; four: 15.3 and 16.9; a token by 131,072 x 4,096: 47.2 and 46.6).
+  if (p.T <= (kE4M3 ? kFewTokens - 1 : kFewTokens) && row_tiles_of(p.n_out) <= 2 * kStreamCtas)
+    return launch_split<kE4M3, true, 2>(p, stream);
+  const LinearSpace space = space_of(p.T, p.n_in, kE4M3);
+  p.factor = (const float*)workspace;
+  p.joined = (int32_t*)(workspace + space.joined);
+  p.parts = (float*)(workspace + space.parts);
+  p.terms = workspace + space.terms;
+  const int64_t slices = slices_of(p.n_in);
+  p.factors = kE4M3 ? 1 : (int32_t)slices;
+  TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
+  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
+  // Tiles for half of the SMs and more: in equal runs (32 tokens by 32,768 x 4,096, 256
+  // tiles: 22.1 us, 26.8 as clusters; 16 tokens by 128,259 x 4,096: 48.7 and 54.3). Fewer:
+  // clusters (8 tokens by 4,096 x 32,768, 32 tiles: 20.2 us, 30.1 in runs, whose tiles have
+  // six parts). Of those, two CTAs to an SM only where clusters of four fill them (clusters
+  // of eight at two to an SM do not always fit at once: four tokens by 4,096 x 32,768 with
+  // E4M3 scales took 26 us so, and 19.9 with clusters of four, one CTA to an SM).
+  const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
+  if (tiles > kStreamCtas / 2) return launch_stream<kE4M3>(p, stream);
+  return p.n <= 128 && tiles * 4 > kStreamCtas ? launch_split<kE4M3, false, 2>(p, stream)
+                                               : launch_split<kE4M3, false, 1>(p, stream);
 }
 
 extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8_t* weights, int32_t n_out, int32_t n_in,
@@ -819,7 +943,7 @@ extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8
     return CSA2_ERR_ALIGNMENT;
   // a grid of at most 2^31 - 1 blocks for each kernel
   if (row_tiles_of(n_out) * token_tiles_of(n_tokens) > 0x0FFFFFFFLL ||
-      (int64_t)n_tokens * (((int64_t)n_in + 2047) / 2048) > 0x7FFFFFFFLL)
+      (int64_t)n_tokens * slices_of(n_in) > 0x7FFFFFFFLL)
     return CSA2_ERR_UNSUPPORTED_SHAPE;
   const size_t need = csa2_fp4_linear_workspace_size(n_tokens, n_in, format);
   if (!workspace || workspace_bytes < need || !csa2_aligned(workspace, 256)) return CSA2_ERR_WORKSPACE;
@@ -835,8 +959,6 @@ extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8
   p.chunks = (int32_t)chunks_of(n_in);
   p.token_tiles = (int32_t)token_tiles_of(n_tokens);
   p.n = tile_columns(n_tokens);
-  const bool e4m3 = format == CSA2_FP4_E4M3;
-  cudaStream_t s = (cudaStream_t)stream;
-  if (n_tokens <= linear::kFewTokens) return e4m3 ? launch_few<true>(p, s) : launch_few<false>(p, s);
-  return e4m3 ? launch_stream<true>(p, (uint8_t*)workspace, s) : launch_stream<false>(p, (uint8_t*)workspace, s);
+  return format == CSA2_FP4_E4M3 ? launch_linear<true>(p, (uint8_t*)workspace, (cudaStream_t)stream)
+                                 : launch_linear<false>(p, (uint8_t*)workspace, (cudaStream_t)stream);
 }

@@ -3,12 +3,14 @@ formula in 64 bits.
 
 Tolerance. With A = sum_k |x_k W_k|, and M the same sum with every |x_k| replaced
 by the largest of its block: the eight terms leave out at most 2^-22 M; their
-magnitudes add up to at most 4 A (a value is at least half of its first term, what
-is left after a term at most as large as it); each tensor core product of 64
+magnitudes add up to at most 4 A + M 2^-20 (digits -4 .. 3 in base 8: the first one that
+is not 0 is followed by at most 4/7 of its place, so the value is at least 3/7 of that
+place's unit n units, the sum of all at most n + 4/7, and the rounding to the grid adds
+less than a unit of the last place, 2^-20 of the largest); each tensor core product of 64
 channels and the sum it is added to are taken to be off by 2^-22 of their
 magnitudes (two roundings of fp32), which the ceil(n_in / 64) products of a column
 add up; then nine fp32 operations join the columns and at most nine the parts and
-factors. |error| <= scale * (2^-22 M + (n_in / 64 + 20) 2^-22 4 A). bf16 adds half a
+factors. |error| <= scale * (2^-22 M + (n_in / 64 + 20) 2^-22 (4 A + 2^-20 M)). bf16 adds half a
 step, 2^-9 of the value (2^-8 covers both).
 """
 
@@ -68,7 +70,7 @@ def check(x, data, scale, form, out, out32, factor=1.0):
     ref = factor * (xd @ w.T)
     A = xd.abs() @ w.abs().T
     M = xd.abs().unflatten(-1, (-1, PER[form])).amax(-1).repeat_interleave(PER[form], -1) @ w.abs().T
-    bound = abs(factor) * (2.0 ** -22 * M + (n_in / 64 + 20) * 2.0 ** -22 * 4 * A)
+    bound = abs(factor) * (2.0 ** -22 * M + (n_in / 64 + 20) * 2.0 ** -22 * (4 * A + 2.0 ** -20 * M))
     assert (out32.double() - ref).abs().le(bound).all(), ((out32.double() - ref).abs() / bound.clamp(min=1e-300)).max()
     assert torch.equal(out, out32.bfloat16())
 

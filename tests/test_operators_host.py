@@ -67,7 +67,7 @@ def test_sizes(lib):
     assert size(1 << 20, 1 << 16, 0) > 1 << 32  # past 32 bits
     assert size(1, 31, 0) == size(-1, 32, 0) == size(1, 32, 3) == 0
     ws = lib.csa2_fp4_linear_workspace_size
-    assert 0 < ws(1, 256, 0) <= ws(4, 256, 0) < ws(5, 256, 0) < ws(33, 256, 0) < ws(33, 512, 0)
+    assert 0 < ws(1, 256, 0) <= ws(8, 256, 0) < ws(9, 256, 0) < ws(33, 256, 0) < ws(33, 512, 0)
     assert ws(0, 256, 0) == ws(1, 0, 0) == ws(1, 256, 9) == 0
     assert ws(1 << 16, 1 << 16, 0) > 1 << 32
     beam = lib.csa2_beam_select_workspace_size
