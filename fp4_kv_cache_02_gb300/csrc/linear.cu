@@ -18,6 +18,8 @@
 // of a token are eight columns of the second operand, so the products cost tensor
 // time that a product bound by its weights' bytes has to spare, and no instruction
 // of the CUDA cores per weight.
+#include <cudaTypedefs.h>
+
 #include "tc_common.cuh"
 
 namespace csa2 {
@@ -31,6 +33,7 @@ constexpr int kChunk = 256;                 // inputs to a block of weights: 128
 constexpr int kRows = 128;                  // outputs to a block
 constexpr int kDataBytes = kRows * kChunk / 2;
 constexpr int kTileTokens = 32;             // tokens to a tile: 256 columns
+constexpr int kTermTokens = 64;             // tokens that enter as terms
 constexpr int kFewTokens = 4;               // tokens whose terms the product's own warps make
 constexpr int kMaxSplit = 8;                // CTAs that split the inputs of such a product
 constexpr int kStreamCtas = 152;            // of a product of more tokens: one to an SM
@@ -267,9 +270,9 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_peer(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void sync_sum_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -338,6 +341,26 @@ __device__ __forceinline__ void put_out(const Params& p, int64_t t, int64_t row,
   y *= p.scale;
   if (p.out_bf16) p.out_bf16[t * p.n_out + row] = __float2bfloat16_rn(y);
   if (p.out_f32) p.out_f32[t * p.n_out + row] = y;
+}
+
+// Behind a cluster's barrier: this CTA's share of the tile's sums [nt][128], added in rank
+// order out of the shared memory of the CTAs that have a part of it (a power of two).
+__device__ __forceinline__ void add_parts(const Params& p, const float* sums, int part, int nt, int64_t t0, int64_t row_tile) {
+  const int per = nt * kRows / p.split;
+  for (int i = threadIdx.x * 4; i < per; i += blockDim.x * 4) {
+    const int at = part * per + i;
+    const uint32_t here = tc::smem_u32(sums + at);
+    float4 v[kMaxSplit];
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c)
+      if (c < p.split) v[c] = ld_peer4(peer(here, c));
+    float4 y = v[0];
+#pragma unroll
+    for (int c = 1; c < kMaxSplit; ++c)
+      if (c < p.split) y.x += v[c].x, y.y += v[c].y, y.z += v[c].z, y.w += v[c].w;
+    const int64_t t = t0 + at / kRows, r = row_tile * kRows + at % kRows;
+    put_out(p, t, r, y.x), put_out(p, t, r + 1, y.y), put_out(p, t, r + 2, y.z), put_out(p, t, r + 3, y.w);
+  }
 }
 
 // ---- few tiles -------------------------------------------------------------------
@@ -531,18 +554,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
   __syncthreads();
   if (p.split > 1) {
     cluster_sync();
-    const int per = nt * kRows / p.split;  // (split is a power of two)
-    for (int i = threadIdx.x; i < per; i += kThreads) {
-      const int at = part * per + i;
-      const uint32_t here = tc::smem_u32(sums + at);
-      float v[kMaxSplit];
-#pragma unroll
-      for (int c = 0; c < kMaxSplit; ++c) v[c] = c < p.split ? ld_peer(peer(here, c)) : 0.0f;
-      float y = v[0];
-#pragma unroll
-      for (int c = 1; c < kMaxSplit; ++c) y += v[c];
-      put_out(p, t0 + at / kRows, row_tile * kRows + at % kRows, y);
-    }
+    add_parts(p, sums, part, nt, t0, row_tile);
     cluster_sync();  // the peers have read this CTA's sums
   }
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, p.tmem_cols);
@@ -789,6 +801,242 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
   if (warp == kSumWarps + 1) tc::tmem_dealloc(tmem, p.tmem_cols);
 }
 
+// ---- many tokens -----------------------------------------------------------------
+// More than 64 tokens: the weights' values are exact in bf16 (two bits, or with an E4M3
+// scale six), so they are made on the way and multiplied by x as it is, 128 outputs x up
+// to 256 tokens a CTA. A token's eight columns take 1/32 of an FP4 block's time of 880
+// cycles (with E4M3 scales), its one bf16 column 1/256 of 2,150, and the values' making
+// 2,000: 96 tokens by 4,096 x 4,096 take 11.8 us, 15.6 as terms, 64 tokens 11.3 and 10.6.
+//   warp 16    producer of blocks of weights;
+//   warp 17    products, A from tensor memory: in shared memory the weights' values would
+//              be written and read beside x, more than its 128 bytes a cycle;
+//   warp 18    producer of 64 channels of the tile's tokens at a time, by a tensor map
+//              (zeros past the last token and channel);
+//   warps 0-15 the values of 64 inputs of a row to a thread, four sets of four warps in
+//              turn (with two sets their making held the products up: 33 us for 1,021
+//              tokens by 4,096 x 4,096, 26 with four); then the accumulator, stored or (clusters that split the inputs)
+//              added in rank order out of one another's shared memory.
+constexpr int kWideTokens = 256;
+constexpr int kSub = 64;             // inputs of a step: 128 bytes of a token, 32 columns of A
+constexpr int kRawStages = 3;
+constexpr int kMaxXStages = 16;      // as many as fit: a trip to L2 is about five steps of 256 tokens
+constexpr int kSlots = 8;            // steps of A in tensor memory, behind 256 accumulator columns
+constexpr int kSets = 4;             // of four warps
+constexpr int kWideThreads = 32 * (4 * kSets + 3);
+
+struct WideParams {
+  Params p;
+  int32_t tokens;  // of a tile, a multiple of 16
+  int32_t x_bytes, x_stages;
+};
+
+// Eight E2M1 codes to bf16, times a scale: the bytes of the magnitudes are looked up
+// (0, 1/2 .. 6: high 00 3F 3F 3F 40 40 40 40, low 00 00 80 C0 00 40 80 C0), the signs put
+// to the high ones, and both interleaved.
+__device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, __nv_bfloat162 scale, uint32_t* out) {
+  const uint32_t m = w & 0x77777777u;
+  const uint32_t even = (w << 4) & 0x80808080u, odd = w & 0x80808080u;
+  const uint32_t h0 = __byte_perm(0x3F3F3F00u, 0x40404040u, m) | __byte_perm(even, odd, 0x5140);
+  const uint32_t h1 = __byte_perm(0x3F3F3F00u, 0x40404040u, m >> 16) | __byte_perm(even, odd, 0x7362);
+  const uint32_t l0 = __byte_perm(0xC0800000u, 0xC0804000u, m), l1 = __byte_perm(0xC0800000u, 0xC0804000u, m >> 16);
+  const uint32_t v[4] = {__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
+                         __byte_perm(l1, h1, 0x7362)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]), scale);
+    out[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+template <bool kE4M3>
+__global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_constant__ CUtensorMap x_map, WideParams wp) {
+  const Params& p = wp.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint64_t* full_w = reinterpret_cast<uint64_t*>(smem_raw);
+  uint64_t* empty_w = full_w + kRawStages;
+  uint64_t* full_x = empty_w + kRawStages;
+  uint64_t* empty_x = full_x + kMaxXStages;
+  uint64_t* full_a = empty_x + kMaxXStages;
+  uint64_t* empty_a = full_a + kSlots;
+  uint64_t* acc_full = empty_a + kSlots;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  uint8_t* s_x = ring_of(smem_raw);
+  uint8_t* s_w = s_x + wp.x_stages * wp.x_bytes;
+  const int n_x = wp.x_stages;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = (int)(blockIdx.x % (uint32_t)p.split);
+  const int64_t tile = blockIdx.x / (uint32_t)p.split;
+  const int32_t t0 = (int32_t)(tile % p.token_tiles) * wp.tokens;
+  const int64_t row_tile = tile / p.token_tiles;
+  const int nt = min(p.T - t0, wp.tokens);
+  const int32_t c0 = (int32_t)((int64_t)p.chunks * part / p.split);
+  const int32_t c1 = (int32_t)((int64_t)p.chunks * (part + 1) / p.split);
+  const int steps = min((c1 - c0) * (kChunk / kSub), (p.n_in - c0 * kChunk + kSub - 1) / kSub);
+  constexpr int kOfChunk = kChunk / kSub;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRawStages; ++s) {
+      tc::mbar_init(&full_w[s], 1);
+      tc::mbar_init(&empty_w[s], kOfChunk * 4);  // each step's four warps
+    }
+    for (int s = 0; s < n_x; ++s) {
+      tc::mbar_init(&full_x[s], 1);
+      tc::mbar_init(&empty_x[s], 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      tc::mbar_init(&full_a[s], 4);
+      tc::mbar_init(&empty_a[s], 1);
+    }
+    tc::mbar_init(acc_full, 1);
+    *s_abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 4 * kSets + 1) tc::tmem_alloc(s_tmem, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem, a_cols = tmem + kWideTokens;
+
+  if (warp == 4 * kSets) {
+    if (lane == 0) {
+      const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
+      const int n_raw = (steps + kOfChunk - 1) / kOfChunk;
+      int i = 0;
+      for (; i < n_raw; ++i) {
+        const int s = i % kRawStages;
+        if (!tc::mbar_wait_bounded(&empty_w[s], ((uint32_t)(i / kRawStages) & 1u) ^ 1u, s_abort, &g_linear_error)) break;
+        tc::mbar_arrive_expect_tx(&full_w[s], block_bytes(kE4M3));
+        tc::bulk_load(s_w + s * block_bytes(kE4M3), from + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full_w[s]);
+      }
+      // copies land before the CTA's memory goes away
+      for (int l = max(0, i - kRawStages); l < i; ++l) tc::mbar_wait_issued(&full_w[l % kRawStages], (uint32_t)(l / kRawStages));
+    }
+    __syncwarp();
+  } else if (warp == 4 * kSets + 2) {
+    if (lane == 0) {
+      pdl_wait();
+      int j = 0, s = 0;
+      uint32_t turn = 1;
+      for (; j < steps; ++j) {
+        if (!tc::mbar_wait_bounded(&empty_x[s], turn, s_abort, &g_linear_error)) break;
+        tc::mbar_arrive_expect_tx(&full_x[s], (uint32_t)wp.x_bytes);
+        tc::tma_load_2d(s_x + s * wp.x_bytes, &x_map, c0 * kChunk + j * kSub, t0, &full_x[s]);
+        if (++s == n_x) s = 0, turn ^= 1u;
+      }
+      for (int l = max(0, j - n_x); l < j; ++l) tc::mbar_wait_issued(&full_x[l % n_x], (uint32_t)(l / n_x));
+    }
+    __syncwarp();
+  } else if (warp == 4 * kSets + 1) {
+    const uint32_t one = tc::elect_one();
+    const uint32_t idesc = tc::idesc_bf16(128, wp.tokens, 0, 0), x_at = tc::smem_u32(s_x);
+    // (places in the rings carried along: a division by the number of stages is longer
+    // than a step's products)
+    int s = 0;
+    uint32_t turn = 0;
+    for (int j = 0; j < steps; ++j) {
+      const int a = j % kSlots;
+      const bool ok = tc::mbar_wait_bounded(&full_x[s], turn, s_abort, &g_linear_error) &&
+                      tc::mbar_wait_bounded(&full_a[a], (uint32_t)(j / kSlots) & 1u, s_abort, &g_linear_error);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc::tc_fence_after();
+      const uint32_t at = x_at + (uint32_t)(s * wp.x_bytes);
+#pragma unroll
+      for (int m = 0; m < kSub / 16; ++m)
+        tc::mma_f16_ta_one(one, tmem, a_cols + (uint32_t)(a * (kSub / 2) + m * 8),
+                           tc::smem_desc(at + 32 * m, 0, 1024, tc::kSwizzle128B), idesc, (j | m) != 0);
+      tc::mma_commit_one(one, &empty_x[s]);
+      tc::mma_commit_one(one, &empty_a[a]);
+      if (++s == n_x) s = 0, turn ^= 1u;
+    }
+    // whatever was issued ends before tensor memory is freed
+    tc::mma_commit_one(one, acc_full);
+    tc::mbar_wait_issued(acc_full, 0);
+    __syncwarp();
+  } else {
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    for (int j = warp >> 2; j < steps; j += kSets) {
+      const int raw = j / kOfChunk, q = j % kOfChunk, a = j % kSlots;
+      const bool ok = tc::mbar_wait_bounded(&full_w[raw % kRawStages], (uint32_t)(raw / kRawStages) & 1u, s_abort, &g_linear_error) &&
+                      tc::mbar_wait_bounded(&empty_a[a], ((uint32_t)(j / kSlots) & 1u) ^ 1u, s_abort, &g_linear_error);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* block = s_w + (raw % kRawStages) * block_bytes(kE4M3);
+      const uint8_t* sf = block + kDataBytes + scale_place(row);
+      __nv_bfloat162 scales[4];  // of each sixteen inputs
+      if (kE4M3) {
+        // an E4M3 byte at a bf16's exponent and first bits is its value times 2^-120
+        const uint32_t four = *reinterpret_cast<const uint32_t*>(sf + q * group_bytes());
+        const __nv_bfloat162 up = __float2bfloat162_rn(__uint_as_float((120u + 127u) << 23));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t two = (four >> (16 * i) & 0x7Fu) << 4 | (four >> (16 * i + 8) & 0x7Fu) << 20;
+          const __nv_bfloat162 f = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&two), up);
+          scales[2 * i] = __low2bfloat162(f);
+          scales[2 * i + 1] = __high2bfloat162(f);
+        }
+      } else {
+        const uint32_t two = *reinterpret_cast<const uint16_t*>(sf + (q / 2) * group_bytes() + (q % 2) * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t e = two >> (8 * i) & 0xFFu;  // (0: 2^-127, a subnormal; 255: NaN)
+          const uint32_t bits = (e << 7 | (((e + 1) & 0xFFu) < 2 ? 0x40u : 0u)) * 0x10001u;
+          scales[2 * i] = scales[2 * i + 1] = *reinterpret_cast<const __nv_bfloat162*>(&bits);
+        }
+      }
+      uint32_t v[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 c = *reinterpret_cast<const uint4*>(block + tc::sw128_offset(row, 2 * q + h));
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        const __nv_bfloat162* scale = scales + 2 * h;  // of the first and second sixteen
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e2m1x8_to_bf16(w[i], scale[i / 2], v + 16 * h + 4 * i);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty_w[raw % kRawStages]);
+      tc::tc_fence_after();
+      tc::tmem_st_32x32b_x32(a_cols + lanes + (uint32_t)(a * (kSub / 2)), v);
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&full_a[a]);
+    }
+    pdl_wait();  // (the outputs may have readers before this call)
+  }
+
+  float* sums = reinterpret_cast<float*>(s_x);  // [nt][128], once the rings are done with
+  if (warp < 4 * kSets) {
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(acc_full, 0, s_abort, &g_linear_error));
+    const int row = (warp & 3) * 32 + lane;
+    if (ok) {
+      tc::tc_fence_after();
+      for (int t = (warp >> 2) * 16; t < nt; t += 16 * kSets) {
+        uint32_t v[16];
+        tc::tmem_ld_32x32b_x16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)t, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (t + i >= nt) break;
+          if (p.split > 1)
+            sums[(t + i) * kRows + row] = __uint_as_float(v[i]);
+          else
+            put_out(p, t0 + t + i, row_tile * kRows + row, __uint_as_float(v[i]));
+        }
+      }
+      tc::tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (p.split > 1) {
+    cluster_sync();
+    add_parts(p, sums, part, nt, t0, row_tile);
+    cluster_sync();  // the peers have read this CTA's sums
+  }
+  if (warp == 4 * kSets + 1) tc::tmem_dealloc(tmem, 512);
+}
+
 }  // namespace linear
 }  // namespace csa2
 
@@ -866,8 +1114,12 @@ static LinearSpace space_of(int32_t T, int32_t n_in, bool e4m3) {
   return s;
 }
 
+// Whether the weights' values are made (a tensor map's box of 64 channels wants as many).
+static bool is_wide(int32_t T, int32_t n_in) { return T > linear::kTermTokens && n_in >= linear::kSub; }
+
 extern "C" size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in, int32_t format) {
   if (n_tokens <= 0 || check_sizes(1, n_in, format) != CSA2_OK) return 0;
+  if (is_wide(n_tokens, n_in)) return 256;  // (nothing is kept there)
   return space_of(n_tokens, n_in, format == CSA2_FP4_E4M3).bytes;
 }
 
@@ -917,6 +1169,51 @@ static int launch_stream(linear::Params p, cudaStream_t stream) {
   return CSA2_OK;
 }
 
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+template <bool kE4M3>
+static int launch_wide(linear::Params p, cudaStream_t stream) {
+  using namespace linear;
+  static Csa2PerDeviceOnce once;
+  constexpr int kSmem = 227 * 1024, kRoom = kSmem - kHeadBytes - 1024 - kRawStages * block_bytes(kE4M3);
+  if (csa2_smem_optin((const void*)wide_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
+  auto encode = tensor_map_encoder();
+  if (!encode) return CSA2_ERR_CUDA;
+  // equal tiles
+  p.token_tiles = (p.T + kWideTokens - 1) / kWideTokens;
+  WideParams wp{p, ((p.T + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16};
+  wp.x_bytes = wp.tokens * kSub * 2;
+  wp.x_stages = kRoom / wp.x_bytes < kMaxXStages ? kRoom / wp.x_bytes : kMaxXStages;
+  CUtensorMap map;
+  cuuint64_t dims[2] = {(cuuint64_t)p.n_in, (cuuint64_t)p.T};
+  cuuint64_t strides[1] = {(cuuint64_t)p.n_in * 2};
+  cuuint32_t box[2] = {(cuuint32_t)kSub, (cuuint32_t)wp.tokens};
+  cuuint32_t estr[2] = {1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)p.x, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return CSA2_ERR_CUDA;
+  const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
+  int split = 1;
+  while (split < kMaxSplit && split * 2 <= p.chunks && tiles * split * 2 <= kStreamCtas) split *= 2;
+  wp.p.split = split;
+  if (csa2_launch_pdl_cluster(wide_kernel<kE4M3>, dim3((unsigned)(tiles * split)), dim3(kWideThreads), (size_t)kSmem, stream,
+                              (unsigned)split, map, wp) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return CSA2_ERR_CUDA;
+  }
+  return CSA2_OK;
+}
+
 template <bool kE4M3>
 static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stream) {
   using namespace linear;
@@ -925,6 +1222,7 @@ static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stre
   // terms ahead; four: 15.3 and 16.9; a token by 131,072 x 4,096: 47.2 and 46.6).
   if (p.T <= (kE4M3 ? kFewTokens - 1 : kFewTokens) && row_tiles_of(p.n_out) <= 2 * kStreamCtas)
     return launch_split<kE4M3, true, 2>(p, stream);
+  if (is_wide(p.T, p.n_in)) return launch_wide<kE4M3>(p, stream);
   const LinearSpace space = space_of(p.T, p.n_in, kE4M3);
   p.factor = (const float*)workspace;
   p.joined = (int32_t*)(workspace + space.joined);

@@ -76,7 +76,9 @@ def check(x, data, scale, form, out, out32, factor=1.0):
 
 
 SHAPES = [(1, 32, 1), (1, 64, 128), (2, 256, 129), (3, 288, 257), (4, 4096, 640), (5, 992, 77), (8, 1024, 300), (9, 2048, 130),
-          (16, 512, 1000), (17, 800, 131), (31, 96, 640), (32, 4096, 384), (33, 1056, 200), (64, 256, 513), (100, 2080, 70),
+          (16, 512, 1000), (17, 800, 131), (33, 32, 70), (33, 64, 70), (49, 2336, 600), (257, 320, 200), (300, 1024, 129),
+          (1021, 288, 300), (65, 64, 70), (70, 32, 129), (50, 288, 10000), (17, 512, 12000), (9, 2336, 9900), (1, 96, 40000),
+          (3, 320, 39001), (16, 2048, 10000), (128, 512, 20000), (31, 96, 640), (32, 4096, 384), (33, 1056, 200), (64, 256, 513), (100, 2080, 70),
           (1, 32768, 130), (40, 8192, 1)]
 
 
@@ -153,23 +155,25 @@ def test_rows_of_all_sizes(csa2, form, power):
 
 
 @pytest.mark.parametrize("form", PER)
-def test_zero_rows_and_rows_that_are_not_finite(csa2, form):
-    T, n_in, n_out = 35, 320, 150
+@pytest.mark.parametrize("T", [68, 34, 3, 20])
+def test_zero_rows_and_rows_that_are_not_finite(csa2, form, T):
+    n_in, n_out = 320, 150
     g = gen(3)
     x = torch.randn(T, n_in, generator=g, device="cuda").bfloat16()
     data, scale = packed(g, n_out, n_in, form)
     _, base = call(csa2, x, data, scale, form)
     bad = x.clone()
-    bad[2] = 0.0
-    bad[5, 17] = float("inf")
-    bad[9, 0] = float("nan")
-    bad[33, 319] = float("-inf")
+    bad[1] = 0.0
+    lines = [0, T // 2 + 1, T - 1]
+    bad[lines[0], 17] = float("inf")
+    bad[lines[1], 0] = float("nan")
+    bad[lines[2], 319] = float("-inf")
     out, out32 = call(csa2, bad, data, scale, form)
     wrong = torch.zeros(T, dtype=torch.bool, device="cuda")
-    wrong[[5, 9, 33]] = True
-    assert out32[wrong].isnan().all() and out[wrong].isnan().all()
-    assert (out32[2] == 0).all()
-    wrong[2] = True
+    wrong[lines] = True
+    assert not out32[wrong].isfinite().any() and not out[wrong].isfinite().any()
+    assert (out32[1] == 0).all()
+    wrong[1] = True
     assert torch.equal(out32[~wrong], base[~wrong])
 
 

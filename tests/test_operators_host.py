@@ -67,9 +67,9 @@ def test_sizes(lib):
     assert size(1 << 20, 1 << 16, 0) > 1 << 32  # past 32 bits
     assert size(1, 31, 0) == size(-1, 32, 0) == size(1, 32, 3) == 0
     ws = lib.csa2_fp4_linear_workspace_size
-    assert 0 < ws(1, 256, 0) <= ws(8, 256, 0) < ws(9, 256, 0) < ws(33, 256, 0) < ws(33, 512, 0)
+    assert 0 < ws(1, 256, 0) < ws(9, 256, 0) < ws(32, 256, 0) < ws(32, 512, 0) < ws(64, 512, 0) and ws(65, 256, 0) > 0 and ws(65, 32, 0) > ws(64, 32, 0)
     assert ws(0, 256, 0) == ws(1, 0, 0) == ws(1, 256, 9) == 0
-    assert ws(1 << 16, 1 << 16, 0) > 1 << 32
+    assert ws(1 << 27, 32, 0) > 1 << 32
     beam = lib.csa2_beam_select_workspace_size
     assert 0 < beam(1, 1, 10, 64) < beam(1, 1, 100000, 64) and beam(1, 1, 100000, 1) < beam(1, 1, 100000, 64)
     assert beam(0, 1, 10, 1) == beam(1, 0, 10, 1) == beam(1, 1, 10, 0) == beam(1, 1, 10, 65) == 0
