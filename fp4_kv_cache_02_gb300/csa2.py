@@ -13,6 +13,7 @@ torch (device memory plumbing) and call the same entry points.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -688,7 +689,8 @@ def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None,
         raise ValueError("x must be [n_tokens, n_in], out or out_f32 [n_tokens, n_out]")
     (n, n_in), n_out = x.shape, to.shape[1]
     kind = _format(format)
-    if weights.numel() < _lib.csa2_fp4_weights_size(n_out, n_in, kind):
+    # (csa2_fp4_weights_size without a call: blocks of 128 x 256 weights)
+    if weights.numel() < (n_out + 127) // 128 * ((n_in + 255) // 256) * (18432 if kind else 17408):
         raise ValueError(f"weights holds fewer than {n_out} x {n_in} weights")
     _call("csa2_fp4_linear", x_at, n, w_at, n_out, n_in, kind, float(scale),
           _optional(out, torch.bfloat16, (n, n_out), "out", dev), _optional(out_f32, torch.float32, (n, n_out), "out_f32", dev),
@@ -734,25 +736,22 @@ def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_o
     if parents.dim() != 1:
         raise ValueError("parents must be [R]")
     R = parents.shape[0]
-    at, pool = [], None
-    for t, width, name in ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"),
-                           (ik_scale, 4, "ik_scale")):
-        if t is None:
-            at.append(None)
-            continue
-        at.append(_take(t, torch.uint8, name, dev))
-        shape = t.shape if t.dim() == 4 else (1, *t.shape)
-        if len(shape) != 4 or (pool is not None and pool != shape[:3]) or shape[3] != width:
-            raise ValueError(f"{name} must be [layers, n_pages, page_size, {width}] like the other planes")
-        pool = tuple(shape[:3])
-    if pool is None or (kv_data is None) != (kv_scale is None) or (ik_data is None) != (ik_scale is None):
+    first = kv_data if kv_data is not None else ik_data
+    if first is None or (kv_data is None) != (kv_scale is None) or (ik_data is None) != (ik_scale is None):
         raise ValueError("codes and scales of the latents, of the keys, or of both are required")
+    pool = first.shape[:-1]
+    if not 2 <= len(pool) <= 3:
+        raise ValueError("planes must be [n_pages, page_size, width] or [layers, n_pages, page_size, width]")
+    at = [_optional(t, torch.uint8, (*pool, width), name, dev)
+          for t, width, name in ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"),
+                                 (ik_scale, 4, "ik_scale"))]
+    layers, n_pages, page = pool if len(pool) == 3 else (1, *pool)
     table = _take(page_table, torch.int32, "page_table", dev)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [rows, max_pages]")
     rows, max_pages = page_table.shape
     _call("csa2_paged_reorder", _shaped(parents, torch.int32, (R,), "parents", dev),
-          _shaped(fresh_pages, torch.int32, (R,), "fresh_pages", dev), R, *at, pool[0], pool[1], pool[2], table, rows,
+          _shaped(fresh_pages, torch.int32, (R,), "fresh_pages", dev), R, *at, layers, n_pages, page, table, rows,
           max_pages, _shaped(n_visible, torch.int32, (rows,), "n_visible", dev),
           _shaped(page_table_out, torch.int32, (R, max_pages), "page_table_out", dev),
           _shaped(n_visible_out, torch.int32, (R,), "n_visible_out", dev), _s(stream))
@@ -765,9 +764,7 @@ def csa2_reorder_rows(src, parents, dst, stream=None):
     src_at, dst_at = _take(src, src.dtype, "src", dev), _take(dst, src.dtype, "dst", dev)
     if src.dim() < 1 or dst.dim() != src.dim() or dst.shape[1:] != src.shape[1:]:
         raise ValueError("src must be [rows, ...] and dst [R, ...] with rows alike")
-    size = src.element_size()
-    for n in src.shape[1:]:
-        size *= n
+    size = src.element_size() * math.prod(src.shape[1:])
     R = dst.shape[0]
     _call("csa2_reorder_rows", src_at, src.shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R, dst_at,
           _s(stream))

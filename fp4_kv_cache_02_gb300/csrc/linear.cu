@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* ready = empty + kMaxStages;  // kOwnTerms: the stage's terms are there
+  uint64_t* acc_full = ready + kMaxStages;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   uint32_t* s_top = s_tmem + 2;  // [warp][token]: the largest channel that the warp has seen
@@ -399,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      tc::mbar_init(&full[s], kOwnTerms ? 1 + p.T : 1);
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&ready[s], p.T);
       tc::mbar_init(&empty[s], 1);
     }
     tc::mbar_init(acc_full, 1);
@@ -445,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
     const uint32_t ring_at = tc::smem_u32(ring), idesc = idesc_of<kE4M3>(p.n);
     for (int done = 0; done < n_chunks; ++done) {
       const int s = done % p.stages;
-      const bool ok = tc::mbar_wait_bounded(&full[s], (uint32_t)(done / p.stages) & 1u, s_abort, &g_linear_error);
+      const uint32_t phase = (uint32_t)(done / p.stages) & 1u;
+      bool ok = tc::mbar_wait_bounded(&full[s], phase, s_abort, &g_linear_error);
+      if (kOwnTerms) ok = ok && tc::mbar_wait_bounded(&ready[s], phase, s_abort, &g_linear_error);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::tc_fence_after();
       const uint32_t a_at = ring_at + (uint32_t)(s * stage_bytes);
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
       put_terms<kE4M3>(v, base_exp<kE4M3>(whole), t, data, data + p.n * (kChunk / 2), 1, lane);
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&full[s]);
+      if (lane == 0) tc::mbar_arrive(&ready[s]);
     }
     if (!kE4M3) share_tops();
   }
