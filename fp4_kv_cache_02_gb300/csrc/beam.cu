@@ -62,6 +62,25 @@ __device__ __forceinline__ uint64_t bound_of_block(uint64_t key, int k, uint64_t
   return *s_bound;
 }
 
+// The same from each warp's own values in turn: the smallest of the warps' ceil(k / 8)-th
+// largest ones, as score_key (0: there is none). Weaker, but a fifth of the time: enough
+// for the first tile, whose list is cut soon. It does not tell equal values apart.
+__device__ __forceinline__ uint32_t bound_of_warps(float top, int k, uint32_t* s_warps) {
+  uint32_t key = top > -INFINITY ? score_key(top) : 0u, best = 0;
+  const int rounds = (k + kThreads / 32 - 1) / (kThreads / 32);
+  for (int i = 0; i < rounds; ++i) {
+    best = __reduce_max_sync(0xffffffffu, key);
+    const uint32_t who = __ballot_sync(0xffffffffu, key == best);
+    if ((threadIdx.x & 31) == __ffs(who) - 1) key = 0;
+  }
+  if ((threadIdx.x & 31) == 0) s_warps[threadIdx.x >> 5] = best;
+  __syncthreads();
+  best = s_warps[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) best = min(best, s_warps[i]);
+  return best;
+}
+
 // Two fp32 operations at once (the values come in pairs of registers).
 __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
   asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
@@ -132,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(RowArgs<T> a) {
   __shared__ __align__(16) uint64_t s_keys[kThreads / 2];
   __shared__ uint64_t s_kth;
   __shared__ int s_added[3], s_left;
+  __shared__ uint32_t s_warps[kThreads / 32];
   __shared__ Part s_part[kThreads / 32];
   pdl_begin();
   const int32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
@@ -233,13 +253,20 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(RowArgs<T> a) {
         }
       }
     };
-    if (!first) push();
+    if (first) {
+      const uint32_t least = bound_of_warps(top, k, s_warps);
+      if (least) {
+        bound = (uint64_t)least << 32;
+        bound_value = key_value(bound);
+      }
+    }
+    push();
     __syncthreads();
     int added = s_added[turn];
     // the tile's before this one: everyone has read it, and it is added to again behind
     // the next barrier. So a tile has one barrier, and the list is not read before it.
     if (threadIdx.x == 0) s_added[turn == 0 ? 2 : turn - 1] = 0;
-    if (first || n + added > kRoom) {
+    if (n + added > kRoom) {
       int at = 0;
 #pragma unroll
       for (int i = kX - 1; i > 0; --i)
@@ -329,62 +356,80 @@ struct JoinArgs {
   float* lse;
 };
 
-struct Best {
-  uint64_t score;  // order-preserving bits of the double; 0: none
-  uint64_t place;  // ~(w << 32 | token)
-};
-__device__ __forceinline__ bool above(uint64_t a, uint64_t b) { return a > b; }
-__device__ __forceinline__ bool above(const Best& a, const Best& b) {
-  return a.score > b.score || (a.score == b.score && a.place > b.place);
-}
-__device__ __forceinline__ uint64_t order(double v) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  return b >> 63 ? ~b : b | 0x8000000000000000ull;
-}
-__device__ __forceinline__ double order_value(uint64_t b) {
-  return __longlong_as_double((long long)(b >> 63 ? b & 0x7FFFFFFFFFFFFFFFull : ~b));
-}
-
-// Joins `lists` lists (each of 2^shift falling entries, one after another, all entries
-// different) in fours or pairs until `left` are left. An entry's rank is its place in its
-// own list and, by bisection, those of the others: one thread an entry, the bisections
-// side by side. x holds the lists and y half as many; returns where the last ones are.
-template <int kWays, typename E>
-__device__ __forceinline__ void join_round(const E* x, E* y, int lists, int shift) {
+// Joins `lists` lists (each of 2^shift falling keys, one after another) in fours or pairs
+// until `left` are left; of equal keys those of the lower list come first. A key's rank is
+// its place in its own list and, by bisection, those in the others: one thread a key, the
+// bisections side by side. x holds the lists and y half as many, xp and yp (kPlaces) what
+// goes with the keys; returns where the last ones are.
+template <int kWays, bool kPlaces>
+__device__ __forceinline__ void join_round(const uint64_t* x, uint64_t* y, const uint64_t* xp, uint64_t* yp, int lists, int shift) {
   const int size = 1 << shift;
   for (int i = threadIdx.x; i < lists << shift; i += kJoinThreads) {
-    const E e = x[i];
+    const uint64_t e = x[i];
     const int l = i >> shift, l0 = l & ~(kWays - 1);
     int pos[kWays - 1] = {};
-    const E* other[kWays - 1];
+    const uint64_t* other[kWays - 1];
+    uint64_t least[kWays - 1];  // keys from here on come before e
 #pragma unroll
-    for (int o = 0; o < kWays - 1; ++o) other[o] = x + ((l0 + ((l + 1 + o) & (kWays - 1))) << shift);
+    for (int o = 0; o < kWays - 1; ++o) {
+      const int m = l0 + ((l + 1 + o) & (kWays - 1));
+      other[o] = x + (m << shift);
+      least[o] = e + (m > l ? 1 : 0);
+    }
     for (int s = size / 2; s; s /= 2) {
 #pragma unroll
       for (int o = 0; o < kWays - 1; ++o)
-        if (above(other[o][pos[o] + s - 1], e)) pos[o] += s;
+        if (other[o][pos[o] + s - 1] >= least[o]) pos[o] += s;
     }
     int rank = i & (size - 1);
 #pragma unroll
-    for (int o = 0; o < kWays - 1; ++o) rank += pos[o] + (above(other[o][pos[o]], e) ? 1 : 0);
-    if (rank < size) y[((l / kWays) << shift) + rank] = e;
+    for (int o = 0; o < kWays - 1; ++o) rank += pos[o] + (other[o][pos[o]] >= least[o] ? 1 : 0);
+    if (rank < size) {
+      const int at = ((l / kWays) << shift) + rank;
+      y[at] = e;
+      if (kPlaces) yp[at] = xp[i];
+    }
   }
   __syncthreads();
 }
-template <typename E>
-__device__ __forceinline__ const E* join_lists(E* x, E* y, int lists, int left, int shift) {
+struct Lists {
+  const uint64_t *keys, *places;
+};
+template <bool kPlaces>
+__device__ __forceinline__ Lists join_lists(uint64_t* x, uint64_t* y, uint64_t* xp, uint64_t* yp, int lists, int left, int shift) {
   while (lists > left) {
     const bool four = lists >= 4 * left;
     if (four)
-      join_round<4>(x, y, lists, shift);
+      join_round<4, kPlaces>(x, y, xp, yp, lists, shift);
     else
-      join_round<2>(x, y, lists, shift);
+      join_round<2, kPlaces>(x, y, xp, yp, lists, shift);
     lists /= four ? 4 : 2;
-    E* t = x;
+    uint64_t* t = x;
     x = y;
     y = t;
+    t = xp;
+    xp = yp;
+    yp = t;
   }
-  return x;
+  return {x, xp};
+}
+
+// score + (x - lse) as the sum of two fp32 values, the first its rounding: 48 bits, by
+// exact sums of two (Knuth), where a 64-bit operation takes the time of 64 of these. Key:
+// larger for a larger sum. (x - lse first: the lowest value of fp32 less itself leaves the
+// score.)
+__device__ __forceinline__ float two_sum(float a, float b, float& e) {
+  const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
+  return s;
+}
+__device__ __forceinline__ uint64_t sum_key(float score, float x, float lse, float lse_rest) {
+  float e, f, g;
+  const float d = two_sum(x, -lse, e);
+  const float t = two_sum(d, score, f);
+  float sum = two_sum(t, __fadd_rn(__fsub_rn(e, lse_rest), f), g);
+  if (!(fabsf(sum) <= FLT_MAX)) sum = -FLT_MAX, g = 0.0f;  // (a score below fp32's range)
+  return (uint64_t)score_key(__fadd_rn(sum, 0.0f)) << 32 | score_key(__fadd_rn(g, 0.0f));
 }
 
 // Powers of two: a list's entries, a sequence's rows.
@@ -395,36 +440,35 @@ __host__ __device__ constexpr int power_shift(int n) {
 }
 __host__ __device__ constexpr int join_bytes(int W, int parts, int k) {
   const int k2 = 1 << power_shift(k), rows2 = 1 << power_shift(W);
-  return 3 * W * parts * k2 / 2 * (int)sizeof(uint64_t) + 3 * rows2 * k2 / 2 * (int)sizeof(Best) + 64;
+  return (3 * W * parts * k2 + 2 * 3 * rows2 * k2) / 2 * (int)sizeof(uint64_t) + 64;
 }
 // (the parts' entries are at most kMaxEntries, or the rows' where each has one part)
-constexpr int kMaxJoinBytes = 3 * kMaxEntries / 2 * (int)sizeof(uint64_t) + 3 * CSA2_MAX_BEAMS * kMaxK / 2 * (int)sizeof(Best) + 64;
+constexpr int kMaxJoinBytes = 3 * (kMaxEntries / 2 + CSA2_MAX_BEAMS * kMaxK) * (int)sizeof(uint64_t) + 64;
 static_assert(CSA2_MAX_BEAMS * kMaxK <= kMaxEntries && kMaxJoinBytes <= 226 * 1024, "lists too long");
 
-// One CTA to a sequence: each row's lists are joined by value, the rows' lists by
-// score. Scores are held in 64 bits, so that their order is that of the formula to
-// what the sums carry (about 2^-22): in 32 bits x - lse would be rounded to 2^-20 for
-// logits about 16. The time does not depend on the values.
+// One CTA to a sequence: each row's lists are joined by value, the rows' lists by score,
+// held to 48 bits so that their order is that of the formula to what the sums carry (in
+// 32 bits x - lse would be rounded to 2^-20 for logits about 16). The time does not depend
+// on the values.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a) {
   pdl_wait();
-  extern __shared__ Best s_best[];  // the rows' lists and half as many, then the parts'
-  __shared__ double s_lse[CSA2_MAX_BEAMS];  // NaN: the row takes no part
-  __shared__ double s_score[CSA2_MAX_BEAMS];
+  extern __shared__ uint64_t s_lists[];  // the rows' keys and half as many, their places, the parts' keys
+  __shared__ float s_lse[2][CSA2_MAX_BEAMS];  // two summands; NaN: the row takes no part
+  __shared__ float s_score[CSA2_MAX_BEAMS];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const int k = a.k;
   const int64_t row0 = (int64_t)b * a.W;
   const int shift = a.k_shift, mask = (1 << shift) - 1;
   const int rows2 = 1 << a.row_shift;
-  Best* x = s_best;
-  Best* y = x + (rows2 << shift);
-  uint64_t* keys = reinterpret_cast<uint64_t*>(y + (rows2 << shift) / 2 + 1);
+  const int size = rows2 << shift, half = size / 2 + 1;
+  uint64_t* x = s_lists;
+  uint64_t* y = x + size;
+  uint64_t* xp = y + half;
+  uint64_t* yp = xp + size;
+  uint64_t* keys = yp + half;
   const int entries = a.W * a.parts << shift;
   const uint64_t* from = a.lists + row0 * a.parts * k;
-  for (int i = tid; i < entries; i += kJoinThreads) {
-    // (what is no candidate is below all that are, and different from the rest)
-    const uint64_t key = (i & mask) < k ? from[(i >> shift) * k + (i & mask)] : 0;
-    keys[i] = key ? key : (uint32_t)~i;
-  }
+  for (int i = tid; i < entries; i += kJoinThreads) keys[i] = (i & mask) < k ? from[(i >> shift) * k + (i & mask)] : 0;
   for (int w = tid >> 5; w < a.W; w += kJoinThreads / 32) {  // a warp to a row
     const Part* p = a.part + (row0 + w) * a.parts;
     float ref = -INFINITY;
@@ -439,44 +483,64 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      double lse = -INFINITY;
+      float lse = -INFINITY, rest = 0.0f;
       if (!(sum <= 3.0e38f) || !(ref < INFINITY)) {
         record_error(&g_beam_error, CSA2_ERR_DEVICE);  // a NaN or +inf among the logits
-        lse = NAN;
+        lse = __uint_as_float(0x7FC00000u);
       } else if (sum > 0.0f) {
-        // the sum's exponent apart: the logarithm of a value in [1, 2) is off by 2^-24,
-        // and 64-bit operations are slow here
+        // the sum's exponent apart (ln 2 in two parts, the first of 15 bits: its products
+        // are exact): the logarithm of a value in [1, 2) is off by 2^-24
         const uint32_t bits = __float_as_uint(sum);
-        const float m = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
-        lse = (double)ref + ((double)((int)(bits >> 23) - 127) * 0.69314718055994531 + (double)logf(m));
+        const float e = (float)((int)(bits >> 23) - 127), m = logf(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
+        float r0, r1;
+        lse = two_sum(ref, e * 0.693145751953125f, r0);
+        lse = two_sum(lse, m, r1);
+        rest = fmaf(e, 1.42860682e-6f, r0 + r1);
+        lse = two_sum(lse, rest, r0);
+        rest = r0;
       }
-      if (a.lse) a.lse[row0 + w] = (float)lse;
+      if (a.lse) a.lse[row0 + w] = lse;
       const float s = a.scores ? a.scores[row0 + w] : 0.0f;
-      s_lse[w] = fabsf(s) < INFINITY && sum > 0.0f ? lse : (double)NAN;
+      s_lse[0][w] = fabsf(s) < INFINITY && sum > 0.0f ? lse : __uint_as_float(0x7FC00000u);
+      s_lse[1][w] = rest;
       s_score[w] = s;
     }
   }
   __syncthreads();
   // (the number of parts is a power of two: a row's lists are joined with one another)
-  const uint64_t* rows = join_lists(keys, keys + entries, a.W * a.parts, a.W, shift);
-  for (int i = tid; i < rows2 << shift; i += kJoinThreads) {
-    const int w = i >> shift;
-    const uint64_t key = w < a.W ? rows[i] : 0;
-    Best c{0, (uint64_t)~i};
-    // (x - lse first: the lowest value of fp32 less itself leaves the score)
-    if (key >> 32 && !isnan(s_lse[w]))
-      c = {order(s_score[w] + ((double)key_value(key) - s_lse[w])), ~((uint64_t)w << 32 | key_place(key))};
-    x[i] = c;
+  const uint64_t* rows = join_lists<false>(keys, keys + entries, nullptr, nullptr, a.W * a.parts, a.W, shift).keys;
+  // (threads past the end take part in the shuffles)
+  for (int i0 = 0; i0 < size; i0 += kJoinThreads) {
+    const int i = i0 + tid, w = i >> shift;
+    uint64_t mine = 0;
+    if (i < size) {
+      const uint64_t key = w < a.W ? rows[i] : 0;
+      if (key != 0 && !isnan(s_lse[0][w])) mine = sum_key(s_score[w], key_value(key), s_lse[0][w], s_lse[1][w]);
+      xp[i] = (uint64_t)w << 32 | key_place(key);
+    }
+    // A row's keys fall, as its logits do: logits closer than the last of the 48 bits may
+    // come out in either order. (32 at a time; a list of 64 below.)
+    const int place = lane & mask;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t before = __shfl_up_sync(0xffffffffu, mine, o);
+      if (place >= o) mine = min(mine, before);
+    }
+    if (i < size) x[i] = mine;
   }
   __syncthreads();
-  const Best* best = join_lists(x, y, rows2, 1, shift);
+  if (mask >= 32) {
+    for (int i = tid; i < size; i += kJoinThreads)
+      if (i & 32) x[i] = min(x[i], x[(i & ~63) + 31]);
+    __syncthreads();
+  }
+  const Lists best = join_lists<true>(x, y, xp, yp, rows2, 1, shift);
   for (int i = tid; i < k; i += kJoinThreads) {
-    const Best c = best[i];
+    const uint64_t key = best.keys[i], at = best.places[i];
     const int64_t o = (int64_t)b * k + i;
-    const uint64_t at = ~c.place;
-    a.out_scores[o] = c.score ? (float)order_value(c.score) : -INFINITY;
-    a.out_parents[o] = c.score ? (int32_t)(row0 + (int64_t)(at >> 32)) : -1;
-    a.out_tokens[o] = c.score ? (int32_t)at : -1;
+    a.out_scores[o] = key ? key_value(key) : -INFINITY;
+    a.out_parents[o] = key ? (int32_t)(row0 + (int64_t)(at >> 32)) : -1;
+    a.out_tokens[o] = key ? (int32_t)at : -1;
   }
 }
 

@@ -39,7 +39,10 @@ def reference(x, scores):
     """All candidates' scores [B, W * V] in 64 bits, -inf where there is none."""
     xd = x.double()
     lse = torch.logsumexp(xd, -1)
-    s = xd - lse[..., None] + (0 if scores is None else scores.double()[..., None])
+    # (x - lse as x less the row's largest, less the log of what is left: of n equal values -log n, which the sum of the
+    # type's lowest value and a logarithm loses in 64 bits too)
+    top = xd.amax(-1, keepdim=True)
+    s = (xd - top) - torch.log(torch.exp(xd - top).sum(-1, keepdim=True)) + (0 if scores is None else scores.double()[..., None])
     bad = ~torch.isfinite(lse)
     if scores is not None:
         bad |= ~torch.isfinite(scores)
@@ -114,6 +117,8 @@ def make(kind, g, B, W, V, dtype):
         x = torch.randn(B, W, V, generator=g, device="cuda")
         x = x.masked_fill(torch.rand(B, W, V, generator=g, device="cuda") < 0.9, torch.finfo(dtype).min)
         x[:, 0] = torch.finfo(dtype).min
+    elif kind == "tiny":  # closer than any sum with their log sum can tell
+        x = torch.randn(B, W, V, generator=g, device="cuda") * 10.0 ** torch.randint(-20, -8, (B, W, 1), generator=g, device="cuda")
     elif kind == "peaked":
         x = torch.randn(B, W, V, generator=g, device="cuda")
         x[..., V // 2] = 60.0
@@ -122,7 +127,7 @@ def make(kind, g, B, W, V, dtype):
     return x.to(dtype).contiguous()
 
 
-KINDS = ["normal", "equal", "few", "rising", "falling", "masked", "lowest", "peaked", "wide"]
+KINDS = ["normal", "equal", "few", "rising", "falling", "masked", "lowest", "peaked", "wide", "tiny"]
 SIZES = [(1, 1, 1, 1), (2, 3, 2, 4), (1, 4, 7, 8), (3, 2, 33, 5), (2, 8, 1000, 16), (1, 4, 5003, 64), (40, 16, 2051, 32),
          (1, 1, 40009, 64), (2, 64, 515, 64), (1, 2, 131075, 7)]
 
