@@ -1062,7 +1062,7 @@ static size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 static int check_sizes(int32_t n_out, int32_t n_in, int32_t format) {
   if (n_out < 0 || n_in < 0) return CSA2_ERR_INVALID_ARG;
   if (format != CSA2_FP4_E8M0 && format != CSA2_FP4_E4M3) return CSA2_ERR_INVALID_ARG;
-  if (n_in == 0 || n_in % 32) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (n_in == 0 || n_in % 32 || n_in > 1 << 30) return CSA2_ERR_UNSUPPORTED_SHAPE;
   return CSA2_OK;
 }
 static int64_t chunks_of(int32_t n_in) { return ((int64_t)n_in + linear::kChunk - 1) / linear::kChunk; }

@@ -746,7 +746,7 @@ int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32_t* cu_q,
  *     CSA2_FP4_E8M0  one E8M0 per 32 inputs [n_out][n_in/32] (csa2_quant_mxfp4),
  *     CSA2_FP4_E4M3  one E4M3 per 16 inputs [n_out][n_in/16], not negative, not NaN
  *                    (csa2_pack_kv_fp4 over the matrix as rows of 512).
- * n_in is a multiple of 32. */
+ * n_in is a multiple of 32, at most 2^30. */
 #define CSA2_FP4_E8M0 0
 #define CSA2_FP4_E4M3 1
 
@@ -758,7 +758,7 @@ size_t csa2_fp4_weights_size(int32_t n_out, int32_t n_in, int32_t format);
  * Lays packed weights out for csa2_fp4_linear, once for a matrix: blocks of 128
  * rows x 256 inputs as the tensor cores read them, codes and scales unchanged.
  *   data, weights 16-byte aligned; weights has csa2_fp4_weights_size bytes, all of
- *   them written.
+ *   them written; it must not overlap data or scale.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, CUDA.
  */
 int csa2_fp4_weights(const uint8_t* data, const uint8_t* scale, int32_t n_out,
@@ -776,14 +776,18 @@ size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in,
  *   x [n_tokens][n_in] bf16; weights from csa2_fp4_weights with the same n_out, n_in
  *   and format; out_bf16 and out_f32 [n_tokens][n_out], at least one of them
  *   (rounded from the same fp32 value).
- *   Precision: a token's blocks of 32 (E8M0) or 16 (E4M3) channels enter as sums of
- *   eight E2M1 vectors: exact for channels within 2^-14 of their block's largest,
- *   off by at most 2^-22 of the largest otherwise (with E4M3 scales, or 2^-39 of the
- *   token's largest; with either, or 2^-121). Products are exact, sums in fp32. A
- *   token with an infinity or a NaN has NaN in all its outputs; other tokens do not
- *   notice it. The same call gives the same bits; a token's result may differ in the
- *   last fp32 bits with the number of tokens.
+ *   Precision: up to 64 tokens, a token's blocks of 32 (E8M0) or 16 (E4M3) channels
+ *   enter as sums of eight E2M1 vectors: exact for channels within 2^-14 of their block's
+ *   largest, off by at most 2^-22 of the largest otherwise (with E4M3 scales, or 2^-39 of
+ *   the token's largest; with either, or 2^-121). More tokens enter as they are. The
+ *   weights are exact, products too, sums are in fp32. A token with an infinity or a NaN
+ *   has infinities or NaN in all its outputs; other tokens do not notice it. The same call
+ *   gives the same bits; a token's result may differ in the last fp32 bits with the number
+ *   of tokens.
  *   x, weights 16-byte aligned; the outputs must not overlap anything that is read.
+ *   weights are read before this call waits for the kernel just before it on the stream:
+ *   they must not be written by a kernel that lets its successor start early
+ *   (csa2_fp4_weights does not).
  *   workspace: csa2_fp4_linear_workspace_size bytes, 256-byte aligned, contents
  *   need not be kept; calls that may run at the same time need one each.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA.

@@ -135,9 +135,10 @@ def test_channels_of_all_sizes(csa2, form):
 
 @pytest.mark.parametrize("form", PER)
 @pytest.mark.parametrize("power", [-120, -60, 60, 110])
-def test_rows_of_all_sizes(csa2, form, power):
+@pytest.mark.parametrize("T", [2, 6, 40, 90])
+def test_rows_of_all_sizes(csa2, form, power, T):
     """Powers of two pass through: the row's own scale, with rows of other sizes beside it."""
-    T, n_in, n_out = 6, 512, 64
+    n_in, n_out = 512, 64
     g = gen(11)
     x = torch.randn(T, n_in, generator=g, device="cuda").bfloat16()
     data, scale = packed(g, n_out, n_in, form, -2, 2)
@@ -177,10 +178,11 @@ def test_zero_rows_and_rows_that_are_not_finite(csa2, form, T):
     assert torch.equal(out32[~wrong], base[~wrong])
 
 
-def test_extreme_scales(csa2):
-    """E8M0 from 2^-127 to 2^120, E4M3 subnormals and 448."""
+@pytest.mark.parametrize("T", [2, 20, 80])
+def test_extreme_scales(csa2, T):
+    """E8M0 from 2^-127 to 2^120, E4M3 subnormals and 448; an E8M0 NaN spoils its own output."""
     g = gen(4)
-    x = torch.randn(5, 256, generator=g, device="cuda").bfloat16()
+    x = torch.randn(T, 256, generator=g, device="cuda").bfloat16()
     data, _ = packed(g, 40, 256, "e8m0")
     for code in (0, 1, 60, 247):
         scale = torch.full((40, 8), code, dtype=torch.uint8, device="cuda")
@@ -189,6 +191,13 @@ def test_extreme_scales(csa2):
         tiny = 2.0 ** -149 * 64  # where the sums are fp32 subnormals
         A = x.double().abs() @ values(data, scale, "e8m0").abs().T
         assert (out32.double() - ref).abs().le(2.0 ** -15 * A + (tiny if code < 2 else 0)).all()
+    scale[:] = 120
+    _, base = call(csa2, x, data, scale, "e8m0")
+    scale[7, 3] = 255
+    _, out32 = call(csa2, x, data, scale, "e8m0")
+    assert out32[:, 7].isnan().all()
+    out32[:, 7] = base[:, 7]
+    assert torch.equal(out32, base)
     scale = torch.randint(0, 127, (40, 16), generator=g, device="cuda", dtype=torch.uint8)
     out, out32 = call(csa2, x, data, scale, "e4m3")
     check(x, data, scale, "e4m3", out, out32)

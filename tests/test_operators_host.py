@@ -40,7 +40,7 @@ WEIGHTS_GOOD = dict(data=P, scale=P, n_out=0, n_in=64, format=0, weights=P)
     ({}, OK), (dict(data=None, scale=None, weights=None), OK), (dict(format=1), OK),
     (dict(n_out=-1), ARG), (dict(n_in=-32), ARG), (dict(format=2), ARG), (dict(format=-1), ARG),
     (dict(n_out=1, data=None), ARG), (dict(n_out=1, scale=None), ARG), (dict(n_out=1, weights=None), ARG),
-    (dict(n_in=0), SHAPE), (dict(n_in=48), SHAPE), (dict(n_out=1 << 30, n_in=1 << 20), SHAPE),
+    (dict(n_in=0), SHAPE), (dict(n_in=48), SHAPE), (dict(n_in=(1 << 30) + 32), SHAPE), (dict(n_out=1 << 30, n_in=1 << 20), SHAPE),
     (dict(n_out=1, data=P + 8), ALIGN), (dict(n_out=1, weights=P + 8), ALIGN)])
 def test_weights(lib, change, status):
     assert call(lib.csa2_fp4_weights, WEIGHTS, WEIGHTS_GOOD, **change) == status
@@ -55,7 +55,7 @@ LINEAR_GOOD = dict(x=P, n=2, weights=P, n_out=8, n_in=64, format=0, scale=1.0, o
     (dict(n=0), OK), (dict(n_out=0), OK), (dict(n=0, x=None, out=None, ws=None), OK),
     (dict(n=-1), ARG), (dict(n_out=-1), ARG), (dict(n_in=-1), ARG), (dict(format=7), ARG), (dict(x=None), ARG),
     (dict(weights=None), ARG), (dict(out=None), ARG), (dict(out=None, out_f32=P), WORKSPACE),
-    (dict(n_in=0), SHAPE), (dict(n_in=33), SHAPE), (dict(n=1 << 30, n_out=1 << 30), SHAPE), (dict(n=1 << 30, n_in=1 << 20), SHAPE),
+    (dict(n_in=0), SHAPE), (dict(n_in=33), SHAPE), (dict(n_in=(1 << 30) + 32), SHAPE), (dict(n=1 << 30, n_out=1 << 30), SHAPE), (dict(n=1 << 30, n_in=1 << 20), SHAPE),
     (dict(x=P + 8), ALIGN), (dict(weights=P + 8), ALIGN), (dict(out=P + 1), ALIGN), (dict(out_f32=P + 2), ALIGN)])
 def test_linear(lib, change, status):
     assert call(lib.csa2_fp4_linear, LINEAR, LINEAR_GOOD, **change) == status
