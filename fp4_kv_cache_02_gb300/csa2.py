@@ -152,6 +152,13 @@ def _s(stream):
     return stream.cuda_stream
 
 
+def _stream_on(stream, dev):
+    """_s for a call whose device is known to be the current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _s(stream)
+
+
 def _req(t, dtype, name, allow_none=False):
     if t is None:
         if allow_none:
@@ -682,19 +689,26 @@ def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None,
     n_out] bf16 = scale * x W^T and / or out_f32, the same in fp32 (either may be
     None, not both)."""
     dev = _device(x, "x")
-    x_at, w_at = _take(x, torch.bfloat16, "x", dev), _take(weights, torch.uint8, "weights", dev)
-    ws_at = _take(workspace, torch.uint8, "workspace", dev)
+    if x.dtype is not torch.bfloat16:
+        _req(x, torch.bfloat16, "x")
     to = out_f32 if out is None else out
-    if x.dim() != 2 or to is None or to.dim() != 2 or to.shape[0] != x.shape[0]:
+    if to is None:
+        raise ValueError("out or out_f32 is required")
+    x_shape, shape = x.shape, to.shape
+    if len(x_shape) != 2 or len(shape) != 2 or shape[0] != x_shape[0]:
         raise ValueError("x must be [n_tokens, n_in], out or out_f32 [n_tokens, n_out]")
-    (n, n_in), n_out = x.shape, to.shape[1]
+    (n, n_in), n_out = x_shape, shape[1]
     kind = _format(format)
+    w_at = _take(weights, torch.uint8, "weights", dev)
     # (csa2_fp4_weights_size without a call: blocks of 128 x 256 weights)
     if weights.numel() < (n_out + 127) // 128 * ((n_in + 255) // 256) * (18432 if kind else 17408):
         raise ValueError(f"weights holds fewer than {n_out} x {n_in} weights")
-    _call("csa2_fp4_linear", x_at, n, w_at, n_out, n_in, kind, float(scale),
-          _optional(out, torch.bfloat16, (n, n_out), "out", dev), _optional(out_f32, torch.float32, (n, n_out), "out_f32", dev),
-          ws_at, workspace.numel(), _s(stream))
+    out_at = None if out is None else _take(out, torch.bfloat16, "out", dev)  # (its shape is the one compared with)
+    out32_at = None if out_f32 is None else _shaped(out_f32, torch.float32, shape, "out_f32", dev)
+    rc = _lib.csa2_fp4_linear(x.data_ptr(), n, w_at, n_out, n_in, kind, scale, out_at, out32_at,
+                              _take(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream_on(stream, dev))
+    if rc != 0:
+        raise Csa2Error("csa2_fp4_linear", rc)
 
 
 # ---- beam search -------------------------------------------------------------------
@@ -704,25 +718,29 @@ def csa2_beam_select(logits, scores, out_scores, out_parents, out_tokens, worksp
     scores [B, W] fp32 or None -> the k best (beam, token) pairs of each sequence:
     out_scores fp32, out_parents (rows b * W + w) and out_tokens int32 [B, k]; lse
     [B, W] fp32 is optional."""
-    dev = out_scores.get_device() if out_scores is not None else -1
-    if logits.dim() != 3 or logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor [B, W, V] of bf16 or fp32")
-    if logits.get_device() != dev or dev != torch.cuda.current_device():
-        raise ValueError(f"logits and out_scores must be on the current device, cuda:{torch.cuda.current_device()}")
-    B, W, V = logits.shape
-    ld = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
-    if (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != W * ld):
-        raise ValueError("logits must have adjacent elements and equally distant rows")
-    if out_scores.dim() != 2 or out_scores.shape[0] != B:
+    dev = _device(out_scores, "out_scores")
+    f32 = logits.dtype is torch.float32
+    shape, out_shape = logits.shape, out_scores.shape
+    if len(shape) != 3 or not (f32 or logits.dtype is torch.bfloat16) or logits.get_device() != dev:
+        raise ValueError(f"logits must be [B, W, V] of bf16 or fp32 on the current device, cuda:{dev}")
+    B, W, V = shape
+    if logits.is_contiguous():
+        ld = V
+    else:
+        at = logits.stride()
+        ld = at[1] if W > 1 else at[0] if B > 1 else V
+        if (V > 1 and at[2] != 1) or (B > 1 and at[0] != W * ld):
+            raise ValueError("logits must have adjacent elements and equally distant rows")
+    if len(out_shape) != 2 or out_shape[0] != B:
         raise ValueError("out_scores must be [B, k]")
-    k = out_scores.shape[1]
-    _call("csa2_beam_select", logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0, B, W, V, ld,
+    k = out_shape[1]
+    _call("csa2_beam_select", logits.data_ptr(), 1 if f32 else 0, B, W, V, ld,
           _optional(scores, torch.float32, (B, W), "scores", dev), k,
           _take(out_scores, torch.float32, "out_scores", dev),
-          _shaped(out_parents, torch.int32, (B, k), "out_parents", dev),
-          _shaped(out_tokens, torch.int32, (B, k), "out_tokens", dev),
+          _shaped(out_parents, torch.int32, out_shape, "out_parents", dev),
+          _shaped(out_tokens, torch.int32, out_shape, "out_tokens", dev),
           _optional(lse, torch.float32, (B, W), "lse", dev),
-          _take(workspace, torch.uint8, "workspace", dev), workspace.numel(), _s(stream))
+          _take(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream_on(stream, dev))
 
 
 def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_out, n_visible_out, kv_data=None,
@@ -733,9 +751,10 @@ def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_o
     caches that share the table; page_table [rows, max_pages] -> page_table_out [R,
     max_pages], n_visible [rows] -> n_visible_out [R]."""
     dev = _device(parents, "parents")
-    if parents.dim() != 1:
+    each = parents.shape
+    if len(each) != 1:
         raise ValueError("parents must be [R]")
-    R = parents.shape[0]
+    R = each[0]
     first = kv_data if kv_data is not None else ik_data
     if first is None or (kv_data is None) != (kv_scale is None) or (ik_data is None) != (ik_scale is None):
         raise ValueError("codes and scales of the latents, of the keys, or of both are required")
@@ -747,14 +766,15 @@ def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_o
                                  (ik_scale, 4, "ik_scale"))]
     layers, n_pages, page = pool if len(pool) == 3 else (1, *pool)
     table = _take(page_table, torch.int32, "page_table", dev)
-    if page_table.dim() != 2:
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [rows, max_pages]")
-    rows, max_pages = page_table.shape
-    _call("csa2_paged_reorder", _shaped(parents, torch.int32, (R,), "parents", dev),
-          _shaped(fresh_pages, torch.int32, (R,), "fresh_pages", dev), R, *at, layers, n_pages, page, table, rows,
+    rows, max_pages = shape
+    _call("csa2_paged_reorder", _take(parents, torch.int32, "parents", dev),
+          _shaped(fresh_pages, torch.int32, each, "fresh_pages", dev), R, *at, layers, n_pages, page, table, rows,
           max_pages, _shaped(n_visible, torch.int32, (rows,), "n_visible", dev),
           _shaped(page_table_out, torch.int32, (R, max_pages), "page_table_out", dev),
-          _shaped(n_visible_out, torch.int32, (R,), "n_visible_out", dev), _s(stream))
+          _shaped(n_visible_out, torch.int32, each, "n_visible_out", dev), _stream_on(stream, dev))
 
 
 def csa2_reorder_rows(src, parents, dst, stream=None):
@@ -762,12 +782,13 @@ def csa2_reorder_rows(src, parents, dst, stream=None):
     a multiple of 16 bytes; parents [R] int32, -1 leaves a row as it was."""
     dev = _device(src, "src")
     src_at, dst_at = _take(src, src.dtype, "src", dev), _take(dst, src.dtype, "dst", dev)
-    if src.dim() < 1 or dst.dim() != src.dim() or dst.shape[1:] != src.shape[1:]:
+    shape, to = src.shape, dst.shape
+    if len(shape) < 1 or len(to) < 1 or shape[1:] != to[1:]:
         raise ValueError("src must be [rows, ...] and dst [R, ...] with rows alike")
-    size = src.element_size() * math.prod(src.shape[1:])
-    R = dst.shape[0]
-    _call("csa2_reorder_rows", src_at, src.shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R, dst_at,
-          _s(stream))
+    size = src.element_size() * math.prod(shape[1:])
+    R = to[0]
+    _call("csa2_reorder_rows", src_at, shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R, dst_at,
+          _stream_on(stream, dev))
 
 
 # ---- allocating helpers (torch memory plumbing + the entry points above) --------
