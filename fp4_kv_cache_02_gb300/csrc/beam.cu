@@ -82,13 +82,13 @@ __device__ __forceinline__ uint32_t bound_of_warps(float top, int k, uint32_t* s
 }
 
 // Two fp32 operations at once (the values come in pairs of registers).
-__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
-  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
-      : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+__device__ __forceinline__ void add2(float a, float b, float x, float y, float& s, float& t) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(s), "=f"(t) : "f"(a), "f"(b), "f"(x), "f"(y));
 }
-__device__ __forceinline__ void mul2(float& a, float& b, float x) {
-  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
-      : "+f"(a), "+f"(b) : "f"(x));
+__device__ __forceinline__ void mul2(float a, float b, float x, float& s, float& t) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(s), "=f"(t) : "f"(a), "f"(b), "f"(x));
 }
 __device__ __forceinline__ float ex2(float x) {
   float e;
@@ -233,25 +233,33 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(RowArgs<T> a) {
     float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kX; i += 2) {
-      float u = x[i], v = x[i + 1];
-      add2(u, v, from, from);
-      mul2(u, v, kLog2e);
-      add2(add[i % 4], add[i % 4 + 1], ex2(u), ex2(v));
+      float u, v;
+      add2(x[i], x[i + 1], from, from, u, v);
+      mul2(u, v, kLog2e, u, v);
+      add2(add[i % 4], add[i % 4 + 1], ex2(u), ex2(v), add[i % 4], add[i % 4 + 1]);
     }
     sum += (add[0] + add[1]) + (add[2] + add[3]);
 
+    // (mostly it is one value of a thread, its largest: to look for it costs a third of
+    // trying each in turn)
+    const auto put = [&](uint64_t key) {
+      if (key < bound) return;
+      const int at = n + atomicAdd(&s_added[turn], 1);
+      if (at < kRoom) s_list[at] = key;
+    };
     const auto push = [&]() {
       if (!(top >= bound_value)) return;
+      uint32_t pass = 0;
 #pragma unroll
-      for (int i = 0; i < kX; ++i) {
-        if (x[i] >= bound_value) {
-          const uint64_t key = make_key(x[i], place_of(i));
-          if (key >= bound) {
-            const int at = n + atomicAdd(&s_added[turn], 1);
-            if (at < kRoom) s_list[at] = key;
-          }
-        }
+      for (int i = 0; i < kX; ++i)
+        if (x[i] >= bound_value) pass |= 1u << i;
+      if ((pass & (pass - 1)) == 0) {
+        put(make_key(top, place_of(__ffs(pass) - 1)));
+        return;
       }
+#pragma unroll
+      for (int i = 0; i < kX; ++i)
+        if (pass >> i & 1u) put(make_key(x[i], place_of(i)));
     };
     if (first) {
       const uint32_t least = bound_of_warps(top, k, s_warps);
