@@ -398,7 +398,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
   const int blk_b = terms_bytes(kE4M3, p.n);
   const int stage_bytes = block_bytes(kE4M3) + blk_b;
 
-  if (threadIdx.x == 0) {
+  const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
+  const auto load_weights = [&](int i, int s) {
+    tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(kOwnTerms ? block_bytes(kE4M3) : stage_bytes));
+    tc::bulk_load(ring + s * stage_bytes, from + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full[s]);
+  };
+  const int ahead = n_chunks < p.stages ? n_chunks : p.stages;
+  if (warp == kProducerWarp && lane == 0) {
     for (int s = 0; s < p.stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&ready[s], p.T);
@@ -407,6 +413,35 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
     tc::mbar_init(acc_full, 1);
     *s_abort = 0;
     tc::fence_mbar_init();
+    tc::fence_proxy_async_smem();
+    for (int i = 0; i < ahead; ++i) load_weights(i, i);
+  }
+  // kOwnTerms: x is looked at before the set-up is through. With E4M3 scales all of this
+  // CTA's channels, for the scales' base.
+  const auto channels = [&](int c, int t) {
+    const int32_t k = (c0 + c) * kChunk + lane * 8;
+    return k < p.n_in ? *reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.n_in + k) : make_uint4(0, 0, 0, 0);
+  };
+  uint32_t top[kFewTokens] = {};
+  const auto write_tops = [&]() {
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, top[t]);
+      if (lane == 0) s_top[warp * kFewTokens + t] = m;
+    }
+  };
+  uint4 ahead_v = make_uint4(0, 0, 0, 0);
+  if (kOwnTerms && warp < kSumWarps) {
+    pdl_wait();  // x; and the outputs may have readers before this call
+    if (kE4M3) {
+      for (int c = warp; c < n_chunks; c += kSumWarps)
+#pragma unroll
+        for (int t = 0; t < kFewTokens; ++t)
+          if (t < p.T) top[t] = max(top[t], top_bits(channels(c, t)));
+      write_tops();
+    } else if (warp < n_chunks * p.T) {
+      ahead_v = channels(warp / p.T, warp % p.T);
+    }
   }
   if (warp == kMmaWarp) tc::tmem_alloc(s_tmem, p.tmem_cols);
   tc::tc_fence_before();
@@ -416,18 +451,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
-      const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
       const uint8_t* terms = kOwnTerms ? nullptr : p.terms + ((int64_t)token_tile * p.chunks + c0) * blk_b;
-      const auto load_weights = [&](int i, int s) {
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(kOwnTerms ? block_bytes(kE4M3) : stage_bytes));
-        tc::bulk_load(ring + s * stage_bytes, from + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full[s]);
-      };
       const auto load_terms = [&](int i, int s) {
         if constexpr (!kOwnTerms)
           tc::bulk_load(ring + s * stage_bytes + block_bytes(kE4M3), terms + (int64_t)i * blk_b, (uint32_t)blk_b, &full[s]);
       };
-      const int ahead = n_chunks < p.stages ? n_chunks : p.stages;
-      for (int i = 0; i < ahead; ++i) load_weights(i, i);
       if constexpr (!kOwnTerms) pdl_wait();
       for (int i = 0; i < ahead; ++i) load_terms(i, i);
       int issued = ahead;
@@ -462,42 +490,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
     tc::mbar_wait_issued(acc_full, 0);
     __syncwarp();
   } else {
-    pdl_wait();  // x or the factors; and the outputs may have readers before this call
+    if (!kOwnTerms) pdl_wait();  // the factors; and the outputs may have readers before this call
   }
   if (kOwnTerms && warp < kSumWarps) {
-    const auto channels = [&](int c, int t) {
-      const int32_t k = (c0 + c) * kChunk + lane * 8;
-      return k < p.n_in ? *reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.n_in + k) : make_uint4(0, 0, 0, 0);
-    };
-    uint32_t top[kFewTokens] = {};
     const auto top_of = [&](int t) {
       uint32_t m = s_top[t];
 #pragma unroll
       for (int i = 1; i < kSumWarps; ++i) m = max(m, s_top[i * kFewTokens + t]);
       return m;
     };
-    const auto share_tops = [&]() {
-#pragma unroll
-      for (int t = 0; t < kFewTokens; ++t) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, top[t]);
-        if (lane == 0) s_top[warp * kFewTokens + t] = m;
-      }
-      sync_sum_warps();
-    };
-    if (kE4M3) {  // the scales' base: the largest of this CTA's channels
-      for (int c = warp; c < n_chunks; c += kSumWarps)
-#pragma unroll
-        for (int t = 0; t < kFewTokens; ++t)
-          if (t < p.T) top[t] = max(top[t], top_bits(channels(c, t)));
-      share_tops();
-    }
     // No more warps than there are (stage, token) places: a warp's last task is then at
     // most a round of the ring behind its next, so that the stage it waits for is in the
     // phase before the awaited one or later (a barrier tells two phases apart, not three).
     const int n_tasks = n_chunks * p.T, workers = min(kSumWarps, p.stages * p.T);
     for (int i = warp < workers ? warp : n_tasks; i < n_tasks; i += workers) {
       const int c = i / p.T, t = i % p.T, s = c % p.stages;
-      const uint4 v = channels(c, t);
+      const uint4 v = !kE4M3 && i == warp ? ahead_v : channels(c, t);
       const bool ok = tc::mbar_wait_bounded(&empty[s], ((uint32_t)(c / p.stages) & 1u) ^ 1u, s_abort, &g_linear_error);
       if (!__all_sync(0xffffffffu, ok)) break;
       uint32_t whole = 0;  // (E8M0 scales need no base of the token's own)
@@ -515,7 +523,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&ready[s]);
     }
-    if (!kE4M3) share_tops();
+    if (!kE4M3) {
+      write_tops();
+      sync_sum_warps();
+    }
   }
 
   float* sums = reinterpret_cast<float*>(ring);  // [nt][128], once the ring is done with
@@ -602,7 +613,26 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
   const int stage_bytes = block_bytes(kE4M3) + blk_b;
   const int accs = p.n <= 128 ? 2 : 1;
 
-  if (threadIdx.x == 0) {
+  struct Place {
+    int64_t row_tile;
+    int32_t token_tile, chunk;
+  };
+  const Place start{tile0 / p.token_tiles, (int32_t)(tile0 % p.token_tiles), chunk0};
+  const auto advance = [&](Place& at) {
+    if (++at.chunk < p.chunks) return;
+    at.chunk = 0;
+    if (++at.token_tile < p.token_tiles) return;
+    at.token_tile = 0;
+    ++at.row_tile;
+  };
+  const auto load_weights = [&](const Place& at, int s) {
+    tc::mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
+    tc::bulk_load(ring + s * stage_bytes, p.weights + (at.row_tile * p.chunks + at.chunk) * block_bytes(kE4M3),
+                  block_bytes(kE4M3), &full[s]);
+  };
+  const int64_t n_units = u1 - u0;
+  const int ahead = n_units < p.stages ? (int)n_units : p.stages;
+  if (warp == kProducerWarp && lane == 0) {
     for (int s = 0; s < p.stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -613,6 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
     }
     *s_abort = 0;
     tc::fence_mbar_init();
+    tc::fence_proxy_async_smem();
+    Place at = start;
+    for (int i = 0; i < ahead; ++i, advance(at)) load_weights(at, i);
   }
   if (warp == kSumWarps + 1) tc::tmem_alloc(s_tmem, p.tmem_cols);
   tc::tc_fence_before();
@@ -622,38 +655,17 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
 
   if (warp == kSumWarps) {
     if (lane == 0) {
-      struct Place {
-        int64_t row_tile;
-        int32_t token_tile, chunk;
-      };
-      const Place start{tile0 / p.token_tiles, (int32_t)(tile0 % p.token_tiles), chunk0};
-      const auto advance = [&](Place& at) {
-        if (++at.chunk < p.chunks) return;
-        at.chunk = 0;
-        if (++at.token_tile < p.token_tiles) return;
-        at.token_tile = 0;
-        ++at.row_tile;
-      };
-      const auto load_weights = [&](const Place& at, int s) {
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
-        tc::bulk_load(ring + s * stage_bytes, p.weights + (at.row_tile * p.chunks + at.chunk) * block_bytes(kE4M3),
-                      block_bytes(kE4M3), &full[s]);
-      };
       const auto load_terms = [&](const Place& at, int s) {
         tc::bulk_load(ring + s * stage_bytes + block_bytes(kE4M3), p.terms + ((int64_t)at.token_tile * p.chunks + at.chunk) * blk_b,
                       (uint32_t)blk_b, &full[s]);
       };
-      const int64_t n = u1 - u0;
-      const int ahead = n < p.stages ? (int)n : p.stages;
-      Place at = start;
-      for (int i = 0; i < ahead; ++i, advance(at)) load_weights(at, i);
       pdl_wait();
-      at = start;
+      Place at = start;
       for (int i = 0; i < ahead; ++i, advance(at)) load_terms(at, i);
       int64_t issued = ahead;
       int s = ahead % p.stages;
       uint32_t turn = (uint32_t)(ahead / p.stages);  // times that the ring has gone round
-      for (; issued < n; ++issued, advance(at)) {
+      for (; issued < n_units; ++issued, advance(at)) {
         if (!tc::mbar_wait_bounded(&empty[s], (turn & 1u) ^ 1u, s_abort, &g_linear_error)) break;
         load_weights(at, s);
         load_terms(at, s);
@@ -880,7 +892,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
   const int steps = min((c1 - c0) * (kChunk / kSub), (p.n_in - c0 * kChunk + kSub - 1) / kSub);
   constexpr int kOfChunk = kChunk / kSub;
 
-  if (threadIdx.x == 0) {
+  const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
+  const int n_raw = (steps + kOfChunk - 1) / kOfChunk;
+  const auto load_raw = [&](int i, int s) {
+    tc::mbar_arrive_expect_tx(&full_w[s], block_bytes(kE4M3));
+    tc::bulk_load(s_w + s * block_bytes(kE4M3), from + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full_w[s]);
+  };
+  if (warp == 4 * kSets && lane == 0) {
     for (int s = 0; s < kRawStages; ++s) {
       tc::mbar_init(&full_w[s], 1);
       tc::mbar_init(&empty_w[s], kOfChunk * 4);  // each step's four warps
@@ -896,6 +914,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     tc::mbar_init(acc_full, 1);
     *s_abort = 0;
     tc::fence_mbar_init();
+    tc::fence_proxy_async_smem();
+    for (int i = 0; i < min(n_raw, kRawStages); ++i) load_raw(i, i);
   }
   if (warp == 4 * kSets + 1) tc::tmem_alloc(s_tmem, 512);
   tc::tc_fence_before();
@@ -905,14 +925,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
 
   if (warp == 4 * kSets) {
     if (lane == 0) {
-      const uint8_t* from = p.weights + (row_tile * p.chunks + c0) * block_bytes(kE4M3);
-      const int n_raw = (steps + kOfChunk - 1) / kOfChunk;
-      int i = 0;
+      int i = min(n_raw, kRawStages);
       for (; i < n_raw; ++i) {
         const int s = i % kRawStages;
         if (!tc::mbar_wait_bounded(&empty_w[s], ((uint32_t)(i / kRawStages) & 1u) ^ 1u, s_abort, &g_linear_error)) break;
-        tc::mbar_arrive_expect_tx(&full_w[s], block_bytes(kE4M3));
-        tc::bulk_load(s_w + s * block_bytes(kE4M3), from + (int64_t)i * block_bytes(kE4M3), block_bytes(kE4M3), &full_w[s]);
+        load_raw(i, s);
       }
       // copies land before the CTA's memory goes away
       for (int l = max(0, i - kRawStages); l < i; ++l) tc::mbar_wait_issued(&full_w[l % kRawStages], (uint32_t)(l / kRawStages));
