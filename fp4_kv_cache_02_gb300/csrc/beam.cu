@@ -24,10 +24,10 @@ constexpr int kJoinThreads = 512;
 constexpr int kMaxEntries = 8192;           // entries of a sequence's lists in the joining kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Values by size, equal ones by place, the lower first: larger is better, all
-// different, 0 for none.
+// Values by size, equal ones (zeros of either sign too) by place, the lower first:
+// larger is better, all different, 0 for none.
 __device__ __forceinline__ uint64_t make_key(float x, uint32_t place) {
-  return (uint64_t)score_key(x) << 32 | (uint32_t)~place;
+  return (uint64_t)score_key(__fadd_rn(x, 0.0f)) << 32 | (uint32_t)~place;
 }
 __device__ __forceinline__ float key_value(uint64_t key) {
   const uint32_t b = (uint32_t)(key >> 32);
@@ -681,7 +681,7 @@ static int check_beam(int32_t B, int32_t W, int32_t V, int32_t k) {
   return CSA2_OK;
 }
 
-// Parts of a row, a power of two: at most 608 CTAs in all (four to each of 152 SMs: the
+// Parts of a row, a power of two: at most 304 CTAs in all (two to each of 152 SMs: the
 // size of a workspace does not depend on the device) unless there are more rows, parts
 // of 2,048 values at least.
 static int beam_parts(int32_t B, int32_t W, int32_t V, int32_t k) {

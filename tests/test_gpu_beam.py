@@ -179,6 +179,17 @@ def test_equal_beams_go_by_place(csa2):
     assert torch.equal(((parents - first) * 500 + tokens).long(), want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_zeros_of_either_sign_are_equal(csa2, dtype):
+    g = gen(2)
+    x = torch.where(torch.rand(3, 2, 5003, generator=g, device="cuda") < 0.5, 0.0, -0.0).to(dtype)
+    x[..., ::7] = -1.0
+    check(x, torch.zeros(3, 2, device="cuda"), call(csa2, x, torch.zeros(3, 2, device="cuda"), 40))
+    _, _, tokens, _ = call(csa2, x[:, :1].contiguous(), None, 64)
+    want = [i for i in range(100) if i % 7][:64]
+    assert tokens.tolist() == [want] * 3
+
+
 def test_beams_that_take_no_part(csa2):
     g = gen(21)
     x = torch.randn(3, 4, 3000, generator=g, device="cuda")
