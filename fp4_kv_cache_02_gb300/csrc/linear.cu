@@ -366,7 +366,7 @@ __device__ __forceinline__ void add_parts(const Params& p, const float* sums, in
 // ---- few tiles -------------------------------------------------------------------
 // Products of too few tiles (128 outputs x up to 32 tokens) to fill the SMs, and those
 // of few tokens. The CTAs of a cluster split a tile's chunks, and their sums are added in
-// rank order out of one another's shared memory. kOwnTerms: up to eight tokens, whose terms
+// rank order out of one another's shared memory. kOwnTerms: up to four tokens, whose terms
 // each CTA makes itself: ahead of the product they would cost a launch and a trip through
 // L2 (4 us of 15 for a token by 32,768 x 4,096 weights).
 //   warp 8     producer: a bulk copy of a block of weights per stage (and one of the
@@ -567,12 +567,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
     if (ok) tc::tc_fence_before();
   }
   __syncthreads();
+  // (before the peers are waited for: of two calls at once neither then waits for tensor
+  // memory that the other one's waiting CTAs hold)
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, p.tmem_cols);
   if (p.split > 1) {
     cluster_sync();
     add_parts(p, sums, part, nt, t0, row_tile);
     cluster_sync();  // the peers have read this CTA's sums
   }
-  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, p.tmem_cols);
 }
 
 // ---- many tiles ------------------------------------------------------------------
@@ -1050,12 +1052,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     }
   }
   __syncthreads();
+  if (warp == 4 * kSets + 1) tc::tmem_dealloc(tmem, 512);  // (first, as above)
   if (p.split > 1) {
     cluster_sync();
     add_parts(p, sums, part, nt, t0, row_tile);
     cluster_sync();  // the peers have read this CTA's sums
   }
-  if (warp == 4 * kSets + 1) tc::tmem_dealloc(tmem, 512);
 }
 
 }  // namespace linear
@@ -1140,8 +1142,9 @@ static bool is_wide(int32_t T, int32_t n_in) { return T > linear::kTermTokens &&
 
 extern "C" size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in, int32_t format) {
   if (n_tokens <= 0 || check_sizes(1, n_in, format) != CSA2_OK) return 0;
-  if (is_wide(n_tokens, n_in)) return 256;  // (nothing is kept there)
-  return space_of(n_tokens, n_in, format == CSA2_FP4_E4M3).bytes;
+  // (a product of bf16 values keeps nothing there; the size never falls with more tokens,
+  // so that one workspace does for all calls of up to as many)
+  return space_of(is_wide(n_tokens, n_in) ? linear::kTermTokens : n_tokens, n_in, format == CSA2_FP4_E4M3).bytes;
 }
 
 // Stages that fit beside `acc` accumulator columns.

@@ -765,7 +765,8 @@ int csa2_fp4_weights(const uint8_t* data, const uint8_t* scale, int32_t n_out,
                      int32_t n_in, int32_t format, uint8_t* weights,
                      csa2_stream_t stream);
 
-/** Bytes of workspace csa2_fp4_linear needs: the same for every n_out. */
+/** Bytes of workspace csa2_fp4_linear needs: the same for every n_out, and no fewer
+ * for more tokens (one for the most does for all). */
 size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in,
                                       int32_t format);
 

@@ -75,6 +75,13 @@ def test_sizes(lib):
     assert beam(0, 1, 10, 1) == beam(1, 0, 10, 1) == beam(1, 1, 10, 0) == beam(1, 1, 10, 65) == 0
 
 
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("n_in", [32, 64, 256, 4096, 32768])
+def test_a_workspace_for_more_tokens_does_for_fewer(lib, n_in, kind):
+    sizes = [lib.csa2_fp4_linear_workspace_size(t, n_in, kind) for t in [*range(1, 140), 1021, 4096, 100003]]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 BEAM = "logits f32 B W V ld scores k out parents tokens lse ws ws_bytes".split()
 BEAM_GOOD = dict(logits=P, f32=1, B=2, W=3, V=100, ld=100, scores=P, k=4, out=P, parents=P, tokens=P, lse=None, ws=P, ws_bytes=0)
 
