@@ -142,6 +142,8 @@ def _p(t):
 
 # the current stream's handle without a Stream object (0.4 us instead of 3), where this torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device of a process that has a CUDA tensor (0.06 us instead of 0.2)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _s(stream):
@@ -502,9 +504,10 @@ def _take(t, dtype, name, dev):
 def _device(t, name):
     """The device of a call: its first tensor's, which has to be the current one
     (the kernels are launched there)."""
-    _req(t, t.dtype if t is not None else None, name)
+    if t is None or not t.is_cuda or not t.is_contiguous():
+        _req(t, t.dtype if t is not None else None, name)
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
@@ -529,10 +532,11 @@ def _pool(dev, planes, page_table, n_visible):
 
 
 def _shaped(t, dtype, shape, name, dev):
-    at = _take(t, dtype, name, dev)
+    if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, name, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    return at
+    return t.data_ptr()
 
 
 def _optional(t, dtype, shape, name, dev):
@@ -754,41 +758,52 @@ def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_o
     each = parents.shape
     if len(each) != 1:
         raise ValueError("parents must be [R]")
-    R = each[0]
     first = kv_data if kv_data is not None else ik_data
     if first is None or (kv_data is None) != (kv_scale is None) or (ik_data is None) != (ik_scale is None):
         raise ValueError("codes and scales of the latents, of the keys, or of both are required")
-    pool = first.shape[:-1]
-    if not 2 <= len(pool) <= 3:
+    pool = tuple(first.shape)[:-1]
+    if len(pool) == 2:
+        layers, (n_pages, page) = 1, pool
+    elif len(pool) == 3:
+        layers, n_pages, page = pool
+    else:
         raise ValueError("planes must be [n_pages, page_size, width] or [layers, n_pages, page_size, width]")
-    at = [_optional(t, torch.uint8, (*pool, width), name, dev)
-          for t, width, name in ((kv_data, 256, "kv_data"), (kv_scale, 32, "kv_scale"), (ik_data, 64, "ik_data"),
-                                 (ik_scale, 4, "ik_scale"))]
-    layers, n_pages, page = pool if len(pool) == 3 else (1, *pool)
-    table = _take(page_table, torch.int32, "page_table", dev)
+    kv_at = kvs_at = ik_at = iks_at = None
+    if kv_data is not None:
+        kv_at = _shaped(kv_data, torch.uint8, (*pool, 256), "kv_data", dev)
+        kvs_at = _shaped(kv_scale, torch.uint8, (*pool, 32), "kv_scale", dev)
+    if ik_data is not None:
+        ik_at = _shaped(ik_data, torch.uint8, (*pool, 64), "ik_data", dev)
+        iks_at = _shaped(ik_scale, torch.uint8, (*pool, 4), "ik_scale", dev)
+    int32 = torch.int32
+    table = _take(page_table, int32, "page_table", dev)
     shape = page_table.shape
     if len(shape) != 2:
         raise ValueError("page_table must be [rows, max_pages]")
-    rows, max_pages = shape
-    _call("csa2_paged_reorder", _take(parents, torch.int32, "parents", dev),
-          _shaped(fresh_pages, torch.int32, each, "fresh_pages", dev), R, *at, layers, n_pages, page, table, rows,
-          max_pages, _shaped(n_visible, torch.int32, (rows,), "n_visible", dev),
-          _shaped(page_table_out, torch.int32, (R, max_pages), "page_table_out", dev),
-          _shaped(n_visible_out, torch.int32, each, "n_visible_out", dev), _stream_on(stream, dev))
+    (R,), (rows, max_pages) = each, shape
+    rc = _lib.csa2_paged_reorder(
+        _take(parents, int32, "parents", dev), _shaped(fresh_pages, int32, each, "fresh_pages", dev), R, kv_at, kvs_at,
+        ik_at, iks_at, layers, n_pages, page, table, rows, max_pages,
+        _shaped(n_visible, int32, (rows,), "n_visible", dev),
+        _shaped(page_table_out, int32, (R, max_pages), "page_table_out", dev),
+        _shaped(n_visible_out, int32, each, "n_visible_out", dev), _stream_on(stream, dev))
+    if rc != 0:
+        raise Csa2Error("csa2_paged_reorder", rc)
 
 
 def csa2_reorder_rows(src, parents, dst, stream=None):
     """dst[r] = src[parents[r]]: src [rows, ...], dst [R, ...] of any one type, rows of
     a multiple of 16 bytes; parents [R] int32, -1 leaves a row as it was."""
     dev = _device(src, "src")
-    src_at, dst_at = _take(src, src.dtype, "src", dev), _take(dst, src.dtype, "dst", dev)
-    shape, to = src.shape, dst.shape
+    dtype, shape = src.dtype, src.shape
+    dst_at, to = _take(dst, dtype, "dst", dev), dst.shape
     if len(shape) < 1 or len(to) < 1 or shape[1:] != to[1:]:
         raise ValueError("src must be [rows, ...] and dst [R, ...] with rows alike")
-    size = src.element_size() * math.prod(shape[1:])
-    R = to[0]
-    _call("csa2_reorder_rows", src_at, shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R, dst_at,
-          _stream_on(stream, dev))
+    size, R = dtype.itemsize * math.prod(shape[1:]), to[0]
+    rc = _lib.csa2_reorder_rows(src.data_ptr(), shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R,
+                                dst_at, _stream_on(stream, dev))
+    if rc != 0:
+        raise Csa2Error("csa2_reorder_rows", rc)
 
 
 # ---- allocating helpers (torch memory plumbing + the entry points above) --------
