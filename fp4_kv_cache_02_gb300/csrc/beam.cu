@@ -21,7 +21,6 @@ constexpr int kMaxK = CSA2_MAX_BEAM_K;
 constexpr int kX = 16;                      // values of a thread in a tile
 constexpr int kRoom = 2560;                 // candidates that fit
 constexpr int kJoinThreads = 512;
-constexpr int kMaxEntries = 8192;           // entries of a sequence's lists in the joining kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Values by size, equal ones (zeros of either sign too) by place, the lower first:
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(RowArgs<T> a) {
 // ---- joining ---------------------------------------------------------------------
 
 struct JoinArgs {
-  int32_t W, k, parts, k_shift, row_shift;
+  int32_t W, k, parts, merged, k_shift, row_shift;
   const Part* part;
   const uint64_t* lists;
   const float* scores;
@@ -400,6 +399,57 @@ __device__ __forceinline__ void join_round(const uint64_t* x, uint64_t* y, const
   }
   __syncthreads();
 }
+
+// Ahead of that, where there are many lists: `merged` lists of a row, one after another in
+// memory, into one by a warp, a list's 2^shift keys in kE registers of as many lanes. The
+// larger ones of the keys so far and the next list's from its end are the best of both, rising
+// and falling, and put in order by shift exchanges with the lanes 2^i apart. (A bisection
+// reads shared memory at 32 places at once: with four times the lists, 4,096 keys, the
+// kernel took 17 us longer, so merged 1.)
+template <int kE>
+__device__ __forceinline__ void merge_parts(const uint64_t* from, uint64_t* to, int lists, int merged, int k, int shift) {
+  const int size = 1 << shift, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int place = lane & (size - 1);  // and place + 32
+  const int at_once = kE == 1 ? 32 >> shift : 1;
+  for (int g0 = warp * at_once; g0 < lists / merged; g0 += kJoinThreads / 32 * at_once) {
+    const int g = g0 + (kE == 1 ? lane >> shift : 0);
+    const bool here = g < lists / merged;
+    const uint64_t* list = from + (int64_t)g * merged * k;
+    const auto load = [&](int j, int at) { return here && j < merged && at < k ? list[(int64_t)j * k + at] : 0; };
+    uint64_t best[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) best[e] = load(0, place + 32 * e);
+    for (int j0 = 1; j0 < merged; j0 += 4) {
+      uint64_t next[4][kE];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) next[i][e] = load(j0 + i, size - 1 - place - 32 * e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (j0 + i >= merged) break;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) best[e] = max(best[e], next[i][e]);
+        if (kE == 2) {
+          const uint64_t a = best[0], b = best[kE - 1];
+          best[0] = max(a, b);
+          best[kE - 1] = min(a, b);
+        }
+        for (int o = kE == 2 ? 16 : size / 2; o; o /= 2) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, best[e], o);
+            best[e] = (lane & o) == 0 ? max(best[e], other) : min(best[e], other);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+      if (here) to[(g << shift) + place + 32 * e] = best[e];
+  }
+}
+
 struct Lists {
   const uint64_t *keys, *places;
 };
@@ -446,13 +496,20 @@ __host__ __device__ constexpr int power_shift(int n) {
   while ((1 << s) < n) ++s;
   return s;
 }
-__host__ __device__ constexpr int join_bytes(int W, int parts, int k) {
-  const int k2 = 1 << power_shift(k), rows2 = 1 << power_shift(W);
-  return (3 * W * parts * k2 + 2 * 3 * rows2 * k2) / 2 * (int)sizeof(uint64_t) + 64;
+// Lists that merge_parts() makes one: so many that a warp's lanes have one each, or a row's.
+__host__ __device__ constexpr int merged_parts(int W, int parts, int k) {
+  const int k2 = 1 << power_shift(k), at_once = kJoinThreads / 32 * (k2 < 32 ? 32 / k2 : 1);
+  int merged = 1;
+  while (merged < parts && W * (parts / merged) > at_once) merged *= 2;
+  return merged;
 }
-// (the parts' entries are at most kMaxEntries, or the rows' where each has one part)
-constexpr int kMaxJoinBytes = 3 * (kMaxEntries / 2 + CSA2_MAX_BEAMS * kMaxK) * (int)sizeof(uint64_t) + 64;
-static_assert(CSA2_MAX_BEAMS * kMaxK <= kMaxEntries && kMaxJoinBytes <= 226 * 1024, "lists too long");
+__host__ __device__ constexpr int join_bytes(int W, int lists, int k) {
+  const int k2 = 1 << power_shift(k), rows2 = 1 << power_shift(W);
+  return (3 * lists * k2 + 2 * 3 * rows2 * k2) / 2 * (int)sizeof(uint64_t) + 64;
+}
+// (the lists merged are a row's or at most as many as the warps take at once)
+constexpr int kMaxJoinBytes = 3 * 3 * CSA2_MAX_BEAMS * kMaxK / 2 * (int)sizeof(uint64_t) + 64;
+static_assert(kJoinThreads / 32 * kMaxK <= CSA2_MAX_BEAMS * kMaxK && kMaxJoinBytes <= 226 * 1024, "lists too long");
 
 // One CTA to a sequence: each row's lists are joined by value, the rows' lists by score,
 // held to 48 bits so that their order is that of the formula to what the sums carry (in
@@ -474,9 +531,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a) {
   uint64_t* xp = y + half;
   uint64_t* yp = xp + size;
   uint64_t* keys = yp + half;
-  const int entries = a.W * a.parts << shift;
+  const int lists = a.W * (a.parts / a.merged);
   const uint64_t* from = a.lists + row0 * a.parts * k;
-  for (int i = tid; i < entries; i += kJoinThreads) keys[i] = (i & mask) < k ? from[(i >> shift) * k + (i & mask)] : 0;
+  if (shift <= 5)
+    merge_parts<1>(from, keys, a.W * a.parts, a.merged, k, shift);
+  else
+    merge_parts<2>(from, keys, a.W * a.parts, a.merged, k, shift);
   for (int w = tid >> 5; w < a.W; w += kJoinThreads / 32) {  // a warp to a row
     const Part* p = a.part + (row0 + w) * a.parts;
     float ref = -INFINITY;
@@ -516,7 +576,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a) {
   }
   __syncthreads();
   // (the number of parts is a power of two: a row's lists are joined with one another)
-  const uint64_t* rows = join_lists<false>(keys, keys + entries, nullptr, nullptr, a.W * a.parts, a.W, shift).keys;
+  const uint64_t* rows = join_lists<false>(keys, keys + (lists << shift), nullptr, nullptr, lists, a.W, shift).keys;
   // (threads past the end take part in the shuffles)
   for (int i0 = 0; i0 < size; i0 += kJoinThreads) {
     const int i = i0 + tid, w = i >> shift;
@@ -684,17 +744,16 @@ static int check_beam(int32_t B, int32_t W, int32_t V, int32_t k) {
 // Parts of a row, a power of two: at most 304 CTAs in all (two to each of 152 SMs: the
 // size of a workspace does not depend on the device) unless there are more rows, parts
 // of 2,048 values at least.
-static int beam_parts(int32_t B, int32_t W, int32_t V, int32_t k) {
+static int beam_parts(int32_t B, int32_t W, int32_t V) {
   const int64_t rows = (int64_t)B * W;
-  const int64_t entries = (int64_t)W << beam::power_shift(k);
   int64_t parts = 1;
-  while (2 * parts * rows <= 304 && 2 * parts * 2048 <= V && 2 * parts * entries <= beam::kMaxEntries) parts *= 2;
+  while (2 * parts * rows <= 304 && 2 * parts * 2048 <= V) parts *= 2;
   return (int)parts;
 }
 
 extern "C" size_t csa2_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t k) {
   if (check_beam(B, W, V, k) != CSA2_OK || B == 0 || W == 0) return 0;
-  const size_t lists = (size_t)B * W * beam_parts(B, W, V, k);
+  const size_t lists = (size_t)B * W * beam_parts(B, W, V);
   return al256(lists * sizeof(beam::Part)) + al256(lists * k * sizeof(uint64_t));
 }
 
@@ -721,7 +780,7 @@ extern "C" int csa2_beam_select(const void* logits, int32_t logits_f32, int32_t 
     return CSA2_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < csa2_beam_select_workspace_size(B, W, V, k) || !csa2_aligned(workspace, 256))
     return CSA2_ERR_WORKSPACE;
-  const int parts = beam_parts(B, W, V, k);
+  const int parts = beam_parts(B, W, V);
   const int64_t rows = (int64_t)B * W;
   beam::Part* part = (beam::Part*)workspace;
   uint64_t* lists = (uint64_t*)((char*)workspace + al256((size_t)rows * parts * sizeof(beam::Part)));
@@ -731,9 +790,10 @@ extern "C" int csa2_beam_select(const void* logits, int32_t logits_f32, int32_t 
   if (rc) return rc;
   static Csa2PerDeviceOnce once;
   if (csa2_smem_optin((const void*)beam::join_kernel, beam::kMaxJoinBytes, once) != CSA2_OK) return CSA2_ERR_CUDA;
-  beam::JoinArgs j{W, k, parts, beam::power_shift(k), beam::power_shift(W), part, lists, scores, out_scores, out_parents, out_tokens, lse};
+  const int merged = beam::merged_parts(W, parts, k);
+  beam::JoinArgs j{W, k, parts, merged, beam::power_shift(k), beam::power_shift(W), part, lists, scores, out_scores, out_parents, out_tokens, lse};
   CSA2_LAUNCH_PDL(beam::join_kernel, dim3((unsigned)B), dim3(beam::kJoinThreads),
-                  (size_t)beam::join_bytes(W, parts, k), s, j);
+                  (size_t)beam::join_bytes(W, W * (parts / merged), k), s, j);
   return CSA2_OK;
 }
 
