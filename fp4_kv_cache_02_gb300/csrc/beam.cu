@@ -416,37 +416,59 @@ __device__ __forceinline__ void merge_parts(const uint64_t* from, uint64_t* to, 
     const bool here = g < lists / merged;
     const uint64_t* list = from + (int64_t)g * merged * k;
     const auto load = [&](int j, int at) { return here && j < merged && at < k ? list[(int64_t)j * k + at] : 0; };
-    uint64_t best[kE];
+    // two at a time, the even lists and the odd ones: an exchange waits 25 cycles for its lanes
+    uint64_t best[2][kE];
+    const auto order = [&](int n) {
+      if (kE == 2)
 #pragma unroll
-    for (int e = 0; e < kE; ++e) best[e] = load(0, place + 32 * e);
-    for (int j0 = 1; j0 < merged; j0 += 4) {
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t a = best[c][0], b = best[c][kE - 1];
+          best[c][0] = max(a, b);
+          best[c][kE - 1] = min(a, b);
+        }
+      for (int o = kE == 2 ? 16 : size / 2; o; o /= 2)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            if (c >= n) continue;
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, best[c][e], o);
+            best[c][e] = (lane & o) == 0 ? max(best[c][e], other) : min(best[c][e], other);
+          }
+    };
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < kE; ++e) best[c][e] = load(c, c == 0 || merged > 2 ? place + 32 * e : size - 1 - place - 32 * e);
+    for (int j0 = 2; j0 < merged; j0 += 4) {
       uint64_t next[4][kE];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < kE; ++e) next[i][e] = load(j0 + i, size - 1 - place - 32 * e);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; i += 2) {
         if (j0 + i >= merged) break;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) best[e] = max(best[e], next[i][e]);
-        if (kE == 2) {
-          const uint64_t a = best[0], b = best[kE - 1];
-          best[0] = max(a, b);
-          best[kE - 1] = min(a, b);
-        }
-        for (int o = kE == 2 ? 16 : size / 2; o; o /= 2) {
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            const uint64_t other = __shfl_xor_sync(0xffffffffu, best[e], o);
-            best[e] = (lane & o) == 0 ? max(best[e], other) : min(best[e], other);
-          }
-        }
+          for (int e = 0; e < kE; ++e) best[c][e] = max(best[c][e], next[i + c][e]);
+        order(2);
       }
+    }
+    if (merged > 1) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        uint64_t other = best[1][kE - 1 - e];
+        if (merged > 2) other = __shfl_xor_sync(0xffffffffu, other, kE == 2 ? 31 : size - 1);
+        else other = best[1][e];
+        best[0][e] = max(best[0][e], other);
+      }
+      order(1);
     }
 #pragma unroll
     for (int e = 0; e < kE; ++e)
-      if (here) to[(g << shift) + place + 32 * e] = best[e];
+      if (here) to[(g << shift) + place + 32 * e] = best[0][e];
   }
 }
 
@@ -741,19 +763,20 @@ static int check_beam(int32_t B, int32_t W, int32_t V, int32_t k) {
   return CSA2_OK;
 }
 
-// Parts of a row, a power of two: at most 304 CTAs in all (two to each of 152 SMs: the
-// size of a workspace does not depend on the device) unless there are more rows, parts
-// of 2,048 values at least.
-static int beam_parts(int32_t B, int32_t W, int32_t V) {
+// Parts of a row, a power of two, of 2,048 values at least: at most 608 CTAs in all (four to
+// each of 152 SMs: the size of a workspace does not depend on the device), 304 for k > 16,
+// whose lists take longer (128 rows of 128,259 fp32, k 16: 22.4 us with 608, 23.8 with 304;
+// 32 rows, k 32: 19.9 and 17.6), unless there are more rows.
+static int beam_parts(int32_t B, int32_t W, int32_t V, int32_t k) {
   const int64_t rows = (int64_t)B * W;
   int64_t parts = 1;
-  while (2 * parts * rows <= 304 && 2 * parts * 2048 <= V) parts *= 2;
+  while (2 * parts * rows <= (k <= 16 ? 608 : 304) && 2 * parts * 2048 <= V) parts *= 2;
   return (int)parts;
 }
 
 extern "C" size_t csa2_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t k) {
   if (check_beam(B, W, V, k) != CSA2_OK || B == 0 || W == 0) return 0;
-  const size_t lists = (size_t)B * W * beam_parts(B, W, V);
+  const size_t lists = (size_t)B * W * beam_parts(B, W, V, k);
   return al256(lists * sizeof(beam::Part)) + al256(lists * k * sizeof(uint64_t));
 }
 
@@ -780,7 +803,7 @@ extern "C" int csa2_beam_select(const void* logits, int32_t logits_f32, int32_t 
     return CSA2_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < csa2_beam_select_workspace_size(B, W, V, k) || !csa2_aligned(workspace, 256))
     return CSA2_ERR_WORKSPACE;
-  const int parts = beam_parts(B, W, V);
+  const int parts = beam_parts(B, W, V, k);
   const int64_t rows = (int64_t)B * W;
   beam::Part* part = (beam::Part*)workspace;
   uint64_t* lists = (uint64_t*)((char*)workspace + al256((size_t)rows * parts * sizeof(beam::Part)));
