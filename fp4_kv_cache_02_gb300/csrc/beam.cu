@@ -95,6 +95,12 @@ __device__ __forceinline__ float ex2(float x) {
   return e;
 }
 
+__device__ __forceinline__ float warp_max(float x) {  // (NaN only where all are)
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
 template <typename T>
 struct Vec;  // 16 bytes of logits
 template <>
@@ -222,9 +228,11 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(RowArgs<T> a) {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < kX; ++i) top = fmaxf(top, x[i]);
-    if (top > ref) {
-      if (ref > -INFINITY) sum *= exp2f((ref - top) * kLog2e);
-      ref = top;
+    // (one reference for a warp: each lane's own rises in most tiles)
+    const float warp_top = warp_max(top);
+    if (warp_top > ref) {
+      if (ref > -INFINITY) sum *= exp2f((ref - warp_top) * kLog2e);
+      ref = warp_top;
     }
     // (x - ref first: exact where it counts, and 0 for a row of the type's lowest
     // value, whose product with log2 e is infinite; with ref +inf the sum is NaN)
