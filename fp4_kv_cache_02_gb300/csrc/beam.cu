@@ -663,6 +663,7 @@ __device__ __constant__ const int kPlaneBytes[4] = {kKvBytes, kKvScales, kIkByte
 // if a lower row has the same parent. Every block finds that out for itself from
 // the parents; nothing that is read is written.
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(ReorderArgs a) {
+  pdl_begin();
   const int32_t r = blockIdx.x;
   const int32_t p = a.parents[r];
   if (p < 0 || p >= a.rows_in) {
@@ -727,6 +728,9 @@ constexpr int kRowSlice = kReorderThreads * 16 * 4;  // bytes of a row to a bloc
 __global__ void __launch_bounds__(kReorderThreads)
     rows_copy_kernel(const uint8_t* __restrict__ src, int64_t rows_in, int64_t row_bytes, int64_t slices,
                      const int32_t* __restrict__ parents, uint8_t* __restrict__ dst) {
+  // (no pdl_launch_dependents(): the selected attention behind reads its windows, which
+  // this may have written, before its own wait)
+  pdl_wait();
   const int64_t r = blockIdx.x / slices, slice = blockIdx.x % slices;
   const int32_t p = parents[r];
   if (p < 0 || p >= rows_in) {
@@ -851,8 +855,8 @@ extern "C" int csa2_paged_reorder(const int32_t* parents, const int32_t* fresh_p
   if (page_table_out == page_table || n_visible_out == n_visible) return CSA2_ERR_INVALID_ARG;
   beam::ReorderArgs a{parents, fresh_pages, R, rows_in, layers, {kv_data, kv_scale, ik_data, ik_scale}, pages, n_visible,
                       page_table_out, n_visible_out};
-  beam::reorder_kernel<<<dim3((unsigned)R, (unsigned)(1 + layers)), beam::kReorderThreads, 0, (cudaStream_t)stream>>>(a);
-  CSA2_CHECK_LAUNCH();
+  CSA2_LAUNCH_PDL(beam::reorder_kernel, dim3((unsigned)R, (unsigned)(1 + layers)), dim3(beam::kReorderThreads), (size_t)0,
+                  (cudaStream_t)stream, a);
   return CSA2_OK;
 }
 
@@ -865,8 +869,7 @@ extern "C" int csa2_reorder_rows(const void* src, int64_t rows_in, int64_t row_b
   if ((!src && rows_in != 0) || !parents || !dst || src == dst) return CSA2_ERR_INVALID_ARG;
   const int64_t slices = (row_bytes + beam::kRowSlice - 1) / beam::kRowSlice;
   if (slices > 0x7FFFFFFFLL / R) return CSA2_ERR_UNSUPPORTED_SHAPE;
-  beam::rows_copy_kernel<<<(unsigned)(R * slices), beam::kReorderThreads, 0, (cudaStream_t)stream>>>(
-      (const uint8_t*)src, rows_in, row_bytes, slices, parents, (uint8_t*)dst);
-  CSA2_CHECK_LAUNCH();
+  CSA2_LAUNCH_PDL(beam::rows_copy_kernel, dim3((unsigned)(R * slices)), dim3(beam::kReorderThreads), (size_t)0,
+                  (cudaStream_t)stream, (const uint8_t*)src, rows_in, row_bytes, slices, parents, (uint8_t*)dst);
   return CSA2_OK;
 }
