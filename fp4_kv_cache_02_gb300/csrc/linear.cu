@@ -1258,7 +1258,7 @@ static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stre
   CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
   // Tiles for half of the SMs and more: in equal runs (32 tokens by 32,768 x 4,096, 256
   // tiles: 22.1 us, 26.8 as clusters; 16 tokens by 128,259 x 4,096: 48.7 and 54.3). Fewer:
-  // clusters (8 tokens by 4,096 x 32,768, 32 tiles: 20.2 us, 30.1 in runs, whose tiles have
+  // clusters (8 tokens by 4,096 x 32,768, 32 tiles: 19.7 us, 30.1 in runs, whose tiles have
   // six parts). Of those, two CTAs to an SM only where clusters of four fill them (clusters
   // of eight at two to an SM do not always fit at once: four tokens by 4,096 x 32,768 with
   // E4M3 scales took 26 us so, and 19.9 with clusters of four, one CTA to an SM).
