@@ -42,7 +42,7 @@ constexpr int kSumWarps = 8;                // warps that make terms and sum col
 constexpr int kProducerWarp = kSumWarps;
 constexpr int kMmaWarp = kSumWarps + 1;
 constexpr int kThreads = 32 * (kSumWarps + 2);
-constexpr int kTermThreads = 256;
+constexpr int term_threads(bool e4m3) { return e4m3 ? 512 : 256; }  // of terms_kernel, eight channels each
 constexpr int kMinExp = -100;               // of a block's largest: all the terms' scales are E8M0 then
 
 // Groups of scales in a block of 256 inputs: a group is what one tcgen05.cp moves,
@@ -112,13 +112,13 @@ __device__ __forceinline__ uint32_t top_bits(uint4 v) {
 // product as the token's factor. With E8M0 scales base is 1: the first scale of a block
 // with E = 127 is 2^128. With E4M3 scales it is such that the largest block's first one
 // is 2^8, the largest power of two that E4M3 holds, and the terms' common ratios are left
-// to sum_terms. A row that holds an infinity or a NaN has the factor NaN.
-template <bool kE4M3>
-__device__ __forceinline__ int base_exp(uint32_t top) { return kE4M3 ? block_exp(top) - 7 : 1; }
-template <bool kE4M3>
+// to sum_terms. A row that holds an infinity or a NaN has NaN for the scales of that block
+// (E8M0: the factor is 2 for every token, and none has to be found out: looked up by all
+// CTAs, eight words a token, it cost 2 us for 8 tokens by 4,096 x 32,768) or as its factor.
+constexpr int kE8M0Base = 1;
+__device__ __forceinline__ int base_exp(uint32_t top) { return block_exp(top) - 7; }
 __device__ __forceinline__ float factor_of(uint32_t top) {
-  return top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                        : __uint_as_float((uint32_t)(base_exp<kE4M3>(top) + 127) << 23);
+  return top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(base_exp(top) + 127) << 23);
 }
 
 // Base-8 digits (24 bits) one to a nibble; each nibble's highest bit is not defined.
@@ -188,7 +188,7 @@ __device__ __forceinline__ void put_terms(uint4 v, int base, int tl, uint8_t* da
 #pragma unroll
   for (int j = 0; j < kTerms; ++j) {
     *reinterpret_cast<uint32_t*>(to + tc::sw128_offset(j, lane / 4)) = digit_codes(d[7 - j]);
-    if (lane % kLanesPer == 0) s_to[16 * j] = (uint8_t)(kE4M3 ? e4m3 : (uint32_t)(rel + 127 - 3 * j));
+    if (lane % kLanesPer == 0) s_to[16 * j] = (uint8_t)(kE4M3 ? e4m3 : m >= 0x7F80u ? 0xFFu : (uint32_t)(rel + 127 - 3 * j));
   }
 }
 
@@ -200,46 +200,40 @@ struct TermArgs {
   int32_t* joined;
 };
 
-// The terms of all tokens, ahead of the product: one CTA takes 4,096 channels of a
-// token, twice eight to a thread. A token's factor is the sum of factor[t][0 .. factors - 1]:
-// with E4M3 scales one (every CTA looks at the whole row for its base), with E8M0 one to
-// a CTA (of 32,768 channels a look at the whole row took 3 us longer).
+// The terms of all tokens, ahead of the product: eight channels of a token to a thread.
+// With E4M3 scales every CTA of a token looks at its whole row for its base.
 template <bool kE4M3>
-__global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
+__global__ void __launch_bounds__(term_threads(kE4M3)) terms_kernel(TermArgs a) {
   pdl_begin();
-  __shared__ uint32_t s_max[kTermThreads / 32];
+  constexpr int kThreads = term_threads(kE4M3);
+  static_assert(kThreads >= kStreamCtas, "a count to a thread");
   if (blockIdx.x == 0 && threadIdx.x < kStreamCtas) a.joined[threadIdx.x] = 0;
   const int32_t t = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
   const uint16_t* row = a.x + (int64_t)t * a.n_in;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t k = ((int64_t)slice * 2 * kTermThreads + threadIdx.x) * 8;
-  constexpr int kStep = kTermThreads * 8;
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  const uint4 v0 = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : none;
-  const uint4 v1 = k + kStep < a.n_in ? *reinterpret_cast<const uint4*>(row + k + kStep) : none;
-  uint32_t top = max(top_bits(v0), top_bits(v1));
-  if (kE4M3 && a.slices > 1)
+  const int64_t k = ((int64_t)slice * kThreads + threadIdx.x) * 8;
+  const uint4 v = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0, 0, 0, 0);
+  int base = kE8M0Base;
+  if constexpr (kE4M3) {
+    __shared__ uint32_t s_max[kThreads / 32];
+    uint32_t top = top_bits(v);
+    if (a.slices > 1)
 #pragma unroll 4
-    for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kStep)
-      top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_max[warp] = top;
-  __syncthreads();
-  top = s_max[0];
+      for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kThreads * 8)
+        top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) s_max[warp] = top;
+    __syncthreads();
+    top = s_max[0];
 #pragma unroll
-  for (int i = 1; i < kTermThreads / 32; ++i) top = max(top, s_max[i]);
-  if (threadIdx.x == 0 && (!kE4M3 || slice == 0)) {
-    const float factor = factor_of<kE4M3>(top);
-    a.factor[kE4M3 ? t : (int64_t)t * a.slices + slice] = slice == 0 || isnan(factor) ? factor : 0.0f;
+    for (int i = 1; i < kThreads / 32; ++i) top = max(top, s_max[i]);
+    if (threadIdx.x == 0 && slice == 0) a.factor[t] = factor_of(top);
+    base = base_exp(top);
   }
-  const int base = base_exp<kE4M3>(top);
-  const auto put = [&](uint4 v, int32_t c) {  // (a warp has one chunk)
-    uint8_t* block = a.terms + ((int64_t)(t / kTileTokens) * a.chunks + c) * terms_bytes(kE4M3, a.n);
-    put_terms<kE4M3>(v, base, t % kTileTokens, block, block + a.n * (kChunk / 2), column_groups(a.n), lane);
-  };
-  const int32_t c = (int32_t)(k / kChunk);
-  if (c < a.chunks) put(v0, c);
-  if (c + kStep / kChunk < a.chunks) put(v1, c + kStep / kChunk);
+  const int32_t c = (int32_t)(k / kChunk);  // (a warp has one chunk)
+  if (c >= a.chunks) return;
+  uint8_t* block = a.terms + ((int64_t)(t / kTileTokens) * a.chunks + c) * terms_bytes(kE4M3, a.n);
+  put_terms<kE4M3>(v, base, t % kTileTokens, block, block + a.n * (kChunk / 2), column_groups(a.n), lane);
 }
 
 // ---- the product -----------------------------------------------------------------
@@ -250,13 +244,13 @@ struct Params {
   const uint8_t* weights;
   const uint16_t* x;
   const uint8_t* terms;
-  const float* factor;
+  const float* factor;  // [tokens], with E4M3 scales
   int32_t* joined;  // stream_kernel: parts that are there of the tile that CTA g is the first to have a part of
   float* parts;     // stream_kernel: [CTA][2][tokens of a tile][128]
   __nv_bfloat16* out_bf16;
   float* out_f32;
   float scale;
-  int32_t T, n_out, n_in, chunks, token_tiles, n, stages, split, factors;
+  int32_t T, n_out, n_in, chunks, token_tiles, n, stages, split;
   int64_t units;          // tiles x chunks
   uint32_t tmem_cols;
 };
@@ -328,12 +322,10 @@ __device__ __forceinline__ float sum_terms(const uint32_t* v) {
   return y;
 }
 
-// A token's factor, of which terms_kernel's CTAs wrote a part each.
-__device__ __forceinline__ float token_factor(const Params& p, int64_t t) {
-  float factor = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < p.factors; ++i) factor += __ldcg(p.factor + t * p.factors + i);
-  return factor;
+// Token t's factor out of its lane.
+template <bool kE4M3>
+__device__ __forceinline__ float factor_from(float lanes, int t) {
+  return kE4M3 ? __shfl_sync(0xffffffffu, lanes, t & 31) : (float)(1 << kE8M0Base);
 }
 
 __device__ __forceinline__ void put_out(const Params& p, int64_t t, int64_t row, float y) {
@@ -422,23 +414,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
     const int32_t k = (c0 + c) * kChunk + lane * 8;
     return k < p.n_in ? *reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.n_in + k) : make_uint4(0, 0, 0, 0);
   };
-  uint32_t top[kFewTokens] = {};
-  const auto write_tops = [&]() {
-#pragma unroll
-    for (int t = 0; t < kFewTokens; ++t) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, top[t]);
-      if (lane == 0) s_top[warp * kFewTokens + t] = m;
-    }
-  };
   uint4 ahead_v = make_uint4(0, 0, 0, 0);
   if (kOwnTerms && warp < kSumWarps) {
     pdl_wait();  // x; and the outputs may have readers before this call
     if (kE4M3) {
+      uint32_t top[kFewTokens] = {};
       for (int c = warp; c < n_chunks; c += kSumWarps)
 #pragma unroll
         for (int t = 0; t < kFewTokens; ++t)
           if (t < p.T) top[t] = max(top[t], top_bits(channels(c, t)));
-      write_tops();
+#pragma unroll
+      for (int t = 0; t < kFewTokens; ++t) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, top[t]);
+        if (lane == 0) s_top[warp * kFewTokens + t] = m;
+      }
     } else if (warp < n_chunks * p.T) {
       ahead_v = channels(warp / p.T, warp % p.T);
     }
@@ -492,13 +481,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
   } else {
     if (!kOwnTerms) pdl_wait();  // the factors; and the outputs may have readers before this call
   }
-  if (kOwnTerms && warp < kSumWarps) {
-    const auto top_of = [&](int t) {
-      uint32_t m = s_top[t];
+  const auto top_of = [&](int t) {  // kOwnTerms, E4M3
+    uint32_t m = s_top[t];
 #pragma unroll
-      for (int i = 1; i < kSumWarps; ++i) m = max(m, s_top[i * kFewTokens + t]);
-      return m;
-    };
+    for (int i = 1; i < kSumWarps; ++i) m = max(m, s_top[i * kFewTokens + t]);
+    return m;
+  };
+  if (kOwnTerms && warp < kSumWarps) {
     // No more warps than there are (stage, token) places: a warp's last task is then at
     // most a round of the ring behind its next, so that the stage it waits for is in the
     // phase before the awaited one or later (a barrier tells two phases apart, not three).
@@ -508,24 +497,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
       const uint4 v = !kE4M3 && i == warp ? ahead_v : channels(c, t);
       const bool ok = tc::mbar_wait_bounded(&empty[s], ((uint32_t)(c / p.stages) & 1u) ^ 1u, s_abort, &g_linear_error);
       if (!__all_sync(0xffffffffu, ok)) break;
-      uint32_t whole = 0;  // (E8M0 scales need no base of the token's own)
-      if (kE4M3) {
-        whole = top_of(t);
-      } else {
-        const uint32_t m = top_bits(v);
-#pragma unroll
-        for (int j = 0; j < kFewTokens; ++j)
-          if (j == t) top[j] = max(top[j], m);
-      }
       uint8_t* data = ring + s * stage_bytes + block_bytes(kE4M3);
-      put_terms<kE4M3>(v, base_exp<kE4M3>(whole), t, data, data + p.n * (kChunk / 2), 1, lane);
+      put_terms<kE4M3>(v, kE4M3 ? base_exp(top_of(t)) : kE8M0Base, t, data, data + p.n * (kChunk / 2), 1, lane);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&ready[s]);
-    }
-    if (!kE4M3) {
-      write_tops();
-      sync_sum_warps();
     }
   }
 
@@ -533,16 +509,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
   if (warp < kSumWarps) {
     // lane t holds token t's factor (asked for one by one they cost a trip to L2 each)
     float factor = 0.0f;
-    if (lane < nt) {
-      if constexpr (kOwnTerms) {
-        uint32_t m = s_top[lane];
-#pragma unroll
-        for (int i = 1; i < kSumWarps; ++i) m = max(m, s_top[i * kFewTokens + lane]);
-        factor = factor_of<kE4M3>(m);
-      } else {
-        factor = token_factor(p, t0 + lane);
-      }
-    }
+    if (kE4M3 && lane < nt) factor = kOwnTerms ? factor_of(top_of(lane)) : __ldcg(p.factor + t0 + lane);
     const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(acc_full, 0, s_abort, &g_linear_error));
     if (ok) tc::tc_fence_after();
     const int row = (warp & 3) * 32 + lane;
@@ -556,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
       }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const float y = sum_terms<kE4M3>(v + 8 * h) * __shfl_sync(0xffffffffu, factor, (t + h) & 31);
+        const float y = sum_terms<kE4M3>(v + 8 * h) * factor_from<kE4M3>(factor, t + h);
         if (t + h >= min(first + half, nt) || !ok) continue;
         if (p.split > 1)
           sums[(t + h) * kRows + row] = y;
@@ -726,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
       chunk = 0;
       // lane t holds token t's factor
       float factor = 0.0f;
-      if (lane < nt) factor = token_factor(p, t0 + lane);
+      if (kE4M3 && lane < nt) factor = __ldcg(p.factor + t0 + lane);
       // A tile in parts: the CTAs that its first and last chunk belong to. Where there are
       // two and the other's part is there (that of a run's last tile mostly is: the next
       // CTA began with it), it is added to this one's, which need not be written.
@@ -763,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
           tc::tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 4; ++h)
-            y[i + h] = sum_terms<kE4M3>(v + 8 * h) * __shfl_sync(0xffffffffu, factor, (first + i + h) & 31);
+            y[i + h] = sum_terms<kE4M3>(v + 8 * h) * factor_from<kE4M3>(factor, first + i + h);
         }
         tc::tc_fence_before();
       }
@@ -1120,7 +1087,10 @@ static int64_t token_tiles_of(int32_t n_tokens) {
 }
 
 // CTAs to a token's terms.
-static int64_t slices_of(int32_t n_in) { return ((int64_t)n_in + linear::kTermThreads * 16 - 1) / (linear::kTermThreads * 16); }
+static int64_t slices_of(int32_t n_in, bool e4m3) {
+  const int per = linear::term_threads(e4m3) * 8;
+  return ((int64_t)n_in + per - 1) / per;
+}
 
 // Workspace of a product of more than kFewTokens: the tokens' factors, the counts and
 // parts of the tiles that CTAs share, the terms.
@@ -1130,7 +1100,7 @@ struct LinearSpace {
 static LinearSpace space_of(int32_t T, int32_t n_in, bool e4m3) {
   const int n = tile_columns(T);
   LinearSpace s;
-  s.joined = al256((size_t)T * (e4m3 ? 1 : slices_of(n_in)) * sizeof(float));
+  s.joined = e4m3 ? al256((size_t)T * sizeof(float)) : 0;
   s.parts = s.joined + al256(linear::kStreamCtas * sizeof(int32_t));
   s.terms = s.parts + (size_t)linear::kStreamCtas * 2 * (n / linear::kTerms) * linear::kRows * sizeof(float);
   s.bytes = s.terms + (size_t)token_tiles_of(T) * (size_t)chunks_of(n_in) * linear::terms_bytes(e4m3, n);
@@ -1252,10 +1222,9 @@ static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stre
   p.joined = (int32_t*)(workspace + space.joined);
   p.parts = (float*)(workspace + space.parts);
   p.terms = workspace + space.terms;
-  const int64_t slices = slices_of(p.n_in);
-  p.factors = kE4M3 ? 1 : (int32_t)slices;
+  const int64_t slices = slices_of(p.n_in, kE4M3);
   TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
-  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
+  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(term_threads(kE4M3)), (size_t)0, stream, ta);
   // Tiles for half of the SMs and more: in equal runs (32 tokens by 32,768 x 4,096, 256
   // tiles: 22.1 us, 26.8 as clusters; 16 tokens by 128,259 x 4,096: 48.7 and 54.3). Fewer:
   // clusters (8 tokens by 4,096 x 32,768, 32 tiles: 19.7 us, 30.1 in runs, whose tiles have
@@ -1280,7 +1249,7 @@ extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8
     return CSA2_ERR_ALIGNMENT;
   // a grid of at most 2^31 - 1 blocks for each kernel
   if (row_tiles_of(n_out) * token_tiles_of(n_tokens) > 0x0FFFFFFFLL ||
-      (int64_t)n_tokens * slices_of(n_in) > 0x7FFFFFFFLL)
+      (int64_t)n_tokens * slices_of(n_in, format == CSA2_FP4_E4M3) > 0x7FFFFFFFLL)
     return CSA2_ERR_UNSUPPORTED_SHAPE;
   const size_t need = csa2_fp4_linear_workspace_size(n_tokens, n_in, format);
   if (!workspace || workspace_bytes < need || !csa2_aligned(workspace, 256)) return CSA2_ERR_WORKSPACE;
