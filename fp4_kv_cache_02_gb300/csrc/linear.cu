@@ -34,7 +34,7 @@ constexpr int kRows = 128;                  // outputs to a block
 constexpr int kDataBytes = kRows * kChunk / 2;
 constexpr int kTileTokens = 32;             // tokens to a tile: 256 columns
 constexpr int kTermTokens = 64;             // tokens that enter as terms
-constexpr int kFewTokens = 4;               // tokens whose terms the product's own warps make
+constexpr int kFewTokens = 3;               // tokens whose terms the product's own warps make
 constexpr int kMaxSplit = 8;                // CTAs that split the inputs of such a product
 constexpr int kStreamCtas = 152;            // of a product of more tokens: one to an SM
 constexpr int kMaxStages = 8;
@@ -358,7 +358,7 @@ __device__ __forceinline__ void add_parts(const Params& p, const float* sums, in
 // ---- few tiles -------------------------------------------------------------------
 // Products of too few tiles (128 outputs x up to 32 tokens) to fill the SMs, and those
 // of few tokens. The CTAs of a cluster split a tile's chunks, and their sums are added in
-// rank order out of one another's shared memory. kOwnTerms: up to four tokens, whose terms
+// rank order out of one another's shared memory. kOwnTerms: up to three tokens, whose terms
 // each CTA makes itself: ahead of the product they would cost a launch and a trip through
 // L2 (4 us of 15 for a token by 32,768 x 4,096 weights).
 //   warp 8     producer: a bulk copy of a block of weights per stage (and one of the
@@ -1117,12 +1117,30 @@ extern "C" size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in,
   return space_of(is_wide(n_tokens, n_in) ? linear::kTermTokens : n_tokens, n_in, format == CSA2_FP4_E4M3).bytes;
 }
 
+// CTAs in clusters of that many that are on the SMs at once, one to an SM: a cluster lies
+// within a group of SMs, and clusters of eight leave 32 of the 152 SMs over (as the runtime's
+// occupancy query says; past that a product takes a second wave: 8 tokens by 2,048 x 2,048
+// in 16 clusters of eight took 8.4 us).
+static int64_t cluster_room(int n) { return n == 8 ? 120 : n == 4 ? 144 : linear::kStreamCtas; }
+
 // Stages that fit beside `acc` accumulator columns.
 static int stages_for(bool e4m3, int n, int acc, int cols, int smem) {
   const int by_smem = (smem - linear::kHeadBytes - 1024) / (linear::block_bytes(e4m3) + linear::terms_bytes(e4m3, n));
   const int by_cols = (cols - acc) / linear::scale_cols(e4m3, n);
   const int most = by_smem < by_cols ? by_smem : by_cols;
   return most < linear::kMaxStages ? most : linear::kMaxStages;
+}
+
+// CTAs to a tile: for all SMs; two to an SM where each has four chunks and more to itself
+// (a token by 4,096 x 32,768: 14.8 us with 256 CTAs, 16.0 with 128; by 4,096 x 4,096: 6.2
+// and 5.7).
+static int split_of(int64_t tiles, int32_t chunks, int ctas) {
+  int split = 1;
+  while (split < linear::kMaxSplit && split * 2 <= chunks &&
+         (tiles * split * 2 <= cluster_room(split * 2) ||
+          (tiles * split * 2 <= ctas * cluster_room(split * 2) && chunks >= 8 * split)))
+    split *= 2;
+  return split;
 }
 
 template <bool kE4M3, bool kOwnTerms, int kCtas>
@@ -1134,12 +1152,7 @@ static int launch_split(linear::Params p, cudaStream_t stream) {
   const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
   p.tmem_cols = kCols;
   p.stages = stages_for(kE4M3, p.n, p.n, kCols, kSmem);
-  p.split = 1;
-  // CTAs for all SMs; two to an SM where each has four chunks and more to itself (a token
-  // by 4,096 x 32,768: 14.8 us with 256 CTAs, 16.0 with 128; by 4,096 x 4,096: 6.2 and 5.7).
-  while (p.split < kMaxSplit && p.split * 2 <= p.chunks &&
-         (tiles * p.split * 2 <= kStreamCtas || (tiles * p.split * 2 <= kCtas * kStreamCtas && p.chunks >= 8 * p.split)))
-    p.split *= 2;
+  p.split = split_of(tiles, p.chunks, kCtas);
   if (csa2_launch_pdl_cluster(split_kernel<kE4M3, kOwnTerms, kCtas>, dim3((unsigned)(tiles * p.split)), dim3(kThreads),
                               (size_t)kSmem, stream, (unsigned)p.split, p) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -1198,7 +1211,7 @@ static int launch_wide(linear::Params p, cudaStream_t stream) {
     return CSA2_ERR_CUDA;
   const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
   int split = 1;
-  while (split < kMaxSplit && split * 2 <= p.chunks && tiles * split * 2 <= kStreamCtas) split *= 2;
+  while (split < kMaxSplit && split * 2 <= p.chunks && tiles * split * 2 <= cluster_room(split * 2)) split *= 2;
   wp.p.split = split;
   if (csa2_launch_pdl_cluster(wide_kernel<kE4M3>, dim3((unsigned)(tiles * split)), dim3(kWideThreads), (size_t)kSmem, stream,
                               (unsigned)split, map, wp) != cudaSuccess) {
@@ -1211,10 +1224,11 @@ static int launch_wide(linear::Params p, cudaStream_t stream) {
 template <bool kE4M3>
 static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stream) {
   using namespace linear;
-  // Up to four tokens (three with E4M3 scales, whose base is a second look at x), and row
-  // tiles for one wave: in one launch (a token by 32,768 x 4,096: 13.9 us, 16.6 with the
-  // terms ahead; four: 15.3 and 16.9; a token by 131,072 x 4,096: 47.2 and 46.6).
-  if (p.T <= (kE4M3 ? kFewTokens - 1 : kFewTokens) && row_tiles_of(p.n_out) <= 2 * kStreamCtas)
+  // Up to three tokens, and row tiles for one wave: in one launch (E8M0, a token by 4,096 x
+  // 32,768: 13.8 us, 14.5 with the terms ahead; three 13.9 and 14.5; four 15.3 and 14.5; a
+  // token by 131,072 x 4,096: 47.2 and 46.6). With E4M3 scales, whose base is a second look
+  // at x, one or two (two by 4,096 x 16,384: 10.5 and 11.2; by 16,384 x 16,384 29.9 and 28.0).
+  if (p.T <= (kE4M3 ? (p.n_in <= 4096 ? 2 : 1) : kFewTokens) && row_tiles_of(p.n_out) <= 2 * kStreamCtas)
     return launch_split<kE4M3, true, 2>(p, stream);
   if (is_wide(p.T, p.n_in)) return launch_wide<kE4M3>(p, stream);
   const LinearSpace space = space_of(p.T, p.n_in, kE4M3);
@@ -1225,16 +1239,18 @@ static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stre
   const int64_t slices = slices_of(p.n_in, kE4M3);
   TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
   CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(term_threads(kE4M3)), (size_t)0, stream, ta);
-  // Tiles for half of the SMs and more: in equal runs (32 tokens by 32,768 x 4,096, 256
-  // tiles: 22.1 us, 26.8 as clusters; 16 tokens by 128,259 x 4,096: 48.7 and 54.3). Fewer:
-  // clusters (8 tokens by 4,096 x 32,768, 32 tiles: 19.7 us, 30.1 in runs, whose tiles have
-  // six parts). Of those, two CTAs to an SM only where clusters of four fill them (clusters
-  // of eight at two to an SM do not always fit at once: four tokens by 4,096 x 32,768 with
-  // E4M3 scales took 26 us so, and 19.9 with clusters of four, one CTA to an SM).
+  // Tiles for one wave (of up to 16 tokens two CTAs to an SM): clusters, or CTAs by
+  // themselves. More: in equal runs, whose joins take 3 us (E8M0, 5 tokens by 4,096 x 16,384,
+  // 128 tiles: 10.5 us, 13.6 in runs; by 32,768 x 4,096: 14.4 and 17.1; 32 tokens, 256 tiles:
+  // 26.8 and 21.8 (E4M3); 16 tokens by 4,096 x 128,259: 51.7 and 48.0).
+  // Two CTAs to an SM, each with half of the stages, where a tile gets more of them so (5
+  // tokens by 16,384 x 4,864: 12.2 us, 15.6 with one; but 8 by 32,768 x 4,096, four to a tile
+  // either way, 18.8 and 17.6).
   const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
-  if (tiles > kStreamCtas / 2) return launch_stream<kE4M3>(p, stream);
-  return p.n <= 128 && tiles * 4 > kStreamCtas ? launch_split<kE4M3, false, 2>(p, stream)
-                                               : launch_split<kE4M3, false, 1>(p, stream);
+  if (tiles > (p.n <= 128 ? 2 : 1) * kStreamCtas) return launch_stream<kE4M3>(p, stream);
+  return p.n <= 128 && (tiles > kStreamCtas || split_of(tiles, p.chunks, 2) > split_of(tiles, p.chunks, 1))
+             ? launch_split<kE4M3, false, 2>(p, stream)
+             : launch_split<kE4M3, false, 1>(p, stream);
 }
 
 extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8_t* weights, int32_t n_out, int32_t n_in,
