@@ -547,9 +547,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
 // ---- many tiles ------------------------------------------------------------------
 // Tiles of 128 outputs x up to 32 tokens. All tiles' chunks form one list (a row tile's
 // token tiles one after another, so that its weights are in L2 for them), cut into one
-// equal run to an SM. A run begins and ends inside tiles: their parts go through the
-// workspace, and the CTA that brings a tile's last part adds them, in the list's order
-// whoever that is. Nobody waits for another CTA.
+// equal run to an SM. A run begins and ends inside tiles. There are more tiles than runs, so
+// that no run is shorter than a tile, and a tile has two parts at most: the CTA that is
+// done with its own last adds the other's, out of the workspace (in either order the
+// same). Nobody waits for another CTA.
 //   warp 8     producer: bulk copies of a block of weights and one of terms per stage,
 //              ahead across tiles;
 //   warp 9     scales to tensor memory, products; two accumulators up to 16 tokens;
@@ -694,25 +695,24 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
       // lane t holds token t's factor
       float factor = 0.0f;
       if (kE4M3 && lane < nt) factor = __ldcg(p.factor + t0 + lane);
-      // A tile in parts: the CTAs that its first and last chunk belong to. Where there are
-      // two and the other's part is there (that of a run's last tile mostly is: the next
-      // CTA began with it), it is added to this one's, which need not be written.
+      // A tile in two parts, the other one the next CTA's or the last one's. Where that is
+      // there already (the next CTA began with it: mostly it is), it is added to this one's,
+      // which need not be written.
       const bool shared = !begins || !ends;
-      int64_t g0 = g, g1 = g;
+      int* joined = p.joined + (begins ? g : g - 1);
+      const float* from = part_of(begins ? g + 1 : g - 1, !begins) + (int64_t)first * kRows + row;
       bool complete = false;
       float other[16];
-      if (shared) {
-        g0 = ((tile * p.chunks + 1) * G - 1) / p.units;
-        g1 = (((tile + 1) * p.chunks) * G - 1) / p.units;
-        if (g1 - g0 == 1) {
-          if (threadIdx.x == 0) s_complete[begins] = load_acquire(&p.joined[g0]);
-          sync_sum_warps();
-          complete = s_complete[begins] != 0;
-          const float* from = part_of(g == g0 ? g1 : g0, g != g0) + (int64_t)first * kRows + row;
+      const auto load_other = [&]() {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (complete && i < half && first + i < nt) other[i] = __ldcg(from + i * kRows);
-        }
+        for (int i = 0; i < 16; ++i)
+          if (i < half && first + i < nt) other[i] = __ldcg(from + i * kRows);
+      };
+      if (shared) {
+        if (threadIdx.x == 0) s_complete[begins] = load_acquire(joined);
+        sync_sum_warps();
+        complete = s_complete[begins] != 0;
+        if (complete) load_other();
       }
       // (after a wait that ran out the warps still meet at the same barriers: the waits of
       // an aborted run end at once, and nothing is read or stored)
@@ -739,47 +739,22 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
       if (++a == accs) a = 0, ++acc_turn;
 
       const int mine = ok ? min(half, nt - first) : 0;  // (none or fewer at the last tokens)
-      if (complete) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] += other[i];  // (in either order the same)
-      }
-      if (!shared || complete) {
+      if (shared && !complete) {
+        float* to = part_of(g, begins) + (int64_t)first * kRows + row;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (i < mine) put_out(p, t0 + first + i, out_row + row, y[i]);
-        continue;
+          if (i < mine) __stcg(to + i * kRows, y[i]);
+        __threadfence();
+        sync_sum_warps();
+        if (threadIdx.x == 0) *s_last = ok && atomicAdd(joined, 1) == 1;
+        sync_sum_warps();
+        if (*s_last == 0) continue;
+        __threadfence();
+        load_other();
       }
-      float* to = part_of(g, begins) + (int64_t)first * kRows + row;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i < mine) __stcg(to + i * kRows, y[i]);
-      __threadfence();
-      sync_sum_warps();
-      if (threadIdx.x == 0) *s_last = ok && atomicAdd(&p.joined[g0], 1) == (int)(g1 - g0);
-      sync_sum_warps();
-      if (*s_last == 0) continue;
-      __threadfence();
-      // (four rows of up to four tokens to a thread, all loads of a part in flight at once:
-      // one value after another cost 10 us for 32 tokens in three parts)
-      constexpr int kQuads = kTileTokens * kRows / 4 / (32 * kSumWarps);
-      float4 sum[kQuads] = {};
-#pragma unroll 2
-      for (int64_t c = g0; c <= g1; ++c) {
-        const float4* from = reinterpret_cast<const float4*>(part_of(c, c == g0)) + threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          if ((int)threadIdx.x + i * 32 * kSumWarps >= nt * kRows / 4) break;
-          const float4 v = __ldcg(from + i * 32 * kSumWarps);
-          sum[i].x += v.x, sum[i].y += v.y, sum[i].z += v.z, sum[i].w += v.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const int at = ((int)threadIdx.x + i * 32 * kSumWarps) * 4;
-        if (at >= nt * kRows) break;
-        const int64_t t = t0 + at / kRows, r = out_row + at % kRows;
-        put_out(p, t, r, sum[i].x), put_out(p, t, r + 1, sum[i].y), put_out(p, t, r + 2, sum[i].z), put_out(p, t, r + 3, sum[i].w);
-      }
+        if (i < mine) put_out(p, t0 + first + i, out_row + row, shared ? y[i] + other[i] : y[i]);
     }
   }
   __syncthreads();
@@ -1171,8 +1146,7 @@ static int launch_stream(linear::Params p, cudaStream_t stream) {
   p.tmem_cols = 512;
   p.stages = stages_for(kE4M3, p.n, p.n <= 128 ? 2 * p.n : p.n, 512, kSmem);
   p.units = tiles * p.chunks;
-  const int64_t ctas = p.units < kStreamCtas ? p.units : kStreamCtas;
-  CSA2_LAUNCH_PDL(stream_kernel<kE4M3>, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, p);
+  CSA2_LAUNCH_PDL(stream_kernel<kE4M3>, dim3(kStreamCtas), dim3(kThreads), (size_t)kSmem, stream, p);
   return CSA2_OK;
 }
 

@@ -93,6 +93,18 @@ def test_against_64_bits(csa2, shape, form):
     check(x, data, scale, form, out, out32, 0.37)
 
 
+# more tiles than one wave holds: equal runs over their chunks, tiles in one part and in two (and past it: (16, 512, 38900)
+# is the last that is one wave, as (17, 800, 19400) is of tiles of more tokens)
+RUNS = [(17, 512, 20000), (32, 1056, 19500), (5, 96, 40000), (16, 2080, 39001), (50, 800, 10000), (64, 4128, 10100),
+        (33, 32, 10000), (3000, 32, 1000), (16, 512, 38900), (17, 800, 19400), (6, 288, 25000), (12, 4096, 2048), (40, 2080, 4000)]
+
+
+@pytest.mark.parametrize("form", PER)
+@pytest.mark.parametrize("shape", RUNS)
+def test_many_tiles_against_64_bits(csa2, shape, form):
+    test_against_64_bits(csa2, shape, form)
+
+
 @pytest.mark.parametrize("form", PER)
 @pytest.mark.parametrize("shape", [(1, 64, 128), (3, 96, 70), (8, 1024, 256), (20, 4096, 200), (70, 352, 129)])
 def test_whole_numbers_are_exact(csa2, shape, form):

@@ -67,6 +67,17 @@ CASES = [(1, 8192, 600), (3, 2048, 5000), (8, 4096, 900), (12, 4096, 6000), (30,
 @pytest.mark.parametrize("case", CASES)
 @pytest.mark.parametrize("form", ["e8m0", "e4m3"])
 def test_products_whose_waits_run_out(csa2, hasty, case, form):
+    run_out(csa2, hasty, case, form)
+
+
+# runs over more tiles than one wave holds, two CTAs to an SM by themselves
+@pytest.mark.parametrize("case", [(9, 512, 40000), (32, 1056, 20000), (50, 2816, 10000), (12, 800, 25000)])
+@pytest.mark.parametrize("form", ["e8m0", "e4m3"])
+def test_products_of_many_tiles_whose_waits_run_out(csa2, hasty, case, form):
+    run_out(csa2, hasty, case, form)
+
+
+def run_out(csa2, hasty, case, form):
     T, n_in, n_out = case
     g = torch.Generator(device="cuda").manual_seed(T)
     data = torch.randint(0, 256, (n_out, n_in // 2), generator=g, device="cuda", dtype=torch.uint8)
