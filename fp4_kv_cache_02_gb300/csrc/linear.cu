@@ -42,7 +42,7 @@ constexpr int kSumWarps = 8;                // warps that make terms and sum col
 constexpr int kProducerWarp = kSumWarps;
 constexpr int kMmaWarp = kSumWarps + 1;
 constexpr int kThreads = 32 * (kSumWarps + 2);
-constexpr int term_threads(bool e4m3) { return e4m3 ? 512 : 256; }  // of terms_kernel, eight channels each
+constexpr int kTermThreads = 256;           // of terms_kernel, eight channels each
 constexpr int kMinExp = -100;               // of a block's largest: all the terms' scales are E8M0 then
 
 // Groups of scales in a block of 256 inputs: a group is what one tcgen05.cp moves,
@@ -201,32 +201,33 @@ struct TermArgs {
 };
 
 // The terms of all tokens, ahead of the product: eight channels of a token to a thread.
-// With E4M3 scales every CTA of a token looks at its whole row for its base.
+// With E4M3 scales every CTA of a token looks at its whole row for its base. (With half as
+// many CTAs of twice the threads 8 tokens by 4,096 x 4,096, E4M3, took 7.2 us, so 6.9; with
+// twice as many of 128 6.8, but by 4,096 x 32,768 21.1 and 19.5.)
 template <bool kE4M3>
-__global__ void __launch_bounds__(term_threads(kE4M3)) terms_kernel(TermArgs a) {
+__global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
   pdl_begin();
-  constexpr int kThreads = term_threads(kE4M3);
-  static_assert(kThreads >= kStreamCtas, "a count to a thread");
+  static_assert(kTermThreads >= kStreamCtas, "a count to a thread");
   if (blockIdx.x == 0 && threadIdx.x < kStreamCtas) a.joined[threadIdx.x] = 0;
   const int32_t t = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
   const uint16_t* row = a.x + (int64_t)t * a.n_in;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t k = ((int64_t)slice * kThreads + threadIdx.x) * 8;
+  const int64_t k = ((int64_t)slice * kTermThreads + threadIdx.x) * 8;
   const uint4 v = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0, 0, 0, 0);
   int base = kE8M0Base;
   if constexpr (kE4M3) {
-    __shared__ uint32_t s_max[kThreads / 32];
+    __shared__ uint32_t s_max[kTermThreads / 32];
     uint32_t top = top_bits(v);
     if (a.slices > 1)
 #pragma unroll 4
-      for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kThreads * 8)
+      for (int64_t i = (int64_t)threadIdx.x * 8; i < a.n_in; i += kTermThreads * 8)
         top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) s_max[warp] = top;
     __syncthreads();
     top = s_max[0];
 #pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) top = max(top, s_max[i]);
+    for (int i = 1; i < kTermThreads / 32; ++i) top = max(top, s_max[i]);
     if (threadIdx.x == 0 && slice == 0) a.factor[t] = factor_of(top);
     base = base_exp(top);
   }
@@ -1062,10 +1063,7 @@ static int64_t token_tiles_of(int32_t n_tokens) {
 }
 
 // CTAs to a token's terms.
-static int64_t slices_of(int32_t n_in, bool e4m3) {
-  const int per = linear::term_threads(e4m3) * 8;
-  return ((int64_t)n_in + per - 1) / per;
-}
+static int64_t slices_of(int32_t n_in) { return ((int64_t)n_in + linear::kTermThreads * 8 - 1) / (linear::kTermThreads * 8); }
 
 // Workspace of a product of more than kFewTokens: the tokens' factors, the counts and
 // parts of the tiles that CTAs share, the terms.
@@ -1198,10 +1196,10 @@ static int launch_wide(linear::Params p, cudaStream_t stream) {
 template <bool kE4M3>
 static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stream) {
   using namespace linear;
-  // Up to three tokens, and row tiles for one wave: in one launch (E8M0, a token by 4,096 x
-  // 32,768: 13.8 us, 14.5 with the terms ahead; three 13.9 and 14.5; four 15.3 and 14.5; a
+  // Up to three tokens, and row tiles for one wave: in one launch (E8M0, a token by 32,768
+  // x 4,096: 13.8 us, 14.5 with the terms ahead; three 13.9 and 14.5; four 15.3 and 14.5; a
   // token by 131,072 x 4,096: 47.2 and 46.6). With E4M3 scales, whose base is a second look
-  // at x, one or two (two by 4,096 x 16,384: 10.5 and 11.2; by 16,384 x 16,384 29.9 and 28.0).
+  // at x, one or two (two by 16,384 x 4,096: 10.5 and 11.2; by 16,384 x 16,384 29.9 and 28.0).
   if (p.T <= (kE4M3 ? (p.n_in <= 4096 ? 2 : 1) : kFewTokens) && row_tiles_of(p.n_out) <= 2 * kStreamCtas)
     return launch_split<kE4M3, true, 2>(p, stream);
   if (is_wide(p.T, p.n_in)) return launch_wide<kE4M3>(p, stream);
@@ -1210,15 +1208,15 @@ static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stre
   p.joined = (int32_t*)(workspace + space.joined);
   p.parts = (float*)(workspace + space.parts);
   p.terms = workspace + space.terms;
-  const int64_t slices = slices_of(p.n_in, kE4M3);
+  const int64_t slices = slices_of(p.n_in);
   TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
-  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(term_threads(kE4M3)), (size_t)0, stream, ta);
+  CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
   // Tiles for one wave (of up to 16 tokens two CTAs to an SM): clusters, or CTAs by
-  // themselves. More: in equal runs, whose joins take 3 us (E8M0, 5 tokens by 4,096 x 16,384,
+  // themselves. More: in equal runs, whose joins take 3 us (E8M0, 5 tokens by 16,384 x 4,096,
   // 128 tiles: 10.5 us, 13.6 in runs; by 32,768 x 4,096: 14.4 and 17.1; 32 tokens, 256 tiles:
-  // 26.8 and 21.8 (E4M3); 16 tokens by 4,096 x 128,259: 51.7 and 48.0).
+  // 26.8 and 21.3 (E4M3); 16 tokens by 128,259 x 4,096: 51.7 and 48.0).
   // Two CTAs to an SM, each with half of the stages, where a tile gets more of them so (5
-  // tokens by 16,384 x 4,864: 12.2 us, 15.6 with one; but 8 by 32,768 x 4,096, four to a tile
+  // tokens by 4,864 x 16,384: 12.2 us, 15.6 with one; but 8 by 4,096 x 32,768, four to a tile
   // either way, 18.8 and 17.6).
   const int64_t tiles = row_tiles_of(p.n_out) * p.token_tiles;
   if (tiles > (p.n <= 128 ? 2 : 1) * kStreamCtas) return launch_stream<kE4M3>(p, stream);
@@ -1239,7 +1237,7 @@ extern "C" int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens, const uint8
     return CSA2_ERR_ALIGNMENT;
   // a grid of at most 2^31 - 1 blocks for each kernel
   if (row_tiles_of(n_out) * token_tiles_of(n_tokens) > 0x0FFFFFFFLL ||
-      (int64_t)n_tokens * slices_of(n_in, format == CSA2_FP4_E4M3) > 0x7FFFFFFFLL)
+      (int64_t)n_tokens * slices_of(n_in) > 0x7FFFFFFFLL)
     return CSA2_ERR_UNSUPPORTED_SHAPE;
   const size_t need = csa2_fp4_linear_workspace_size(n_tokens, n_in, format);
   if (!workspace || workspace_bytes < need || !csa2_aligned(workspace, 256)) return CSA2_ERR_WORKSPACE;
