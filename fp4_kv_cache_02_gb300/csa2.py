@@ -488,6 +488,7 @@ def csa2_sparse_attn_prefill_replay(q, kv_data, kv_scale, idx, swa, n_swa, repla
 
 # (A decode step makes several of these calls; their checks are written to cost
 # little, and say what is wrong only when something is.)
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 def _refuse(t, dtype, name, dev):
     _req(t, dtype, name)
@@ -537,6 +538,14 @@ def _shaped(t, dtype, shape, name, dev):
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     return t.data_ptr()
+
+
+def _plain(tensors, dtype, dev):
+    """Whether all are contiguous, of this type and on the call's device."""
+    for t in tensors:
+        if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
 
 
 def _optional(t, dtype, shape, name, dev):
@@ -738,13 +747,18 @@ def csa2_beam_select(logits, scores, out_scores, out_parents, out_tokens, worksp
     if len(out_shape) != 2 or out_shape[0] != B:
         raise ValueError("out_scores must be [B, k]")
     k = out_shape[1]
-    _call("csa2_beam_select", logits.data_ptr(), 1 if f32 else 0, B, W, V, ld,
-          _optional(scores, torch.float32, (B, W), "scores", dev), k,
-          _take(out_scores, torch.float32, "out_scores", dev),
-          _shaped(out_parents, torch.int32, out_shape, "out_parents", dev),
-          _shaped(out_tokens, torch.int32, out_shape, "out_tokens", dev),
-          _optional(lse, torch.float32, (B, W), "lse", dev),
-          _take(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream_on(stream, dev))
+    if not (_plain((out_scores,), _F32, dev) and _plain((out_parents, out_tokens), _I32, dev)
+            and out_parents.shape == out_shape == out_tokens.shape):
+        _take(out_scores, _F32, "out_scores", dev)
+        _shaped(out_parents, _I32, out_shape, "out_parents", dev)
+        _shaped(out_tokens, _I32, out_shape, "out_tokens", dev)
+    scores_at = None if scores is None else _shaped(scores, _F32, (B, W), "scores", dev)
+    lse_at = None if lse is None else _shaped(lse, _F32, (B, W), "lse", dev)
+    rc = _lib.csa2_beam_select(logits.data_ptr(), 1 if f32 else 0, B, W, V, ld, scores_at, k, out_scores.data_ptr(),
+                               out_parents.data_ptr(), out_tokens.data_ptr(), lse_at,
+                               _take(workspace, _U8, "workspace", dev), workspace.numel(), _stream_on(stream, dev))
+    if rc != 0:
+        raise Csa2Error("csa2_beam_select", rc)
 
 
 def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_out, n_visible_out, kv_data=None,
@@ -770,23 +784,30 @@ def csa2_paged_reorder(parents, fresh_pages, page_table, n_visible, page_table_o
         raise ValueError("planes must be [n_pages, page_size, width] or [layers, n_pages, page_size, width]")
     kv_at = kvs_at = ik_at = iks_at = None
     if kv_data is not None:
-        kv_at = _shaped(kv_data, torch.uint8, (*pool, 256), "kv_data", dev)
-        kvs_at = _shaped(kv_scale, torch.uint8, (*pool, 32), "kv_scale", dev)
+        if not _plain((kv_data, kv_scale), _U8, dev) or kv_data.shape != (*pool, 256) or kv_scale.shape != (*pool, 32):
+            _shaped(kv_data, _U8, (*pool, 256), "kv_data", dev)
+            _shaped(kv_scale, _U8, (*pool, 32), "kv_scale", dev)
+        kv_at, kvs_at = kv_data.data_ptr(), kv_scale.data_ptr()
     if ik_data is not None:
-        ik_at = _shaped(ik_data, torch.uint8, (*pool, 64), "ik_data", dev)
-        iks_at = _shaped(ik_scale, torch.uint8, (*pool, 4), "ik_scale", dev)
-    int32 = torch.int32
-    table = _take(page_table, int32, "page_table", dev)
+        if not _plain((ik_data, ik_scale), _U8, dev) or ik_data.shape != (*pool, 64) or ik_scale.shape != (*pool, 4):
+            _shaped(ik_data, _U8, (*pool, 64), "ik_data", dev)
+            _shaped(ik_scale, _U8, (*pool, 4), "ik_scale", dev)
+        ik_at, iks_at = ik_data.data_ptr(), ik_scale.data_ptr()
+    if not _plain((parents, fresh_pages, page_table, n_visible, page_table_out, n_visible_out), _I32, dev):
+        for t, name in ((parents, "parents"), (fresh_pages, "fresh_pages"), (page_table, "page_table"),
+                        (n_visible, "n_visible"), (page_table_out, "page_table_out"), (n_visible_out, "n_visible_out")):
+            _take(t, _I32, name, dev)
     shape = page_table.shape
     if len(shape) != 2:
         raise ValueError("page_table must be [rows, max_pages]")
     (R,), (rows, max_pages) = each, shape
+    if (fresh_pages.shape != each or n_visible_out.shape != each or n_visible.shape != (rows,)
+            or page_table_out.shape != (R, max_pages)):
+        raise ValueError("fresh_pages and n_visible_out must be [R], n_visible [rows], page_table_out [R, max_pages]")
     rc = _lib.csa2_paged_reorder(
-        _take(parents, int32, "parents", dev), _shaped(fresh_pages, int32, each, "fresh_pages", dev), R, kv_at, kvs_at,
-        ik_at, iks_at, layers, n_pages, page, table, rows, max_pages,
-        _shaped(n_visible, int32, (rows,), "n_visible", dev),
-        _shaped(page_table_out, int32, (R, max_pages), "page_table_out", dev),
-        _shaped(n_visible_out, int32, each, "n_visible_out", dev), _stream_on(stream, dev))
+        parents.data_ptr(), fresh_pages.data_ptr(), R, kv_at, kvs_at, ik_at, iks_at, layers, n_pages, page,
+        page_table.data_ptr(), rows, max_pages, n_visible.data_ptr(), page_table_out.data_ptr(),
+        n_visible_out.data_ptr(), _stream_on(stream, dev))
     if rc != 0:
         raise Csa2Error("csa2_paged_reorder", rc)
 
@@ -797,11 +818,12 @@ def csa2_reorder_rows(src, parents, dst, stream=None):
     dev = _device(src, "src")
     dtype, shape = src.dtype, src.shape
     dst_at, to = _take(dst, dtype, "dst", dev), dst.shape
-    if len(shape) < 1 or len(to) < 1 or shape[1:] != to[1:]:
+    if len(shape) < 1 or len(to) < 1 or (shape != to and shape[1:] != to[1:]):
         raise ValueError("src must be [rows, ...] and dst [R, ...] with rows alike")
-    size, R = dtype.itemsize * math.prod(shape[1:]), to[0]
-    rc = _lib.csa2_reorder_rows(src.data_ptr(), shape[0], size, _shaped(parents, torch.int32, (R,), "parents", dev), R,
-                                dst_at, _stream_on(stream, dev))
+    rows, R = shape[0], to[0]
+    size = dtype.itemsize * (src.numel() // rows if rows else math.prod(shape[1:]))
+    rc = _lib.csa2_reorder_rows(src.data_ptr(), rows, size, _shaped(parents, _I32, (R,), "parents", dev), R, dst_at,
+                                _stream_on(stream, dev))
     if rc != 0:
         raise Csa2Error("csa2_reorder_rows", rc)
 
