@@ -144,6 +144,18 @@ def test_select(csa2, size, kind, dtype):
     assert csa2.csa2_get_last_error() == 0
 
 
+# rows in many parts, whose lists are merged in registers: two, four and sixteen to one, of up to 64 keys
+PARTS = [(1, 16, 50261, 32), (4, 16, 8193, 64), (1, 3, 70001, 33), (1, 1, 600011, 17), (1, 7, 90001, 5), (2, 1, 500009, 64),
+         (1, 2, 300007, 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["normal", "few", "rising", "masked", "lowest", "tiny"])
+@pytest.mark.parametrize("size", PARTS)
+def test_select_from_many_parts(csa2, size, kind, dtype):
+    test_select(csa2, size, kind, dtype)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("V", [1, 5, 8, 255, 2048, 4097, 30011])
 def test_rows_at_every_alignment(csa2, V, dtype):

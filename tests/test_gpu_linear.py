@@ -323,6 +323,38 @@ def test_calls_behind_one_another_share_a_workspace(csa2):
     assert csa2.csa2_get_last_error() == 0
 
 
+def test_products_on_several_streams_at_once(csa2):
+    """Clusters, single CTAs, runs and values of the weights beside one another, each stream with its own workspace."""
+    g = gen(16)
+    cases = []
+    for form, (T, n_in, n_out) in itertools.product(PER, [(1, 8192, 1500), (6, 8192, 1900), (12, 1024, 21000), (30, 1024, 20000),
+                                                          (90, 4096, 1100)]):
+        x = torch.randn(T, n_in, generator=g, device="cuda").bfloat16()
+        data, scale = packed(g, n_out, n_in, form)
+        w = csa2.fp4_weights(data, scale, form)
+        want = torch.empty(T, n_out, device="cuda")
+        csa2.csa2_fp4_linear(x, w, None, csa2.fp4_linear_workspace(T, n_in, form), form, out_f32=want)
+        cases.append((x, w, form, want))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    runs = []
+    for k, s in enumerate(streams):
+        ws = [csa2.fp4_linear_workspace(x.shape[0], x.shape[1], form) for x, _, form, _ in cases]
+        runs.append((s, cases[k * 3:] + cases[:k * 3], max(ws, key=lambda t: t.numel()), [[] for _ in cases]))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, mine, ws, outs in runs:
+            with torch.cuda.stream(s):
+                for (x, w, form, want), out in zip(mine, outs):
+                    out.append(torch.empty_like(want))
+                    csa2.csa2_fp4_linear(x, w, None, ws, form, out_f32=out[-1])
+    torch.cuda.synchronize()
+    for s, mine, ws, outs in runs:
+        for (x, w, form, want), out in zip(mine, outs):
+            assert all(torch.equal(o, want) for o in out)
+    assert csa2.csa2_get_last_error() == 0
+
+
 def test_a_chain_feeds_each_product_from_the_last(csa2):
     """Outputs read by the next call at once: what a kernel of this library may start early, it does not read early."""
     g = gen(15)
