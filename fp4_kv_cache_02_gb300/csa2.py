@@ -691,10 +691,11 @@ def csa2_fp4_weights(data, scale, weights, format, stream=None):
         raise ValueError("data must be [n_out, n_in / 2]")
     n_out, n_in = data.shape[0], 2 * data.shape[1]
     scale_at = _shaped(scale, torch.uint8, (n_out, n_in // (16 if format == "e4m3" else 32)), "scale", dev)
+    weights_at = _take(weights, torch.uint8, "weights", dev)
     if weights.numel() < csa2_fp4_weights_size(n_out, n_in, format):
         raise ValueError("weights needs csa2_fp4_weights_size(n_out, n_in, format) bytes")
-    _call("csa2_fp4_weights", _take(data, torch.uint8, "data", dev), scale_at, n_out, n_in, _format(format),
-          _take(weights, torch.uint8, "weights", dev), _s(stream))
+    _call("csa2_fp4_weights", _take(data, torch.uint8, "data", dev), scale_at, n_out, n_in, _format(format), weights_at,
+          _s(stream))
 
 
 def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None, stream=None):
@@ -712,14 +713,16 @@ def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None,
         raise ValueError("x must be [n_tokens, n_in], out or out_f32 [n_tokens, n_out]")
     (n, n_in), n_out = x_shape, shape[1]
     kind = _format(format)
-    w_at = _take(weights, torch.uint8, "weights", dev)
+    if not _plain((weights, workspace), _U8, dev):
+        _take(weights, _U8, "weights", dev)
+        _take(workspace, _U8, "workspace", dev)
     # (csa2_fp4_weights_size without a call: blocks of 128 x 256 weights)
     if weights.numel() < (n_out + 127) // 128 * ((n_in + 255) // 256) * (18432 if kind else 17408):
         raise ValueError(f"weights holds fewer than {n_out} x {n_in} weights")
     out_at = None if out is None else _take(out, torch.bfloat16, "out", dev)  # (its shape is the one compared with)
     out32_at = None if out_f32 is None else _shaped(out_f32, torch.float32, shape, "out_f32", dev)
-    rc = _lib.csa2_fp4_linear(x.data_ptr(), n, w_at, n_out, n_in, kind, scale, out_at, out32_at,
-                              _take(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream_on(stream, dev))
+    rc = _lib.csa2_fp4_linear(x.data_ptr(), n, weights.data_ptr(), n_out, n_in, kind, scale, out_at, out32_at,
+                              workspace.data_ptr(), workspace.numel(), _stream_on(stream, dev))
     if rc != 0:
         raise Csa2Error("csa2_fp4_linear", rc)
 
@@ -732,6 +735,8 @@ def csa2_beam_select(logits, scores, out_scores, out_parents, out_tokens, worksp
     out_scores fp32, out_parents (rows b * W + w) and out_tokens int32 [B, k]; lse
     [B, W] fp32 is optional."""
     dev = _device(out_scores, "out_scores")
+    if logits is None:
+        raise ValueError("logits is required")
     f32 = logits.dtype is torch.float32
     shape, out_shape = logits.shape, out_scores.shape
     if len(shape) != 3 or not (f32 or logits.dtype is torch.bfloat16) or logits.get_device() != dev:

@@ -381,6 +381,24 @@ def test_reorder_rows(csa2, shape, dtype):
     assert (dst[2] == 101).all() and (dst[4] == 101).all() and torch.equal(dst[7], src[1])
 
 
+def test_arguments_that_are_missing(csa2):
+    f = lambda *n: torch.empty(*n, device="cuda")
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")
+    calls = [(csa2.csa2_beam_select, dict(logits=f(2, 3, 40), out_scores=f(2, 4), out_parents=i(2, 4), out_tokens=i(2, 4),
+                                          workspace=csa2.beam_select_workspace(2, 3, 40, 4)), dict(scores=f(2, 3))),
+             (csa2.csa2_paged_reorder, dict(parents=i(2), fresh_pages=i(2), page_table=i(3, 2), n_visible=i(3),
+                                            page_table_out=i(2, 2), n_visible_out=i(2),
+                                            kv_data=torch.zeros(4, 16, 256, dtype=torch.uint8, device="cuda"),
+                                            kv_scale=torch.zeros(4, 16, 32, dtype=torch.uint8, device="cuda")), {}),
+             (csa2.csa2_reorder_rows, dict(src=f(2, 4), dst=f(3, 4), parents=i(3)), {})]
+    for call_of, good, more in calls:
+        call_of(**good, **more)
+        for name in good:
+            with pytest.raises(ValueError):
+                call_of(**{**good, **more, name: None})
+    csa2.csa2_get_last_error()
+
+
 def test_refusals_of_the_binding(csa2):
     x = torch.zeros(2, 3, 40, device="cuda")
     s = torch.zeros(2, 3, device="cuda")

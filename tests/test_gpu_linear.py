@@ -374,6 +374,23 @@ def test_a_chain_feeds_each_product_from_the_last(csa2):
         assert torch.equal(b, again)
 
 
+def test_arguments_that_are_missing(csa2):
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    data = torch.zeros(8, 32, dtype=torch.uint8, device="cuda")
+    scale = torch.zeros(8, 2, dtype=torch.uint8, device="cuda")
+    good = dict(x=x, weights=csa2.fp4_weights(data, scale, "e8m0"), out=torch.empty(2, 8, dtype=torch.bfloat16, device="cuda"),
+                workspace=csa2.fp4_linear_workspace(2, 64, "e8m0"), format="e8m0")
+    csa2.csa2_fp4_linear(**good)
+    for name in good:
+        with pytest.raises(ValueError):
+            csa2.csa2_fp4_linear(**{**good, name: None})
+    good = dict(data=data, scale=scale, weights=good["weights"], format="e8m0")
+    csa2.csa2_fp4_weights(**good)
+    for name in good:
+        with pytest.raises(ValueError):
+            csa2.csa2_fp4_weights(**{**good, name: None})
+
+
 def test_refusals_of_the_binding(csa2):
     x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
     data = torch.zeros(8, 32, dtype=torch.uint8, device="cuda")
