@@ -766,8 +766,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
 // More than 64 tokens: the weights' values are exact in bf16 (two bits, or with an E4M3
 // scale six), so they are made on the way and multiplied by x as it is, 128 outputs x up
 // to 256 tokens a CTA. A token's eight columns take 1/32 of an FP4 block's time of 880
-// cycles (with E4M3 scales), its one bf16 column 1/256 of 2,150, and the values' making
-// 2,000: 96 tokens by 4,096 x 4,096 take 11.8 us, 15.6 as terms, 64 tokens 11.3 and 10.6.
+// cycles (with E4M3 scales); a bf16 block takes 2,150 to 2,300 for 80 to 256 tokens alike (a
+// product with A in tensor memory takes 134 cycles for its 16 inputs however few its columns;
+// neither 30 % fewer instructions in the values' making nor half as many warps again changed
+// that): 96 tokens by 4,096 x 4,096 take 11.9 us, 64 11.3, 10.1 as terms.
 //   warp 16    producer of blocks of weights;
 //   warp 17    products, A from tensor memory: in shared memory the weights' values would
 //              be written and read beside x, more than its 128 bytes a cycle;
