@@ -363,7 +363,9 @@ __device__ __forceinline__ void add_parts(const Params& p, const float* sums, in
 // each CTA makes itself: ahead of the product they would cost a launch and a trip through
 // L2 (4 us of 15 for a token by 32,768 x 4,096 weights).
 //   warp 8     producer: a bulk copy of a block of weights per stage (and one of the
-//              terms), the first weights before the call's inputs are waited for;
+//              terms); behind terms ahead the first weights before those are waited for
+//              (weights that nobody waited for would gain nothing: a token by 4,096 x 640
+//              4.9 us either way, by 4,096 x 32,768 14.0);
 //   warp 9     scales to tensor memory, products;
 //   warps 0-7  kOwnTerms: the terms, a (chunk, token) to a warp; then the columns summed
 //              (a quarter of the rows, half of the tokens each), stored.
@@ -407,6 +409,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) split_kernel(Params p) {
     *s_abort = 0;
     tc::fence_mbar_init();
     tc::fence_proxy_async_smem();
+    // The kernel before may have written the weights. With terms ahead that is their
+    // kernel, which lets this one start once it has waited for all that was before it.
+    if constexpr (kOwnTerms) pdl_wait();
     for (int i = 0; i < ahead; ++i) load_weights(i, i);
   }
   // kOwnTerms: x is looked at before the set-up is through. With E4M3 scales all of this
@@ -615,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
     *s_abort = 0;
     tc::fence_mbar_init();
     tc::fence_proxy_async_smem();
+    // (before the terms are waited for: their kernel has waited for whatever wrote weights)
     Place at = start;
     for (int i = 0; i < ahead; ++i, advance(at)) load_weights(at, i);
   }
@@ -862,6 +868,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     *s_abort = 0;
     tc::fence_mbar_init();
     tc::fence_proxy_async_smem();
+    pdl_wait();  // (the kernel before may have written the weights)
     for (int i = 0; i < min(n_raw, kRawStages); ++i) load_raw(i, i);
   }
   if (warp == 4 * kSets + 1) tc::tmem_alloc(s_tmem, 512);

@@ -786,9 +786,7 @@ size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in,
  *   gives the same bits; a token's result may differ in the last fp32 bits with the number
  *   of tokens.
  *   x, weights 16-byte aligned; the outputs must not overlap anything that is read.
- *   weights are read before this call waits for the kernel just before it on the stream:
- *   they must not be written by a kernel that lets its successor start early
- *   (csa2_fp4_weights does not).
+ *   Whatever came before on the stream may have written x and weights.
  *   workspace: csa2_fp4_linear_workspace_size bytes, 256-byte aligned, contents
  *   need not be kept; calls that may run at the same time need one each.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA.
