@@ -799,14 +799,16 @@ struct WideParams {
   int32_t x_bytes, x_stages;
 };
 
-// Eight E2M1 codes to bf16, times a scale: the bytes of the magnitudes are looked up
-// (0, 1/2 .. 6: high 00 3F 3F 3F 40 40 40 40, low 00 00 80 C0 00 40 80 C0), the signs put
-// to the high ones, and both interleaved.
+// Eight E2M1 codes to bf16, times a scale and 1/4: the bytes of the magnitudes' quarters
+// are looked up (0, 1/8 .. 3/2: high 00 3E 3E 3E 3F 3F 3F 3F, low 00 00 80 C0 00 40 80 C0),
+// the signs put to the high ones, and both interleaved. So 6 x 2^127 has a place in bf16,
+// and 1/2 x 2^-127 too. An E4M3 scale is held four times as large; with E8M0 ones the
+// quarter is put back behind the product.
 __device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, __nv_bfloat162 scale, uint32_t* out) {
   const uint32_t m = w & 0x77777777u;
   const uint32_t even = (w << 4) & 0x80808080u, odd = w & 0x80808080u;
-  const uint32_t h0 = __byte_perm(0x3F3F3F00u, 0x40404040u, m) | __byte_perm(even, odd, 0x5140);
-  const uint32_t h1 = __byte_perm(0x3F3F3F00u, 0x40404040u, m >> 16) | __byte_perm(even, odd, 0x7362);
+  const uint32_t h0 = __byte_perm(0x3E3E3E00u, 0x3F3F3F3Fu, m) | __byte_perm(even, odd, 0x5140);
+  const uint32_t h1 = __byte_perm(0x3E3E3E00u, 0x3F3F3F3Fu, m >> 16) | __byte_perm(even, odd, 0x7362);
   const uint32_t l0 = __byte_perm(0xC0800000u, 0xC0804000u, m), l1 = __byte_perm(0xC0800000u, 0xC0804000u, m >> 16);
   const uint32_t v[4] = {__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
                          __byte_perm(l1, h1, 0x7362)};
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
       if (kE4M3) {
         // an E4M3 byte at a bf16's exponent and first bits is its value times 2^-120
         const uint32_t four = *reinterpret_cast<const uint32_t*>(sf + q * group_bytes());
-        const __nv_bfloat162 up = __float2bfloat162_rn(__uint_as_float((120u + 127u) << 23));
+        const __nv_bfloat162 up = __float2bfloat162_rn(__uint_as_float((120u + 2u + 127u) << 23));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t two = (four >> (16 * i) & 0x7Fu) << 4 | (four >> (16 * i + 8) & 0x7Fu) << 20;
@@ -994,10 +996,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (t + i >= nt) break;
+          const float y = __uint_as_float(v[i]) * (kE4M3 ? 1.0f : 4.0f);
           if (p.split > 1)
-            sums[(t + i) * kRows + row] = __uint_as_float(v[i]);
+            sums[(t + i) * kRows + row] = y;
           else
-            put_out(p, t0 + t + i, row_tile * kRows + row, __uint_as_float(v[i]));
+            put_out(p, t0 + t + i, row_tile * kRows + row, y);
         }
       }
       tc::tc_fence_before();
