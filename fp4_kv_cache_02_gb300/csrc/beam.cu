@@ -714,11 +714,11 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(ReorderArgs a)
     const int64_t width = (int64_t)kPlaneBytes[i] << a.pages.shift;
     const uint8_t* s = a.planes[i] + (layer + src) * width;
     uint8_t* d = a.planes[i] + (layer + dst) * width;
-    const int bytes = fill * kPlaneBytes[i];
-    for (int at = threadIdx.x * 16; at + 16 <= bytes; at += kReorderThreads * 16)
+    const int64_t bytes = (int64_t)fill * kPlaneBytes[i];  // (a page of 2^23 entries holds 2^31 bytes of codes)
+    for (int64_t at = threadIdx.x * 16; at + 16 <= bytes; at += kReorderThreads * 16)
       *reinterpret_cast<uint4*>(d + at) = *reinterpret_cast<const uint4*>(s + at);
-    const int tail = bytes & ~15;
-    const int at = tail + (int)threadIdx.x * 4;
+    const int64_t tail = bytes & ~(int64_t)15;
+    const int64_t at = tail + threadIdx.x * 4;
     if (at < bytes) *reinterpret_cast<uint32_t*>(d + at) = *reinterpret_cast<const uint32_t*>(s + at);
   }
 }
