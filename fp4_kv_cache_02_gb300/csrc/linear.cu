@@ -43,6 +43,8 @@ constexpr int kProducerWarp = kSumWarps;
 constexpr int kMmaWarp = kSumWarps + 1;
 constexpr int kThreads = 32 * (kSumWarps + 2);
 constexpr int kTermThreads = 256;           // of terms_kernel, eight channels each
+constexpr int kFactorThreads = 1024;        // of factors_kernel
+constexpr int kLongSlices = 16;             // CTAs to a token's terms above which it goes ahead of them
 constexpr int kMinExp = -100;               // of a block's largest: all the terms' scales are E8M0 then
 
 // Groups of scales in a block of 256 inputs: a group is what one tcgen05.cp moves,
@@ -195,15 +197,37 @@ __device__ __forceinline__ void put_terms(uint4 v, int base, int tl, uint8_t* da
 struct TermArgs {
   const uint16_t* x;
   int32_t T, n_in, chunks, n, slices;
+  bool known;  // the factors are there
   uint8_t* terms;
   float* factor;
   int32_t* joined;
 };
 
+// E4M3: the factors of tokens of more than 32,768 inputs, a CTA to a token, ahead of their
+// terms, every CTA of which would look at the whole row otherwise: work that grows with the
+// square of the inputs (a product's time, 512 outputs: 64 tokens of 32,768 inputs 20.3 us so,
+// 20.7 otherwise, but 8 of them 13.8 and 12.8; 2 and 64 of 65,536 18.2 and 29.3 so, 19.6 and
+// 39.0 otherwise; 64 of 262,144 93 and 245).
+__global__ void __launch_bounds__(kFactorThreads) factors_kernel(const uint16_t* x, int32_t n_in, float* factor) {
+  pdl_begin();
+  __shared__ uint32_t s_max[kFactorThreads / 32];
+  const uint16_t* row = x + (int64_t)blockIdx.x * n_in;
+  uint32_t top = 0;
+#pragma unroll 8
+  for (int64_t i = (int64_t)threadIdx.x * 8; i < n_in; i += kFactorThreads * 8)
+    top = max(top, top_bits(*reinterpret_cast<const uint4*>(row + i)));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  top = __reduce_max_sync(0xffffffffu, s_max[threadIdx.x]);
+  if (threadIdx.x == 0) factor[blockIdx.x] = factor_of(top);
+}
+
 // The terms of all tokens, ahead of the product: eight channels of a token to a thread.
-// With E4M3 scales every CTA of a token looks at its whole row for its base. (With half as
-// many CTAs of twice the threads 8 tokens by 4,096 x 4,096, E4M3, took 7.2 us, so 6.9; with
-// twice as many of 128 6.8, but by 4,096 x 32,768 21.1 and 19.5.)
+// With E4M3 scales every CTA of a token looks at its whole row for its base, unless that is
+// long. (With half as many CTAs of twice the threads 8 tokens by 4,096 x 4,096, E4M3, took
+// 7.2 us, so 6.9; with twice as many of 128 6.8, but by 4,096 x 32,768 21.1 and 19.5.)
 template <bool kE4M3>
 __global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
   pdl_begin();
@@ -215,7 +239,9 @@ __global__ void __launch_bounds__(kTermThreads) terms_kernel(TermArgs a) {
   const int64_t k = ((int64_t)slice * kTermThreads + threadIdx.x) * 8;
   const uint4 v = k < a.n_in ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0, 0, 0, 0);
   int base = kE8M0Base;
-  if constexpr (kE4M3) {
+  if (kE4M3 && a.known) {
+    base = (int)(__float_as_uint(__ldcg(a.factor + t)) >> 23) - 127;
+  } else if constexpr (kE4M3) {
     __shared__ uint32_t s_max[kTermThreads / 32];
     uint32_t top = top_bits(v);
     if (a.slices > 1)
@@ -1221,7 +1247,10 @@ static int launch_linear(linear::Params p, uint8_t* workspace, cudaStream_t stre
   p.parts = (float*)(workspace + space.parts);
   p.terms = workspace + space.terms;
   const int64_t slices = slices_of(p.n_in);
-  TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, workspace + space.terms, (float*)workspace, p.joined};
+  const bool known = kE4M3 && slices > kLongSlices;
+  if (known)
+    CSA2_LAUNCH_PDL(factors_kernel, dim3((unsigned)p.T), dim3(kFactorThreads), (size_t)0, stream, p.x, p.n_in, (float*)workspace);
+  TermArgs ta{p.x, p.T, p.n_in, p.chunks, p.n, (int32_t)slices, known, workspace + space.terms, (float*)workspace, p.joined};
   CSA2_LAUNCH_PDL(terms_kernel<kE4M3>, dim3((unsigned)(p.T * slices)), dim3(kTermThreads), (size_t)0, stream, ta);
   // Tiles for one wave (of up to 16 tokens two CTAs to an SM): clusters, or CTAs by
   // themselves. More: in equal runs, whose joins take 3 us (E8M0, 5 tokens by 16,384 x 4,096,
