@@ -14,7 +14,6 @@
 // each tile gives a partial softmax, and the CTAs of the cluster merge the
 // partials in fixed order, so results are deterministic.
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include "paged_common.cuh"
 
@@ -52,19 +51,6 @@ struct AttnArgs {
 #include "attention_tc.cuh"
 
 using namespace csa2;
-
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
 
 static constexpr int kQueriesPerLaunch = 256;  // bounds the workspace of one launch
 
@@ -229,7 +215,7 @@ static int launch_attn(AttnArgs a, const void* q_bf16, int32_t n_q, uint16_t* ou
   a.part_o = (float*)ws;
   // Q rows of all queries as a 2-D bf16 tensor [n_q * 64][512], loaded in
   // [64 heads][64 channels] boxes with the 128-byte swizzle the MMA reads.
-  auto encode = tensor_map_encoder();
+  auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   CUtensorMap qmap;
   cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)n_q * kHeads};

@@ -36,19 +36,6 @@ int csa2_read_and_clear_index_error(cudaStream_t s) {
   return v;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 static int device_sm_count() {
   static int sms[64] = {};
   int dev = 0;
@@ -75,7 +62,7 @@ int csa2_launch_index_score_tc(const uint8_t* q_data, const uint8_t* q_e8m0, con
   if (n_pos == 0 || B == 0) return CSA2_OK;
   if (q_bf16 ? !csa2_aligned(q_bf16, 16) : (!csa2_aligned(q_data, 16) || !csa2_aligned(q_e8m0, 4)))
     return CSA2_ERR_ALIGNMENT;
-  auto encode = tensor_map_encoder();
+  auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   CUtensorMap map;
   cuuint64_t dims[3] = {(cuuint64_t)kIkBytes, (cuuint64_t)cap, (cuuint64_t)B};
@@ -127,7 +114,7 @@ extern "C" int csa2_paged_index_score(const uint8_t* q_data, const uint8_t* q_e8
       (tile_counters && !csa2_aligned(tile_counters, 8)))
     return CSA2_ERR_ALIGNMENT;
   if (n_pos == 0 || B == 0) return CSA2_OK;
-  auto encode = tensor_map_encoder();
+  auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   const int64_t pool = n_pages << pages.shift;
   const int run = page_size < scan_tc::kTileRows ? page_size : scan_tc::kTileRows;
@@ -177,7 +164,7 @@ extern "C" int csa2_prefill_index_score_compressed(const uint8_t* q_data, const 
     return CSA2_ERR_ALIGNMENT;
   if ((int64_t)T * kIdxHeads > 0x7FFFFFFFLL || n_entries > 0x7FFFFFFFLL) return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || n_entries == 0) return CSA2_OK;
-  auto encode = tensor_map_encoder();
+  auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   using namespace prefill_tc;
   CUtensorMap map_ik, map_q;

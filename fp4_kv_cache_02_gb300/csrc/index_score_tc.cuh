@@ -23,8 +23,6 @@
 // multiply-adds per key that CUDA cores could not sustain at that rate.
 #pragma once
 
-#include <cudaTypedefs.h>
-
 #include "codec_blocks.cuh"
 #include "paged_common.cuh"
 #include "tc_common.cuh"

@@ -18,7 +18,6 @@
 // of a token are eight columns of the second operand, so the products cost tensor
 // time that a product bound by its weights' bytes has to spare, and no instruction
 // of the CUDA cores per weight.
-#include <cudaTypedefs.h>
 
 #include "tc_common.cuh"
 
@@ -1186,25 +1185,13 @@ static int launch_stream(linear::Params p, cudaStream_t stream) {
   return CSA2_OK;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 template <bool kE4M3>
 static int launch_wide(linear::Params p, cudaStream_t stream) {
   using namespace linear;
   static Csa2PerDeviceOnce once;
   constexpr int kSmem = 227 * 1024, kRoom = kSmem - kHeadBytes - 1024 - kRawStages * block_bytes(kE4M3);
   if (csa2_smem_optin((const void*)wide_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
-  auto encode = tensor_map_encoder();
+  auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   // equal tiles
   p.token_tiles = (p.T + kWideTokens - 1) / kWideTokens;

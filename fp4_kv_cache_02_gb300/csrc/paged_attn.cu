@@ -50,7 +50,6 @@
 // and a second kernel joins them in order.
 // Few long sequences and many short ones load the SMs alike, and the workspace
 // (two parts per SM) does not grow with the batch.
-#include <cudaTypedefs.h>
 
 #include "attn_common.cuh"
 #include "paged_common.cuh"
@@ -1080,19 +1079,6 @@ int csa2_read_and_clear_paged_attn_error(cudaStream_t s) {
   return v;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 static constexpr int kMaxCtas = 1024;  // the joining kernel's tables
 
 static int paged_attn_ctas() {
@@ -1158,7 +1144,7 @@ extern "C" int csa2_paged_attn(const void* q_bf16, int32_t n_tokens, const int32
   a.part_o = (float*)ws;
   a.part_ml = (float2*)(ws + part_o_bytes(G));
   a.lists = (pattn::PartList*)(ws + part_o_bytes(G) + part_ml_bytes(G));
-  auto encode = tensor_map_encoder();
+  auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
   // the pool's codes, in boxes of one group's 64 bytes of a run of rows (an empty
   // pool has nothing to copy: the map then only has to be valid, over any memory)

@@ -5,7 +5,10 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "common.cuh"
 
@@ -371,3 +374,21 @@ __device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t c) {
 
 }  // namespace tc
 }  // namespace csa2
+
+// ---- host side ---------------------------------------------------------------------
+// The driver's encoder of tensor maps, looked up once (nullptr where there is none; the
+// first calls of several host threads may each look it up).
+static inline PFN_cuTensorMapEncodeTiled_v12000 csa2_tensor_map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+      known.store(fn, std::memory_order_release);
+    }
+  }
+  return fn;
+}
