@@ -818,6 +818,13 @@ constexpr int kSlots = 8;            // steps of A in tensor memory, behind 256 
 constexpr int kSets = 4;             // of four warps
 constexpr int kWideThreads = 32 * (4 * kSets + 3);
 
+// Equal tiles of tokens, a multiple of 16 each.
+constexpr int32_t wide_tiles(int64_t T) { return (int32_t)((T + kWideTokens - 1) / kWideTokens); }
+constexpr int32_t wide_tokens(int64_t T) { return (int32_t)((T + wide_tiles(T) - 1) / wide_tiles(T) + 15) / 16 * 16; }
+static_assert(wide_tiles(0x7FFFFFFF) == 1 << 23 && wide_tokens(0x7FFFFFFF) == kWideTokens, "sums past 32 bits");
+static_assert(wide_tiles(65) == 1 && wide_tokens(65) == 80 && wide_tiles(257) == 2 && wide_tokens(257) == 144 &&
+              wide_tiles(4097) == 17 && wide_tokens(4097) == kWideTokens, "equal tiles");
+
 struct WideParams {
   Params p;
   int32_t tokens;  // of a tile, a multiple of 16
@@ -1193,9 +1200,8 @@ static int launch_wide(linear::Params p, cudaStream_t stream) {
   if (csa2_smem_optin((const void*)wide_kernel<kE4M3>, kSmem, once) != CSA2_OK) return CSA2_ERR_CUDA;
   auto encode = csa2_tensor_map_encoder();
   if (!encode) return CSA2_ERR_CUDA;
-  // equal tiles
-  p.token_tiles = (p.T + kWideTokens - 1) / kWideTokens;
-  WideParams wp{p, ((p.T + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16};
+  p.token_tiles = wide_tiles(p.T);
+  WideParams wp{p, wide_tokens(p.T)};
   wp.x_bytes = wp.tokens * kSub * 2;
   wp.x_stages = kRoom / wp.x_bytes < kMaxXStages ? kRoom / wp.x_bytes : kMaxXStages;
   CUtensorMap map;
