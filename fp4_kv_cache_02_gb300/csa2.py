@@ -683,6 +683,15 @@ def csa2_fp4_weights_size(n_out, n_in, format) -> int:
     return int(_lib.csa2_fp4_weights_size(n_out, n_in, _format(format)))
 
 
+# bytes of a block of 128 x 256 weights in each format, as the library has them
+_BLOCK_BYTES = tuple(int(_lib.csa2_fp4_weights_size(1, 32, kind)) for kind in sorted(FP4_FORMATS.values()))
+
+
+def _weights_bytes(n_out, n_in, kind):
+    """csa2_fp4_weights_size for a product's check of each call, without the call's 0.7 us."""
+    return (n_out + 127) // 128 * ((n_in + 255) // 256) * _BLOCK_BYTES[kind]
+
+
 def csa2_fp4_weights(data, scale, weights, format, stream=None):
     """data [n_out, n_in / 2] u8 and scale [n_out, n_in / 32 (e8m0) or / 16 (e4m3)]
     u8, as the encoders pack them -> weights (u8, csa2_fp4_weights_size bytes)."""
@@ -716,8 +725,7 @@ def csa2_fp4_linear(x, weights, out, workspace, format, scale=1.0, out_f32=None,
     if not _plain((weights, workspace), _U8, dev):
         _take(weights, _U8, "weights", dev)
         _take(workspace, _U8, "workspace", dev)
-    # (csa2_fp4_weights_size without a call: blocks of 128 x 256 weights)
-    if weights.numel() < (n_out + 127) // 128 * ((n_in + 255) // 256) * (18432 if kind else 17408):
+    if weights.numel() < _weights_bytes(n_out, n_in, kind):
         raise ValueError(f"weights holds fewer than {n_out} x {n_in} weights")
     out_at = None if out is None else _take(out, torch.bfloat16, "out", dev)  # (its shape is the one compared with)
     out32_at = None if out_f32 is None else _shaped(out_f32, torch.float32, shape, "out_f32", dev)
