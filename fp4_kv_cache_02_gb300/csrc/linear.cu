@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(Params p) {
         if (complete) load_other();
       }
       // (after a wait that ran out the warps still meet at the same barriers: the waits of
-      // an aborted run end at once, and nothing is read or stored)
+      // an aborted run end at once. A tile whose products were cut short is stored as it is.)
       const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&acc_full[a], acc_turn & 1u, s_abort, &g_linear_error));
       float y[16];
       if (ok) {

@@ -789,7 +789,9 @@ size_t csa2_fp4_linear_workspace_size(int32_t n_tokens, int32_t n_in,
  *   Whatever came before on the stream may have written x and weights.
  *   workspace: csa2_fp4_linear_workspace_size bytes, 256-byte aligned, contents
  *   need not be kept; calls that may run at the same time need one each.
- * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, CUDA; a bounded device
+ * wait that runs out is reported by csa2_get_last_error as TIMEOUT (the outputs then hold
+ * anything).
  */
 int csa2_fp4_linear(const void* x_bf16, int32_t n_tokens,
                     const uint8_t* weights, int32_t n_out, int32_t n_in,
@@ -823,10 +825,11 @@ size_t csa2_beam_select_workspace_size(int32_t B, int32_t W, int32_t V,
  *   row b * W + w (what csa2_paged_reorder takes); out_tokens [B][k] int32. Behind the
  *   last candidate: -inf, -1, -1. lse (nullable) [B][W] fp32: the rows' log sums (NaN
  *   for one that holds a NaN or +inf).
- *   Sums are held in fp32, scores in 64 bits until they are written: candidates of one
- *   row are in exact order, those of different rows in that of their scores with log
- *   sums good to about 2^-20. (Rows that are alike tie exactly where they lie alike in
- *   memory: ld * the type's size a multiple of 16.) The result is deterministic.
+ *   Sums are held in fp32, scores as sums of two fp32 values (48 bits) until they are
+ *   written: candidates of one row are in exact order, those of different rows in that of
+ *   their scores with log sums good to (V / 1024 + 160) 2^-23, 3.4e-5 for V = 128,000. (Rows
+ *   that are alike tie exactly where they lie alike in memory: ld * the type's size a
+ *   multiple of 16.) The result is deterministic.
  *   1 <= k <= CSA2_MAX_BEAM_K, 1 <= W <= CSA2_MAX_BEAMS, B * W < 2^23.
  *   workspace: csa2_beam_select_workspace_size bytes, 256-byte aligned; calls that may
  *   run at the same time need one each.
